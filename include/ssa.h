@@ -18,8 +18,10 @@
  * ssa_backward (step 7);
  * ssa_geo_select (geometric block routing) and ssa_params.selection (a given
  * selection); ssa_cross_forward / ssa_cross_backward (queries of another token
- * set); ssa_params.conv (learned compression); ssa_bin_noalloc; workspace sizes,
- * status, version and per-kernel timing.
+ * set); ssa_params.conv (learned compression); ssa_window_plan, ssa_window_forward /
+ * _backward and ssa_diff_forward / _backward (attention inside the cells with a learned
+ * relative position bias, and differential attention); ssa_act8_pack / _unpack (8-bit
+ * checkpoints); ssa_bin_noalloc; workspace sizes, status, version and per-kernel timing.
  *
  * Conventions for every entry point:
  *   - All array arguments are DEVICE pointers unless stated; the caller owns
@@ -77,7 +79,9 @@ enum {
   SSA_OP_CROSS_FORWARD = 4,
   SSA_OP_CROSS_BACKWARD = 5,
   SSA_OP_SP_FORWARD = 6,
-  SSA_OP_SP_BACKWARD = 7
+  SSA_OP_SP_BACKWARD = 7,
+  SSA_OP_WINDOW_BACKWARD = 8, /* ssa_window_workspace_size */
+  SSA_OP_DIFF_BACKWARD = 9    /* ssa_window_workspace_size */
 };
 
 /* Shape and method parameters shared by forward and backward. */
@@ -361,6 +365,139 @@ SSA_API ssa_status ssa_sp_backward(const ssa_params* p, int32_t S, int64_t N, co
                                    const ssa_sp_local* loc, const void* q, const void* k, const void* v,
                                    const float* gates, const ssa_saved* saved, const void* dout, float* dq,
                                    float* dk, float* dv, float* dgates, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Attention inside the cells of a partition, with what trains it: a learned relative
+ * position bias, differential attention, and 8-bit checkpoints of Q, K, V.  These calls
+ * stand beside the window branch of ssa_forward (Direct3D-S2 "方法": the sparse 3D window;
+ * the bias, the difference of maps and the checkpoints have no counterpart on the pages):
+ * every token attends the tokens of its own cell (window or block) of any partition that
+ * ssa_bin made.  All of them are asynchronous, allocate nothing, find argument errors on
+ * the host before anything is enqueued, and give the same bits on every run.
+ */
+
+/* The largest window edge a relative position bias can have ((2*16-1)^3 offsets). */
+#define SSA_WINDOW_MAX_EDGE 16
+/* Rows of the plan's tiles: tiles holds n / SSA_WINDOW_TILE + count entries. */
+#define SSA_WINDOW_TILE 16
+
+/*
+ * Work plan of one partition, made once per voxel set by ssa_window_plan and read by every
+ * layer and both passes.  Caller-allocated device arrays:
+ */
+typedef struct ssa_win_plan {
+  int32_t* rows;   /* [n, 2] in cell order: the token and its offset code */
+  int32_t* tiles;  /* [n / SSA_WINDOW_TILE + count, 4]: up to 16 rows of one cell: first row, rows
+                      (+ 65536 where the cell holds two tokens in one voxel), the cell's first and
+                      end row; unused entries hold zeros */
+  int64_t n;       /* out: tokens */
+  int64_t count;   /* out: cells of the partition */
+  int32_t m;       /* out: window edge of the codes, 0 without coordinates */
+} ssa_win_plan;
+
+/*
+ * ssa_window_plan -- fills `plan` for a partition of N tokens.
+ *   coords  int32 [N, 3], the coordinates that were binned, or NULL: a plan without offset
+ *           codes, for calls without a bias (then m is ignored)
+ *   m       window edge, 1..SSA_WINDOW_MAX_EDGE (SSA_ERR_UNSUPPORTED above); the code of a
+ *           token is that of its coordinate modulo m
+ *   win     partition from ssa_bin over the same tokens; a partition whose arrays do not fit
+ *           together is found on the device (ssa_get_device_status: SSA_ERR_INVALID_ARG);
+ *           results are then unspecified but every access stays in bounds
+ * rows and tiles must be 16-byte aligned.
+ */
+SSA_API ssa_status ssa_window_plan(const int32_t* coords, int64_t N, int32_t m, const ssa_partition* win,
+                                   ssa_win_plan* plan, void* stream);
+
+/* Heads and types of the window calls. */
+typedef struct ssa_window_params {
+  int32_t hq;    /* query heads, 1..65535 */
+  int32_t hkv;   /* key/value heads, hq % hkv == 0 */
+  int32_t d;     /* head dim: 32, 64 or 128 (differential attention: 32 or 64) */
+  int32_t dtype; /* SSA_DTYPE_BF16 (bf16 tensor cores, fp32 sums) or SSA_DTYPE_F32 (fp32 throughout) */
+  float scale;   /* softmax scale; 0 means 1/sqrt(d) */
+} ssa_window_params;
+
+/*
+ * Learned relative position bias by buckets: query i and key j of a window with
+ * o = c_i - c_j (each component in -(m-1) .. m-1) get table[h, bucket[o]] added to their
+ * scaled score.  Offsets are numbered ((ox+m-1)*E + oy+m-1)*E + oz+m-1, E = 2m-1.
+ */
+typedef struct ssa_window_bias {
+  const float* table;    /* [hq, nb] fp32; a value at or below -1e38 (minus infinity, the type's
+                            lowest) bars the offsets of a bucket: a row with nothing left gives
+                            zeros, lse minus infinity and no gradient */
+  const int32_t* bucket; /* [E^3], or NULL: every offset is its own bucket (nb = E^3); an offset
+                            whose bucket is outside [0, nb) gets no bias and no gradient */
+  int32_t nb;            /* buckets */
+} ssa_window_bias;
+
+/*
+ * Rows of d values in 8 bits: value = codes * scale, scale a power of two per row, so that
+ * every value is exact in bf16 (ssa_act8_pack).
+ */
+typedef struct ssa_act8 {
+  const int8_t* codes; /* [N, H, d], 16-byte aligned */
+  const float* scale;  /* [N, H] */
+} ssa_act8;
+
+/*
+ * ssa_window_forward -- p_ij = softmax over the tokens j of i's cell of scale <q_i, k_j> +
+ * bias; out_i = sum_j p_ij v_j.
+ *   q, out [N, hq, d], k, v [N, hkv, d] in dtype, 16-byte aligned; bias NULL: none
+ *   lse    fp32 [N, hq] natural-log normalisers, or NULL
+ */
+SSA_API ssa_status ssa_window_forward(const ssa_window_params* p, const ssa_win_plan* plan,
+                                      const ssa_window_bias* bias, const void* q, const void* k, const void* v,
+                                      void* out, float* lse, void* stream);
+
+/*
+ * ssa_window_backward -- gradients of sum(dout * out): dq [N, hq, d], dk, dv [N, hkv, d] in
+ * dtype (each summed in fp32 and rounded once), dbias fp32 [hq, nb] (NULL: not wanted, or
+ * no bias); all written.  It recomputes the probabilities and needs nothing the forward left.
+ *   act8   NULL, or an array of three: Q, K, V from 8-bit checkpoints (q, k, v are then
+ *          ignored); the gradients are those at the values the codes hold, in dtype
+ *   ws     device workspace, 256-byte aligned, ssa_window_workspace_size(SSA_OP_WINDOW_BACKWARD,
+ *          p, plan) bytes (SSA_ERR_WORKSPACE if ws_bytes is less)
+ */
+SSA_API ssa_status ssa_window_backward(const ssa_window_params* p, const ssa_win_plan* plan,
+                                       const ssa_window_bias* bias, const void* q, const void* k, const void* v,
+                                       const ssa_act8* act8, const void* dout, void* dq, void* dk, void* dv,
+                                       float* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * ssa_diff_forward -- differential attention inside the cells: heads 2h and 2h+1 of q, and of
+ * k, are two softmax maps a1, a2 over one value head of width 2d (v's heads 2h, 2h+1 side by
+ * side):  out_i = sum_j (a1_ij - lambda_h a2_ij) v_j in out's heads 2h, 2h+1, with
+ *   lambda_h = exp(<lam[0,h], lam[1,h]>) - exp(<lam[2,h], lam[3,h]>) + lam_init.
+ *   q, out [N, hq, d], k, v [N, hkv, d]; hq and hkv even (SSA_ERR_INVALID_ARG otherwise); pair h
+ *   of q reads pair h / (hq / hkv) of k and v; lam fp32 [4, hq/2, d].  The plan's codes are not read.
+ *
+ * ssa_diff_backward -- gradients of sum(dout * out): dq, dk, dv in dtype and dlam fp32
+ * [4, hq/2, d]; act8 and ws as in ssa_window_backward (SSA_OP_DIFF_BACKWARD).
+ */
+SSA_API ssa_status ssa_diff_forward(const ssa_window_params* p, const ssa_win_plan* plan, const float* lam,
+                                    float lam_init, const void* q, const void* k, const void* v, void* out,
+                                    void* stream);
+SSA_API ssa_status ssa_diff_backward(const ssa_window_params* p, const ssa_win_plan* plan, const float* lam,
+                                     float lam_init, const void* q, const void* k, const void* v,
+                                     const ssa_act8* act8, const void* dout, void* dq, void* dk, void* dv,
+                                     float* dlam, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of SSA_OP_WINDOW_BACKWARD / SSA_OP_DIFF_BACKWARD; 0 for invalid arguments. */
+SSA_API size_t ssa_window_workspace_size(int32_t op, const ssa_window_params* p, const ssa_win_plan* plan);
+
+/*
+ * ssa_act8_pack -- rows x [rows, d] (dtype, 16-byte aligned, d 32, 64 or 128) into 8 bits:
+ * scale = the smallest power of two, 2^-126 at least, with |x| <= 127 scale for the row (1 for
+ * a row of zeros), codes = x / scale to the nearest whole number, ties to even (at most 63 in
+ * magnitude where the scale is 2^122: 64 of them would overflow).  A row with an infinity or a
+ * NaN gets a NaN scale.  ssa_act8_unpack writes codes * scale in dtype.
+ */
+SSA_API ssa_status ssa_act8_pack(int32_t dtype, int64_t rows, int32_t d, const void* x, int8_t* codes,
+                                 float* scale, void* stream);
+SSA_API ssa_status ssa_act8_unpack(int32_t dtype, int64_t rows, int32_t d, const int8_t* codes,
+                                   const float* scale, void* x, void* stream);
 
 /*
  * Workspace bytes needed by `op` (SSA_OP_BIN / _FORWARD / _BACKWARD / _GEO_SELECT /

@@ -208,7 +208,7 @@ size_t carve_bwd(void* base, const ssa_params* p, int32_t S, int64_t N, int64_t 
 
 extern "C" {
 
-SSA_API int32_t ssa_version(void) { return 100; }
+SSA_API int32_t ssa_version(void) { return 200; }
 
 SSA_API const char* ssa_error_string(ssa_status s) {
   switch (s) {
@@ -707,6 +707,221 @@ SSA_API ssa_status ssa_sp_backward(const ssa_params* p, int32_t S, int64_t N, co
   float* wdv = reinterpret_cast<float*>(extra + align256(sizeof(float) * (size_t)nr * p->hkv * p->d));
   return backward_common(p, loc->cu_seqlens, S, nr, N, 1, blk, nullptr, q, k, v, gates, saved, dout, dq, dk, dv,
                          dgates, ws, st, loc, wdk, wdv);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// attention inside the cells of a partition
+// ---------------------------------------------------------------------------
+
+namespace {
+
+bool aligned16(const void* x) { return reinterpret_cast<uintptr_t>(x) % 16 == 0; }
+
+// Heads, types and plan; maps: 1 window, 2 differential.
+ssa_status check_window(const ssa_window_params* p, const ssa_win_plan* plan, int maps) {
+  if (!p || !plan) return SSA_ERR_INVALID_ARG;
+  if (p->hq < 1 || p->hkv < 1 || p->hq % p->hkv != 0 || p->hq % maps != 0 || p->hkv % maps != 0)
+    return SSA_ERR_INVALID_ARG;
+  if (p->dtype != SSA_DTYPE_BF16 && p->dtype != SSA_DTYPE_F32) return SSA_ERR_INVALID_ARG;
+  if (!(p->scale >= 0.f) || isinf(p->scale)) return SSA_ERR_INVALID_ARG;
+  if (plan->n < 0 || plan->n > INT32_MAX - 1 || plan->count < 0 || plan->count > plan->n || plan->m < 0 ||
+      plan->m > SSA_WINDOW_MAX_EDGE)
+    return SSA_ERR_INVALID_ARG;
+  if (p->d != 32 && p->d != 64 && (p->d != 128 || maps == 2)) return SSA_ERR_UNSUPPORTED;
+  if (p->hq > 65535) return SSA_ERR_UNSUPPORTED;
+  if (plan->n / SSA_WINDOW_TILE + plan->count > INT32_MAX) return SSA_ERR_UNSUPPORTED;
+  if (plan->n > 0 && (plan->count < 1 || !plan->rows || !plan->tiles || !aligned16(plan->rows) || !aligned16(plan->tiles)))
+    return SSA_ERR_INVALID_ARG;
+  return SSA_OK;
+}
+
+ssa_status check_bias(const ssa_window_bias* b, const ssa_win_plan* plan) {
+  if (!b) return SSA_OK;
+  if (plan->m < 1 || b->nb < 1 || !b->table) return SSA_ERR_INVALID_ARG;
+  const int e = 2 * plan->m - 1;
+  if (!b->bucket && b->nb != e * e * e) return SSA_ERR_INVALID_ARG;
+  return SSA_OK;
+}
+
+ssa::WinArgs window_args(const ssa_window_params* p, const ssa_win_plan* plan, int maps, const ssa_window_bias* bias,
+                         const float* lam, float lam_init, const void* q, const void* k, const void* v) {
+  ssa::WinArgs a = {};
+  a.dtype = p->dtype;
+  a.d = p->d;
+  a.hq = p->hq;
+  a.hkv = p->hkv;
+  a.maps = maps;
+  a.scale = p->scale > 0.f ? p->scale : 1.f / sqrtf((float)p->d);
+  a.N = plan->n;
+  a.rows = reinterpret_cast<const int2*>(plan->rows);
+  a.tiles = reinterpret_cast<const int4*>(plan->tiles);
+  a.T = (int)(plan->n / SSA_WINDOW_TILE + plan->count);
+  a.m = plan->m;
+  if (bias) {
+    a.table = bias->table;
+    a.bucket = bias->bucket;
+    a.nb = bias->nb;
+  }
+  a.lam = lam;
+  a.lam_init = lam_init;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  return a;
+}
+
+// Workspace of the backward: lse2 and D per query head and row, partial bias gradients.
+size_t carve_window(void* base, const ssa_window_params* p, const ssa_win_plan* plan, int maps, ssa::WinArgs* a) {
+  Carver c(base);
+  const int e = 2 * plan->m - 1;
+  const int64_t T = plan->n / SSA_WINDOW_TILE + plan->count;
+  const int parts = ssa::window_parts(p->hq, T, plan->m);
+  float* lse2 = c.take<float>((size_t)p->hq * plan->n);
+  float* D = c.take<float>((size_t)p->hq * plan->n);
+  float* part = c.take<float>(maps == 1 && plan->m > 0 ? (size_t)p->hq * parts * e * e * e : 0);
+  if (a) {
+    a->lse2 = lse2;
+    a->D = D;
+    a->part = part;
+    a->parts = parts;
+  }
+  return c.used;
+}
+
+ssa_status window_backward(const ssa_window_params* p, const ssa_win_plan* plan, int maps, ssa::WinArgs& a,
+                           const ssa_act8* act8, const void* dout, void* dq, void* dk, void* dv, float* dbias,
+                           float* dlam, void* ws, size_t ws_bytes, cudaStream_t st) {
+  if (act8) {
+    for (int i = 0; i < 3; ++i)
+      if (!act8[i].codes || !act8[i].scale || !aligned16(act8[i].codes)) return SSA_ERR_INVALID_ARG;
+    a.act8 = 1;
+    a.q = act8[0].codes;
+    a.k = act8[1].codes;
+    a.v = act8[2].codes;
+    a.sq = act8[0].scale;
+    a.sk = act8[1].scale;
+    a.sv = act8[2].scale;
+  }
+  for (const void* x : {a.q, a.k, a.v, dout, (const void*)dq, (const void*)dk, (const void*)dv})
+    if (!x || !aligned16(x)) return SSA_ERR_INVALID_ARG;
+  if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0) return SSA_ERR_INVALID_ARG;
+  if (ws_bytes < carve_window(ws, p, plan, maps, &a)) return SSA_ERR_WORKSPACE;
+  a.dout = dout;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.dbias = dbias;
+  a.dlam = dlam;
+  cudaError_t e = ssa::window_bwd_simt(a, st);
+  if (e == cudaSuccess) e = ssa::window_param_grads(a, st);
+  return cuda_status(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+SSA_API ssa_status ssa_window_plan(const int32_t* coords, int64_t N, int32_t m, const ssa_partition* win,
+                                   ssa_win_plan* plan, void* stream) {
+  if (!plan || N < 0 || N > INT32_MAX - 1 || (coords && m < 1) || !partition_ok(win, N)) return SSA_ERR_INVALID_ARG;
+  if (coords && m > SSA_WINDOW_MAX_EDGE) return SSA_ERR_UNSUPPORTED;
+  if (win->count > N || (N > 0 && win->count < 1)) return SSA_ERR_INVALID_ARG;
+  if (N / SSA_WINDOW_TILE + win->count > INT32_MAX) return SSA_ERR_UNSUPPORTED;
+  if (N > 0 && (!plan->rows || !plan->tiles || !aligned16(plan->rows) || !aligned16(plan->tiles)))
+    return SSA_ERR_INVALID_ARG;
+  plan->n = N;
+  plan->count = win->count;
+  // no tokens, no coordinates: an edge that a bias can have is kept
+  plan->m = coords || (N == 0 && m >= 1 && m <= SSA_WINDOW_MAX_EDGE) ? m : 0;
+  if (N == 0) return SSA_OK;
+  int* sp = status_ptr();
+  if (!sp) return SSA_ERR_CUDA;
+  return cuda_status(ssa::window_plan(coords, N, m, win, reinterpret_cast<int2*>(plan->rows),
+                                      reinterpret_cast<int4*>(plan->tiles), sp, static_cast<cudaStream_t>(stream)));
+}
+
+SSA_API size_t ssa_window_workspace_size(int32_t op, const ssa_window_params* p, const ssa_win_plan* plan) {
+  const int maps = op == SSA_OP_WINDOW_BACKWARD ? 1 : op == SSA_OP_DIFF_BACKWARD ? 2 : 0;
+  if (!maps || check_window(p, plan, maps) != SSA_OK) return 0;
+  return carve_window(nullptr, p, plan, maps, nullptr);
+}
+
+SSA_API ssa_status ssa_window_forward(const ssa_window_params* p, const ssa_win_plan* plan,
+                                      const ssa_window_bias* bias, const void* q, const void* k, const void* v,
+                                      void* out, float* lse, void* stream) {
+  ssa_status s = check_window(p, plan, 1);
+  if (s == SSA_OK) s = check_bias(bias, plan);
+  if (s != SSA_OK || plan->n == 0) return s;
+  for (const void* x : {q, k, v, (const void*)out})
+    if (!x || !aligned16(x)) return SSA_ERR_INVALID_ARG;
+  ssa::WinArgs a = window_args(p, plan, 1, bias, nullptr, 0.f, q, k, v);
+  a.out = out;
+  a.lse = lse;
+  return cuda_status(ssa::window_fwd_simt(a, static_cast<cudaStream_t>(stream)));
+}
+
+SSA_API ssa_status ssa_window_backward(const ssa_window_params* p, const ssa_win_plan* plan,
+                                       const ssa_window_bias* bias, const void* q, const void* k, const void* v,
+                                       const ssa_act8* act8, const void* dout, void* dq, void* dk, void* dv,
+                                       float* dbias, void* ws, size_t ws_bytes, void* stream) {
+  ssa_status s = check_window(p, plan, 1);
+  if (s == SSA_OK) s = check_bias(bias, plan);
+  if (s != SSA_OK) return s;
+  if (dbias && !bias) return SSA_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (plan->n == 0)
+    return dbias ? cuda_status(cudaMemsetAsync(dbias, 0, sizeof(float) * (size_t)p->hq * bias->nb, st)) : SSA_OK;
+  ssa::WinArgs a = window_args(p, plan, 1, bias, nullptr, 0.f, q, k, v);
+  return window_backward(p, plan, 1, a, act8, dout, dq, dk, dv, dbias, nullptr, ws, ws_bytes, st);
+}
+
+SSA_API ssa_status ssa_diff_forward(const ssa_window_params* p, const ssa_win_plan* plan, const float* lam,
+                                    float lam_init, const void* q, const void* k, const void* v, void* out,
+                                    void* stream) {
+  ssa_status s = check_window(p, plan, 2);
+  if (s != SSA_OK) return s;
+  if (!lam || isnan(lam_init) || isinf(lam_init)) return SSA_ERR_INVALID_ARG;
+  if (plan->n == 0) return SSA_OK;
+  for (const void* x : {q, k, v, (const void*)out})
+    if (!x || !aligned16(x)) return SSA_ERR_INVALID_ARG;
+  ssa::WinArgs a = window_args(p, plan, 2, nullptr, lam, lam_init, q, k, v);
+  a.out = out;
+  return cuda_status(ssa::window_fwd_simt(a, static_cast<cudaStream_t>(stream)));
+}
+
+SSA_API ssa_status ssa_diff_backward(const ssa_window_params* p, const ssa_win_plan* plan, const float* lam,
+                                     float lam_init, const void* q, const void* k, const void* v,
+                                     const ssa_act8* act8, const void* dout, void* dq, void* dk, void* dv,
+                                     float* dlam, void* ws, size_t ws_bytes, void* stream) {
+  ssa_status s = check_window(p, plan, 2);
+  if (s != SSA_OK) return s;
+  if (!lam || !dlam || isnan(lam_init) || isinf(lam_init)) return SSA_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (plan->n == 0) return cuda_status(cudaMemsetAsync(dlam, 0, sizeof(float) * 2 * (size_t)p->hq * p->d, st));
+  ssa::WinArgs a = window_args(p, plan, 2, nullptr, lam, lam_init, q, k, v);
+  return window_backward(p, plan, 2, a, act8, dout, dq, dk, dv, nullptr, dlam, ws, ws_bytes, st);
+}
+
+SSA_API ssa_status ssa_act8_pack(int32_t dtype, int64_t rows, int32_t d, const void* x, int8_t* codes, float* scale,
+                                 void* stream) {
+  if ((dtype != SSA_DTYPE_BF16 && dtype != SSA_DTYPE_F32) || rows < 0 || rows > INT64_MAX / 128)
+    return SSA_ERR_INVALID_ARG;
+  if (d != 32 && d != 64 && d != 128) return SSA_ERR_UNSUPPORTED;
+  if (rows == 0) return SSA_OK;
+  if (!x || !codes || !scale || !aligned16(x) || !aligned16(codes)) return SSA_ERR_INVALID_ARG;
+  return cuda_status(ssa::act8_pack(dtype, rows, d, x, codes, scale, static_cast<cudaStream_t>(stream)));
+}
+
+SSA_API ssa_status ssa_act8_unpack(int32_t dtype, int64_t rows, int32_t d, const int8_t* codes, const float* scale,
+                                   void* x, void* stream) {
+  if ((dtype != SSA_DTYPE_BF16 && dtype != SSA_DTYPE_F32) || rows < 0 || rows > INT64_MAX / 128)
+    return SSA_ERR_INVALID_ARG;
+  if (d != 32 && d != 64 && d != 128) return SSA_ERR_UNSUPPORTED;
+  if (rows == 0) return SSA_OK;
+  if (!x || !codes || !scale || !aligned16(x) || !aligned16(codes)) return SSA_ERR_INVALID_ARG;
+  return cuda_status(ssa::act8_unpack(dtype, rows, d, codes, scale, x, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

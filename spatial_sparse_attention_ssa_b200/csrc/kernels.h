@@ -149,6 +149,44 @@ bool slc_mma_supported(int dtype, int d, int hq, int hkv, int topk);
 cudaError_t slc_fwd_mma(const FwdArgs& a, cudaStream_t st);
 cudaError_t slc_bwd_mma(const BwdArgs& a, cudaStream_t st);
 
+// Attention inside the cells (window_plan.cu, window_simt.cu, window_mma.cu); see window.cuh.
+struct WinArgs {
+  int dtype, d, hq, hkv, maps;  // maps: 1 window, 2 differential
+  float scale;
+  int64_t N;
+  const int2* rows;   // [N] token, code in cell order
+  const int4* tiles;  // [T] first row, rows (+ flag), cell begin, cell end
+  int T, m;
+  const float* table;  // bias [hq, nb], or null
+  const int32_t* bucket;
+  int nb;
+  const float* lam;  // [4, hq / 2, d] (maps = 2)
+  float lam_init;
+  int act8;  // q, k, v are int8 codes with the row scales below
+  const void *q, *k, *v;
+  const float *sq, *sk, *sv;
+  void* out;
+  float* lse;
+  // backward
+  const void* dout;
+  void *dq, *dk, *dv;
+  float *dbias, *dlam;
+  float *lse2, *D;  // [hq][N] in row order
+  float* part;      // [hq][parts][offsets] partial bias gradients
+  int parts;
+};
+cudaError_t window_plan(const int32_t* coords, int64_t N, int m, const ssa_partition* win, int2* rows, int4* tiles,
+                        int* status, cudaStream_t st);
+// Partial bias gradients per head that the backward keeps (rows of `part`).
+int window_parts(int hq, int64_t T, int m);
+cudaError_t window_fwd_simt(const WinArgs& a, cudaStream_t st);
+cudaError_t window_bwd_simt(const WinArgs& a, cudaStream_t st);
+// Sums of the partial bias gradients by bucket; gradients of lam from D.
+cudaError_t window_param_grads(const WinArgs& a, cudaStream_t st);
+cudaError_t act8_pack(int dtype, int64_t rows, int d, const void* x, int8_t* codes, float* scale, cudaStream_t st);
+cudaError_t act8_unpack(int dtype, int64_t rows, int d, const int8_t* codes, const float* scale, void* x,
+                        cudaStream_t st);
+
 // Diagnostics (diag.cu): a bounded wait that runs out; the FMA-pipe exponential.
 cudaError_t diag_wait_timeout(int* status, int* out, cudaStream_t st);
 cudaError_t diag_ex2(const float* x, float* y_poly, float* y_mufu, int64_t n, cudaStream_t st);

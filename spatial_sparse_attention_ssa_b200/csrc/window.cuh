@@ -1,0 +1,78 @@
+// Attention inside the cells of a partition: argument bundle and helpers shared by the
+// fp32 CUDA-core kernels (window_simt.cu) and the bf16 tensor-core kernels (window_mma.cu).
+//
+// MAPS = 1: window attention, optionally with a relative position bias.
+// MAPS = 2: differential attention; an output head has two maps (heads 2h, 2h + 1 of q and k)
+// and one value head of width 2 d (heads 2h, 2h + 1 of v side by side).  "Head" below is an
+// output head: hq / MAPS of them read hkv / MAPS key heads, G = hq / hkv each.
+//
+// Scores are held in units of log2: s2 = (scale <q, k> + bias) log2(e), p = 2^(s2 - max) / sum.
+// The backward keeps two numbers per row and map between its kernels: lse2 = max + log2(sum)
+// (plus infinity for a row with nothing left, so that every p is 0) and D = sum_j p_j dP_j.
+// D comes from the recomputed p and dP, not from the rounded output, so the fp32 gradients of
+// the bias and of lambda do not carry a rounding to bf16; the forward has to leave nothing.
+#pragma once
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace ssa {
+namespace win {
+
+constexpr int kTile = SSA_WINDOW_TILE;  // rows of a work tile
+constexpr int kDupFlag = 65536;         // tiles[].y: two tokens of the cell share a voxel
+
+// Offsets of a window of edge m, and the number of the offset 0.
+__host__ __device__ inline int offsets(int m) { return (2 * m - 1) * (2 * m - 1) * (2 * m - 1); }
+__host__ __device__ inline int center(int m) { return (m - 1) * ((2 * m - 1) * (2 * m - 1) + (2 * m - 1) + 1); }
+
+// 2^x (x <= 0 here, or minus infinity, or NaN).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kNegInf = -__builtin_inff();
+constexpr float kPosInf = __builtin_inff();
+
+// The maximum to subtract: 0 for a row with nothing left (every score minus infinity).
+__device__ __forceinline__ float safe_max(float m) { return m == kNegInf ? 0.f : m; }
+// 1 / sum, 0 for a row with nothing left; a NaN sum stays NaN.
+__device__ __forceinline__ float safe_inv(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float lse2_of(float m, float l) { return l == 0.f ? kPosInf : m + log2f(l); }
+
+// exp(<a, b>) pair of one head: lambda = e1 - e2 + init, from lam [4, heads, d].  Called by
+// whole warps.
+template <int D>
+__device__ __forceinline__ void lambda_terms(const float* __restrict__ lam, int heads, int h, float& e1, float& e2) {
+  const int lane = threadIdx.x & 31;
+  float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const int c = lane + 32 * i;
+    const size_t st = (size_t)heads * D, at = (size_t)h * D + c;
+    s1 = fmaf(lam[at], lam[st + at], s1);
+    s2 = fmaf(lam[2 * st + at], lam[3 * st + at], s2);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+    s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+  }
+  e1 = expf(s1);
+  e2 = expf(s2);
+}
+
+// Bias of offset `off` in units of log2; values at or below kBar bar as minus infinity does
+// (in units of log2 the type's lowest would overflow).
+constexpr float kBar = -1e38f;
+__device__ __forceinline__ float bias2_at(const WinArgs& a, int h, int off) {
+  const int b = a.bucket ? __ldg(a.bucket + off) : off;
+  if ((unsigned)b >= (unsigned)a.nb) return 0.f;
+  const float x = __ldg(a.table + (size_t)h * a.nb + b);
+  return x <= kBar ? kNegInf : x * kLog2e;
+}
+
+}  // namespace win
+}  // namespace ssa

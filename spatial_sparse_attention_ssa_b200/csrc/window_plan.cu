@@ -1,0 +1,276 @@
+// Plan of the window operators, the sums of their parameter gradients, and 8-bit checkpoints.
+#include "window.cuh"
+
+namespace ssa {
+namespace {
+
+using namespace win;
+
+// One thread per row (position in cell order): its token and offset code, and, from the first
+// row of every 16 of a cell, the tile.  Tile slots need no scan: cell c takes the slots from
+// ptr[c] / 16 + c on; floor(b / 16) - floor(a / 16) + 1 >= ceil((b - a) / 16) of them.
+__global__ void plan_rows_kernel(const int32_t* __restrict__ coords, int64_t N, int64_t W, int m,
+                                 const int32_t* __restrict__ id, const int32_t* __restrict__ perm,
+                                 const int32_t* __restrict__ ptr, int2* __restrict__ rows, int4* __restrict__ tiles,
+                                 int* status) {
+  for (int64_t pos = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; pos < N;
+       pos += (int64_t)gridDim.x * blockDim.x) {
+    const int tok = perm[pos];
+    bool ok = (unsigned)tok < (unsigned)N;
+    const int c = ok ? id[tok] : 0;
+    ok = ok && (unsigned)c < (unsigned)W;
+    const int a = ok ? ptr[c] : 0, b = ok ? ptr[c + 1] : 0;
+    ok = ok && a >= 0 && a <= pos && pos < b && b <= N;
+    if (!ok) {
+      rows[pos] = make_int2(0, 0);
+      atomicOr(status, kStatusSelection);
+      continue;
+    }
+    int code = 0;
+    if (coords) {
+      const int e = 2 * m - 1;
+      int x[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const int r = coords[3 * (int64_t)tok + i] % m;
+        x[i] = r < 0 ? r + m : r;
+      }
+      code = (x[0] * e + x[1]) * e + x[2];
+    }
+    rows[pos] = make_int2(tok, code);
+    if ((pos - a) % kTile == 0) {
+      const int n = (int)(b - pos < kTile ? b - pos : kTile);
+      tiles[a / kTile + c + (pos - a) / kTile] = make_int4((int)pos, n, a, b);
+    }
+  }
+}
+
+// One warp per cell: does it hold two tokens with one code?  A bitmap of the cell's m^3 voxels
+// (m <= 16); a cell with more tokens than voxels does without looking.
+__global__ void plan_dup_kernel(int64_t N, int64_t W, int m, const int32_t* __restrict__ ptr,
+                                const int2* __restrict__ rows, int4* __restrict__ tiles) {
+  __shared__ uint32_t bits[4][128];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int e = 2 * m - 1, vox = m * m * m;
+  for (int64_t c = (int64_t)blockIdx.x * 4 + warp; c < W; c += (int64_t)gridDim.x * 4) {
+    const int a = ptr[c], b = ptr[c + 1];
+    if (a < 0 || b > N || b <= a) continue;  // reported by plan_rows_kernel
+    bool dup = b - a > vox;
+    if (!dup) {
+      for (int i = lane; i < 128; i += 32) bits[warp][i] = 0;
+      __syncwarp();
+      for (int i = a + lane; i < b; i += 32) {
+        const int code = rows[i].y;
+        const int v = (code / (e * e) * m + code / e % e) * m + code % e;
+        dup |= (atomicOr(&bits[warp][v >> 5], 1u << (v & 31)) >> (v & 31)) & 1;
+      }
+      dup = __any_sync(0xffffffffu, dup);
+      __syncwarp();
+    }
+    if (dup) {
+      const int64_t slot = a / kTile + c, nt = (b - a + kTile - 1) / kTile;
+      for (int64_t i = lane; i < nt; i += 32) tiles[slot + i].y |= kDupFlag;
+    }
+  }
+}
+
+// dst[h][o] = sum over parts of part[h][i][o], in a fixed order, left in part i = 0.
+__global__ void bias_parts_kernel(float* __restrict__ part, int parts, int T) {
+  const int o = blockIdx.x * blockDim.x + threadIdx.x;
+  if (o >= T) return;
+  float* p = part + (size_t)blockIdx.y * parts * T + o;
+  float s = 0.f;
+  for (int i = 0; i < parts; ++i) s += p[(size_t)i * T];
+  p[0] = s;
+}
+
+// dbias[h][b] = sum of the offsets o with bucket b, in order of o; one thread per bucket.
+__global__ void bias_buckets_kernel(const float* __restrict__ part, int parts, int T,
+                                    const int32_t* __restrict__ bucket, int nb, float* __restrict__ dbias) {
+  __shared__ int sb[1024];
+  __shared__ float sv[1024];
+  const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  const float* p = part + (size_t)blockIdx.y * parts * T;
+  float s = 0.f;
+  for (int o0 = 0; o0 < T; o0 += 1024) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < 1024 && o0 + i < T; i += blockDim.x) {
+      sb[i] = bucket ? bucket[o0 + i] : o0 + i;
+      sv[i] = p[o0 + i];
+    }
+    __syncthreads();
+    const int n = T - o0 < 1024 ? T - o0 : 1024;
+    for (int i = 0; i < n; ++i) s += sb[i] == b ? sv[i] : 0.f;
+  }
+  if (b < nb) dbias[(size_t)blockIdx.y * nb + b] = s;
+}
+
+// dlambda of a head = -sum of D of its second map; then the chain rule through
+// lambda = exp(<x0, x1>) - exp(<x2, x3>) + init.  One block per head, fixed order, fp64 sums.
+template <int D>
+__global__ void lam_grad_kernel(const float* __restrict__ lam, const float* __restrict__ Drow, int64_t N, int heads,
+                                float* __restrict__ dlam) {
+  __shared__ double red[256];
+  const int h = blockIdx.x, t = threadIdx.x;
+  const float* p = Drow + (size_t)(2 * h + 1) * N;
+  double s = 0.0;
+  for (int64_t i = t; i < N; i += 256) s += (double)p[i];
+  red[t] = s;
+  __syncthreads();
+  for (int o = 128; o; o >>= 1) {
+    if (t < o) red[t] += red[t + o];
+    __syncthreads();
+  }
+  const float dl = (float)-red[0];
+  float e1, e2;
+  lambda_terms<D>(lam, heads, h, e1, e2);
+  const size_t st = (size_t)heads * D, at = (size_t)h * D + t;
+  if (t < D) {
+    dlam[at] = dl * e1 * lam[st + at];
+    dlam[st + at] = dl * e1 * lam[at];
+    dlam[2 * st + at] = -dl * e2 * lam[3 * st + at];
+    dlam[3 * st + at] = -dl * e2 * lam[2 * st + at];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit checkpoints
+// ---------------------------------------------------------------------------
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* x);
+template <>
+__device__ __forceinline__ void load8<float>(const float* p, float* x) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* x) {
+  const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[2 * j] = __uint_as_float(w[j] << 16);
+    x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float* x) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                            pack_bf16x2(x[6], x[7]));
+}
+
+// d / 8 lanes per row, 8 values each.  The step is the smallest power of two s >= 2^-126 with
+// top <= 127 s: with top = f 2^e, f in [1, 2), s = 2^(e - 6) while f <= 127 / 64, else 2^(e - 5).
+template <typename T>
+__global__ void act8_pack_kernel(const T* __restrict__ x, int64_t groups, int per_row, int8_t* __restrict__ codes,
+                                 float* __restrict__ scale) {
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < ((groups + 31) & ~(int64_t)31);
+       i += (int64_t)gridDim.x * blockDim.x) {
+    float v[8];
+    if (i < groups) {
+      load8<T>(x + 8 * i, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    }
+    uint32_t top = 0;  // of the magnitudes' bits: NaN and infinity come out on top
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+    for (int o = per_row >> 1; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    int e = (int)(top >> 23);  // biased exponent; 0 for zero and subnormal rows
+    e = e - 6 + ((top & 0x7fffffu) > 0x7e0000u ? 1 : 0);
+    e = e < 1 ? 1 : e;
+    const bool bad = top >= 0x7f800000u;
+    const float s = bad ? __uint_as_float(0x7fc00000u) : top == 0 ? 1.f : __uint_as_float((uint32_t)e << 23);
+    const int most = e == 249 ? 63 : 127;  // 64 * 2^122 would overflow
+    const float r = bad || top == 0 ? 0.f : __uint_as_float((uint32_t)(254 - e) << 23);  // 1 / s
+    if (i < groups) {
+      uint32_t w[2] = {0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int n = bad ? 0 : max(-most, min(most, __float2int_rn(v[j] * r)));
+        w[j >> 2] |= (uint32_t)(n & 255) << (8 * (j & 3));
+      }
+      reinterpret_cast<uint2*>(codes)[i] = make_uint2(w[0], w[1]);
+      if (i % per_row == 0) scale[i / per_row] = s;
+    }
+  }
+}
+
+template <typename T>
+__global__ void act8_unpack_kernel(const int8_t* __restrict__ codes, const float* __restrict__ scale, int64_t groups,
+                                   int per_row, T* __restrict__ x) {
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < groups;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes) + i);
+    const float s = __ldg(scale + i / per_row);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (float)(int8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3))) * s;
+    store8(x + 8 * i, v);
+  }
+}
+
+int blocks_for(int64_t threads, int per_block) {
+  const int64_t b = (threads + per_block - 1) / per_block;
+  return (int)(b < 148 * 16 ? (b > 0 ? b : 1) : 148 * 16);
+}
+
+}  // namespace
+
+cudaError_t window_plan(const int32_t* coords, int64_t N, int m, const ssa_partition* part, int2* rows, int4* tiles,
+                        int* status, cudaStream_t st) {
+  const int64_t T = N / kTile + part->count;
+  cudaError_t e = cudaMemsetAsync(tiles, 0, sizeof(int4) * T, st);
+  if (e != cudaSuccess) return e;
+  SSA_LAUNCH("plan_rows_kernel", plan_rows_kernel, blocks_for(N, 256), 256, 0, st, coords, N, part->count, m, part->id,
+             part->perm, part->ptr, rows, tiles, status);
+  if (coords)
+    SSA_LAUNCH("plan_dup_kernel", plan_dup_kernel, blocks_for(part->count, 4), 128, 0, st, N, part->count, m,
+               part->ptr, rows, tiles);
+  return cudaGetLastError();
+}
+
+cudaError_t window_param_grads(const WinArgs& a, cudaStream_t st) {
+  if (a.dbias) {
+    const int T = offsets(a.m);
+    const dim3 g1((T + 127) / 128, a.hq), g2((a.nb + 127) / 128, a.hq);
+    SSA_LAUNCH("bias_parts_kernel", bias_parts_kernel, g1, 128, 0, st, a.part, a.parts, T);
+    SSA_LAUNCH("bias_buckets_kernel", bias_buckets_kernel, g2, 128, 0, st, a.part, a.parts, T, a.bucket, a.nb,
+               a.dbias);
+  }
+  if (a.dlam) {
+    auto kern = a.d == 32 ? lam_grad_kernel<32> : lam_grad_kernel<64>;
+    SSA_LAUNCH("lam_grad_kernel", kern, a.hq / 2, 256, 0, st, a.lam, a.D, a.N, a.hq / 2, a.dlam);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t act8_pack(int dtype, int64_t rows, int d, const void* x, int8_t* codes, float* scale, cudaStream_t st) {
+  const int64_t g = rows * (d / 8);
+  if (dtype == SSA_DTYPE_BF16)
+    SSA_LAUNCH("act8_pack_kernel", act8_pack_kernel<__nv_bfloat16>, blocks_for(g, 256), 256, 0, st,
+               static_cast<const __nv_bfloat16*>(x), g, d / 8, codes, scale);
+  else
+    SSA_LAUNCH("act8_pack_kernel", act8_pack_kernel<float>, blocks_for(g, 256), 256, 0, st,
+               static_cast<const float*>(x), g, d / 8, codes, scale);
+  return cudaGetLastError();
+}
+
+cudaError_t act8_unpack(int dtype, int64_t rows, int d, const int8_t* codes, const float* scale, void* x,
+                        cudaStream_t st) {
+  const int64_t g = rows * (d / 8);
+  if (dtype == SSA_DTYPE_BF16)
+    SSA_LAUNCH("act8_unpack_kernel", act8_unpack_kernel<__nv_bfloat16>, blocks_for(g, 256), 256, 0, st, codes, scale,
+               g, d / 8, static_cast<__nv_bfloat16*>(x));
+  else
+    SSA_LAUNCH("act8_unpack_kernel", act8_unpack_kernel<float>, blocks_for(g, 256), 256, 0, st, codes, scale, g, d / 8,
+               static_cast<float*>(x));
+  return cudaGetLastError();
+}
+
+}  // namespace ssa

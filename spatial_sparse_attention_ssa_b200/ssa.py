@@ -26,12 +26,16 @@ DTYPE_BF16, DTYPE_F32 = 0, 1
 GATE_WEIGHTS, GATE_LOGITS = 0, 1
 OP_BIN, OP_FORWARD, OP_BACKWARD, OP_GEO_SELECT, OP_CROSS_FORWARD, OP_CROSS_BACKWARD = 0, 1, 2, 3, 4, 5
 OP_SP_FORWARD, OP_SP_BACKWARD = 6, 7
+OP_WINDOW_BACKWARD, OP_DIFF_BACKWARD = 8, 9
+WINDOW_MAX_EDGE, WINDOW_TILE = 16, 16
 SEL_SCORES, SEL_GIVEN = 0, 1
 
 EXPORTS = ("ssa_bin", "ssa_forward", "ssa_backward", "ssa_workspace_size", "ssa_error_string",
            "ssa_get_device_status", "ssa_version", "ssa_launch_count", "ssa_profile_enable",
            "ssa_profile_read", "ssa_geo_select", "ssa_cross_forward", "ssa_cross_backward", "ssa_pool",
-           "ssa_diag_wait_timeout", "ssa_diag_ex2", "ssa_sp_forward", "ssa_sp_backward")
+           "ssa_diag_wait_timeout", "ssa_diag_ex2", "ssa_sp_forward", "ssa_sp_backward",
+           "ssa_window_plan", "ssa_window_forward", "ssa_window_backward", "ssa_window_workspace_size",
+           "ssa_diff_forward", "ssa_diff_backward", "ssa_act8_pack", "ssa_act8_unpack")
 
 
 class SSAError(RuntimeError):
@@ -69,6 +73,24 @@ class Saved(ctypes.Structure):
     _fields_ = [("kc", ctypes.c_void_p), ("vc", ctypes.c_void_p), ("ks", ctypes.c_void_p),
                 ("vs", ctypes.c_void_p), ("o_branch", ctypes.c_void_p), ("lse", ctypes.c_void_p),
                 ("sel", ctypes.c_void_p)]
+
+
+class WinPlanC(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_void_p), ("tiles", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("count", ctypes.c_int64), ("m", ctypes.c_int32)]
+
+
+class WindowParams(ctypes.Structure):
+    _fields_ = [("hq", ctypes.c_int32), ("hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class WindowBiasC(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("bucket", ctypes.c_void_p), ("nb", ctypes.c_int32)]
+
+
+class Act8C(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
 
 
 _LIB = None
@@ -111,6 +133,24 @@ def _lib():
         lib.ssa_pool.restype = ctypes.c_int
         lib.ssa_geo_select.argtypes = [vp, vp, i32, i64, i32, pp, i32, i32, i32, vp, vp, sz, vp]
         lib.ssa_geo_select.restype = ctypes.c_int
+        wp, pl, wb, a8 = (ctypes.POINTER(x) for x in (WindowParams, WinPlanC, WindowBiasC, Act8C))
+        lib.ssa_window_plan.argtypes = [vp, i64, i32, pp, pl, vp]
+        lib.ssa_window_plan.restype = ctypes.c_int
+        lib.ssa_window_workspace_size.argtypes = [i32, wp, pl]
+        lib.ssa_window_workspace_size.restype = sz
+        lib.ssa_window_forward.argtypes = [wp, pl, wb, vp, vp, vp, vp, vp, vp]
+        lib.ssa_window_forward.restype = ctypes.c_int
+        lib.ssa_window_backward.argtypes = [wp, pl, wb, vp, vp, vp, a8, vp, vp, vp, vp, vp, vp, sz, vp]
+        lib.ssa_window_backward.restype = ctypes.c_int
+        f32 = ctypes.c_float
+        lib.ssa_diff_forward.argtypes = [wp, pl, vp, f32, vp, vp, vp, vp, vp]
+        lib.ssa_diff_forward.restype = ctypes.c_int
+        lib.ssa_diff_backward.argtypes = [wp, pl, vp, f32, vp, vp, vp, a8, vp, vp, vp, vp, vp, vp, sz, vp]
+        lib.ssa_diff_backward.restype = ctypes.c_int
+        lib.ssa_act8_pack.argtypes = [i32, i64, i32, vp, vp, vp, vp]
+        lib.ssa_act8_pack.restype = ctypes.c_int
+        lib.ssa_act8_unpack.argtypes = [i32, i64, i32, vp, vp, vp, vp]
+        lib.ssa_act8_unpack.restype = ctypes.c_int
         lib.ssa_workspace_size.argtypes = [i32, ctypes.POINTER(Params), i32, i64, i64, i64]
         lib.ssa_workspace_size.restype = sz
         lib.ssa_error_string.argtypes = [ctypes.c_int]
@@ -533,6 +573,243 @@ def ssa_cross_backward(p: Params, q_cu: torch.Tensor, blk: Bins, q, k, v, gates,
                                    _ptr(dv), _ptr(dg), _ptr(ws), ws.numel(), _stream(dev))
     _check(st, "ssa_cross_backward")
     return dq, dk, dv, dg
+
+
+# ---------------------------------------------------------------------------
+# attention inside the cells of a partition
+# ---------------------------------------------------------------------------
+
+
+def _on_one_device(*ts: torch.Tensor | None) -> torch.device:
+    """The device that all tensors share (contiguous CUDA tensors, as every call wants)."""
+    ts = [t for t in ts if t is not None]
+    _require_cuda(*ts)
+    if any(t.device != ts[0].device for t in ts):
+        raise ValueError("SSA tensors must be on one device")
+    return ts[0].device
+
+
+def _call(device: torch.device, name: str, *args) -> None:
+    """One library call on the device's current stream, with that device current."""
+    fn = getattr(_lib(), name)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream(device))
+    _check(st, name)
+
+
+def _want(t: torch.Tensor, shape: tuple, dtype: torch.dtype, name: str) -> None:
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError("%s must be %s %s, got %s %s" % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+
+
+@dataclass
+class WindowPlan:
+    """Work plan of one partition (see ssa_win_plan in include/ssa.h): made once per voxel
+    set, read by every layer and both passes of the window and differential calls."""
+    rows: torch.Tensor   # int32 [n, 2]
+    tiles: torch.Tensor  # int32 [n // 16 + count, 4]
+    n: int
+    count: int
+    m: int
+
+    def __post_init__(self):
+        self._c = WinPlanC(_ptr(self.rows), _ptr(self.tiles), self.n, self.count, self.m)
+        self._ref = ctypes.byref(self._c)
+
+
+def ssa_window_plan(coords: torch.Tensor | None, win: Bins, m: int = 0) -> WindowPlan:
+    """Plan of the partition `win` (from ssa_bin; `blk` serves as well).  With the binned
+    coordinates and the window edge m (at most WINDOW_MAX_EDGE) it carries the offset codes
+    that a bias reads; coords = None makes a plan without them, for any partition."""
+    dev = _on_one_device(win.perm, win.id, win.ptr, coords)
+    n = int(win.perm.shape[0])
+    if coords is not None:
+        _want(coords, (n, 3), torch.int32, "coords")
+    e = lambda *s: torch.empty(*s, dtype=torch.int32, device=dev)  # noqa: E731
+    plan = WindowPlan(e(n, 2), e(n // WINDOW_TILE + win.count, 4), n, int(win.count), int(m) if coords is not None else 0)
+    pb = win.c()
+    _call(dev, "ssa_window_plan", _ptr(coords), n, int(m), ctypes.byref(pb), plan._ref)
+    return plan
+
+
+def make_window_params(hq: int, hkv: int, d: int, dtype: torch.dtype, scale: float = 0.0) -> WindowParams:
+    """Heads and type of the window and differential calls (scale 0: 1/sqrt(d))."""
+    dt = DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32 if dtype == torch.float32 else None
+    if dt is None:
+        raise ValueError("dtype must be torch.bfloat16 or torch.float32")
+    p = WindowParams(hq, hkv, d, dt, scale)
+    p._dtype = dtype
+    return p
+
+
+@dataclass
+class WindowBias:
+    """Learned relative position bias: table fp32 [hq, nb]; bucket int32 [(2m-1)^3] maps an
+    offset to its bucket (None: every offset its own, nb = (2m-1)^3)."""
+    table: torch.Tensor
+    bucket: torch.Tensor | None = None
+
+
+def window_log_buckets(m: int, device="cuda") -> tuple[torch.Tensor, int]:
+    """(bucket, nb) of logarithmic buckets: per axis the sign of the offset and the power of
+    two that holds its magnitude (0, 1, 2-3, 4-7, 8-15)."""
+    a = torch.arange(-(m - 1), m, device=device)
+    axis = torch.floor(torch.log2(a.abs().clamp_min(1).double())).long().add(1).mul(a.sign())
+    top = int(axis.max())
+    k = 2 * top + 1
+    x = axis + top
+    return ((x[:, None, None] * k + x[None, :, None]) * k + x[None, None, :]).reshape(-1).to(torch.int32), k ** 3
+
+
+@dataclass
+class Act8:
+    """Rows in 8 bits: codes int8 [..., d], scale fp32 [...] (a power of two per row)."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+
+
+def _bias_c(bias: WindowBias | None, p: WindowParams, plan: WindowPlan):
+    if bias is None:
+        return None, 0
+    if bias.table.dim() != 2:
+        raise ValueError("bias.table must be [hq, nb]")
+    nb = int(bias.table.shape[1])
+    _want(bias.table, (p.hq, nb), torch.float32, "bias.table")
+    if bias.bucket is not None:
+        _want(bias.bucket, ((2 * plan.m - 1) ** 3,), torch.int32, "bias.bucket")
+    return WindowBiasC(_ptr(bias.table), _ptr(bias.bucket), nb), nb
+
+
+def _qkv(p: WindowParams, plan: WindowPlan, q, k, v):
+    """(pointers of q, k, v, the Act8C array or None, their tensors)."""
+    n = plan.n
+    names = (("q", q, p.hq), ("k", k, p.hkv), ("v", v, p.hkv))
+    if all(isinstance(x, Act8) for x in (q, k, v)):
+        for name, x, h in names:
+            _want(x.codes, (n, h, p.d), torch.int8, name + ".codes")
+            _want(x.scale, (n, h), torch.float32, name + ".scale")
+        arr = (Act8C * 3)(*((_ptr(x.codes), _ptr(x.scale)) for x in (q, k, v)))
+        return (None, None, None), arr, [t for x in (q, k, v) for t in (x.codes, x.scale)]
+    for name, x, h in names:
+        _want(x, (n, h, p.d), p._dtype, name)
+    return (_ptr(q), _ptr(k), _ptr(v)), None, [q, k, v]
+
+
+def ssa_window_forward(p: WindowParams, plan: WindowPlan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                       bias: WindowBias | None = None, out: torch.Tensor | None = None,
+                       lse: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of every token over the tokens of its cell, with an optional learned relative
+    position bias: out [N, hq, d].  `lse` (fp32 [N, hq]) receives the softmax normalisers."""
+    ptrs, _, ts = _qkv(p, plan, q, k, v)
+    bc, _ = _bias_c(bias, p, plan)
+    dev = _on_one_device(*ts, plan.rows, out, lse, *((bias.table, bias.bucket) if bias else ()))
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _want(out, q.shape, q.dtype, "out")
+    if lse is not None:
+        _want(lse, (plan.n, p.hq), torch.float32, "lse")
+    _call(dev, "ssa_window_forward", p, plan._ref, bc, *ptrs, _ptr(out), _ptr(lse))
+    return out
+
+
+def _window_backward(op: int, name: str, p: WindowParams, plan: WindowPlan, extra, extra_tensors, q, k, v, dout,
+                     last: torch.Tensor | None, grads, workspace):
+    ptrs, a8, ts = _qkv(p, plan, q, k, v)
+    _want(dout, (plan.n, p.hq, p.d), p._dtype, "dout")
+    dev = _on_one_device(*ts, dout, plan.rows, last, *extra_tensors, *(grads or ()))
+    shapes = ((plan.n, p.hq, p.d), (plan.n, p.hkv, p.d), (plan.n, p.hkv, p.d))
+    if grads is None:
+        grads = tuple(torch.empty(s, dtype=p._dtype, device=dev) for s in shapes)
+    else:
+        for g, s in zip(grads, shapes):
+            _want(g, s, p._dtype, "grads")
+    need = int(_lib().ssa_window_workspace_size(op, p, plan._ref))
+    ws = workspace if workspace is not None and workspace.numel() >= need else _workspace(need, dev)
+    _call(dev, name, p, plan._ref, *extra, *ptrs, a8, _ptr(dout), *(_ptr(g) for g in grads), _ptr(last), _ptr(ws),
+          ws.numel())
+    return (*grads, last)
+
+
+def ssa_window_backward(p: WindowParams, plan: WindowPlan, q, k, v, dout: torch.Tensor,
+                        bias: WindowBias | None = None, grads=None, dbias: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None):
+    """Gradients of ssa_window_forward: (dq, dk, dv, dbias), dq, dk, dv in the dtype of the
+    inputs, dbias fp32 [hq, nb] (None without a bias).  q, k, v are the forward's, or three
+    Act8 of them."""
+    bc, nb = _bias_c(bias, p, plan)
+    if bias is None and dbias is not None:
+        raise ValueError("dbias without a bias")
+    if bias is not None and dbias is None:
+        dbias = torch.empty(p.hq, nb, dtype=torch.float32, device=dout.device)
+    elif bias is not None:
+        _want(dbias, (p.hq, nb), torch.float32, "dbias")
+    return _window_backward(OP_WINDOW_BACKWARD, "ssa_window_backward", p, plan, (bc,),
+                            (bias.table, bias.bucket) if bias else (), q, k, v, dout, dbias, grads, workspace)
+
+
+def ssa_diff_forward(p: WindowParams, plan: WindowPlan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     lam: torch.Tensor, lam_init: float, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Differential attention inside the cells: the difference of the softmax maps of heads
+    2h and 2h+1 over the value heads 2h, 2h+1 side by side; lam fp32 [4, hq/2, d] holds the
+    weights' vectors (see ssa_diff_forward in include/ssa.h).  Returns out [N, hq, d]."""
+    ptrs, _, ts = _qkv(p, plan, q, k, v)
+    _want(lam, (4, p.hq // 2, p.d), torch.float32, "lam")
+    dev = _on_one_device(*ts, lam, plan.rows, out)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _want(out, q.shape, q.dtype, "out")
+    _call(dev, "ssa_diff_forward", p, plan._ref, _ptr(lam), float(lam_init), *ptrs, _ptr(out))
+    return out
+
+
+def ssa_diff_backward(p: WindowParams, plan: WindowPlan, q, k, v, lam: torch.Tensor, lam_init: float,
+                      dout: torch.Tensor, grads=None, dlam: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None):
+    """Gradients of ssa_diff_forward: (dq, dk, dv, dlam), dlam fp32 [4, hq/2, d].  q, k, v are
+    the forward's, or three Act8 of them."""
+    _want(lam, (4, p.hq // 2, p.d), torch.float32, "lam")
+    if dlam is None:
+        dlam = torch.empty_like(lam)
+    else:
+        _want(dlam, lam.shape, torch.float32, "dlam")
+    return _window_backward(OP_DIFF_BACKWARD, "ssa_diff_backward", p, plan, (_ptr(lam), float(lam_init)), (lam,), q, k, v,
+                            dout, dlam, grads, workspace)
+
+
+def ssa_act8_pack(x: torch.Tensor, out: Act8 | None = None) -> Act8:
+    """Rows x [..., d] (bf16 or fp32, d 32, 64 or 128) in 8 bits with a power-of-two scale each."""
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("x must be bfloat16 or float32")
+    if out is None:
+        _require_cuda(x)
+        out = Act8(torch.empty(x.shape, dtype=torch.int8, device=x.device),
+                   torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device))
+    _want(out.codes, x.shape, torch.int8, "codes")
+    _want(out.scale, x.shape[:-1], torch.float32, "scale")
+    dev = _on_one_device(x, out.codes, out.scale)
+    _call(dev, "ssa_act8_pack", DTYPE_BF16 if x.dtype == torch.bfloat16 else DTYPE_F32, out.scale.numel(),
+          int(x.shape[-1]), _ptr(x), _ptr(out.codes), _ptr(out.scale))
+    return out
+
+
+def ssa_act8_unpack(held: Act8, dtype: torch.dtype, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values that `held` stands for, in bf16 (exact) or fp32."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("dtype must be torch.bfloat16 or torch.float32")
+    if out is None:
+        out = torch.empty(held.codes.shape, dtype=dtype, device=held.codes.device)
+    _want(out, held.codes.shape, dtype, "out")
+    _want(held.codes, out.shape, torch.int8, "codes")
+    _want(held.scale, out.shape[:-1], torch.float32, "scale")
+    dev = _on_one_device(held.codes, held.scale, out)
+    _call(dev, "ssa_act8_unpack", DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32, held.scale.numel(),
+          int(out.shape[-1]), _ptr(held.codes), _ptr(held.scale), _ptr(out))
+    return out
 
 
 def device_status(stream: int | None = None) -> int:
