@@ -780,14 +780,21 @@ size_t carve_window(void* base, const ssa_window_params* p, const ssa_win_plan* 
   const int parts = ssa::window_parts(p->hq, T, plan->m);
   float* lse2 = c.take<float>((size_t)p->hq * plan->n);
   float* D = c.take<float>((size_t)p->hq * plan->n);
-  float* part = c.take<float>(maps == 1 && plan->m > 0 ? (size_t)p->hq * parts * e * e * e : 0);
+  const size_t tab = maps == 1 && plan->m > 0 ? (size_t)p->hq * e * e * e : 0;
+  float* part = c.take<float>(tab * parts);
+  float* tab2 = c.take<float>(tab);
   if (a) {
     a->lse2 = lse2;
     a->D = D;
     a->part = part;
     a->parts = parts;
+    a->tab2 = tab2;
   }
   return c.used;
+}
+
+cudaError_t window_forward(const ssa::WinArgs& a, cudaStream_t st) {
+  return a.dtype == SSA_DTYPE_BF16 ? ssa::window_fwd_mma(a, st) : ssa::window_fwd_simt(a, st);
 }
 
 ssa_status window_backward(const ssa_window_params* p, const ssa_win_plan* plan, int maps, ssa::WinArgs& a,
@@ -814,7 +821,9 @@ ssa_status window_backward(const ssa_window_params* p, const ssa_win_plan* plan,
   a.dv = dv;
   a.dbias = dbias;
   a.dlam = dlam;
-  cudaError_t e = ssa::window_bwd_simt(a, st);
+  a.status = status_ptr();
+  if (!a.status) return SSA_ERR_CUDA;
+  cudaError_t e = a.dtype == SSA_DTYPE_BF16 ? ssa::window_bwd_mma(a, st) : ssa::window_bwd_simt(a, st);
   if (e == cudaSuccess) e = ssa::window_param_grads(a, st);
   return cuda_status(e);
 }
@@ -859,7 +868,7 @@ SSA_API ssa_status ssa_window_forward(const ssa_window_params* p, const ssa_win_
   ssa::WinArgs a = window_args(p, plan, 1, bias, nullptr, 0.f, q, k, v);
   a.out = out;
   a.lse = lse;
-  return cuda_status(ssa::window_fwd_simt(a, static_cast<cudaStream_t>(stream)));
+  return cuda_status(window_forward(a, static_cast<cudaStream_t>(stream)));
 }
 
 SSA_API ssa_status ssa_window_backward(const ssa_window_params* p, const ssa_win_plan* plan,
@@ -888,7 +897,7 @@ SSA_API ssa_status ssa_diff_forward(const ssa_window_params* p, const ssa_win_pl
     if (!x || !aligned16(x)) return SSA_ERR_INVALID_ARG;
   ssa::WinArgs a = window_args(p, plan, 2, nullptr, lam, lam_init, q, k, v);
   a.out = out;
-  return cuda_status(ssa::window_fwd_simt(a, static_cast<cudaStream_t>(stream)));
+  return cuda_status(window_forward(a, static_cast<cudaStream_t>(stream)));
 }
 
 SSA_API ssa_status ssa_diff_backward(const ssa_window_params* p, const ssa_win_plan* plan, const float* lam,

@@ -174,6 +174,8 @@ struct WinArgs {
   float *lse2, *D;  // [hq][N] in row order
   float* part;      // [hq][parts][offsets] partial bias gradients
   int parts;
+  float* tab2;      // [hq][offsets] the bias by offset, in units of log2
+  int* status;      // device check word
 };
 cudaError_t window_plan(const int32_t* coords, int64_t N, int m, const ssa_partition* win, int2* rows, int4* tiles,
                         int* status, cudaStream_t st);
@@ -181,6 +183,9 @@ cudaError_t window_plan(const int32_t* coords, int64_t N, int m, const ssa_parti
 int window_parts(int hq, int64_t T, int m);
 cudaError_t window_fwd_simt(const WinArgs& a, cudaStream_t st);
 cudaError_t window_bwd_simt(const WinArgs& a, cudaStream_t st);
+// bf16 on warp-level MMAs
+cudaError_t window_fwd_mma(const WinArgs& a, cudaStream_t st);
+cudaError_t window_bwd_mma(const WinArgs& a, cudaStream_t st);
 // Sums of the partial bias gradients by bucket; gradients of lam from D.
 cudaError_t window_param_grads(const WinArgs& a, cudaStream_t st);
 cudaError_t act8_pack(int dtype, int64_t rows, int d, const void* x, int8_t* codes, float* scale, cudaStream_t st);
