@@ -378,7 +378,7 @@ SSA_API ssa_status ssa_sp_backward(const ssa_params* p, int32_t S, int64_t N, co
 
 /* The largest window edge a relative position bias can have ((2*16-1)^3 offsets). */
 #define SSA_WINDOW_MAX_EDGE 16
-/* Rows of the plan's tiles: tiles holds n / SSA_WINDOW_TILE + count entries. */
+/* Rows of the plan's tiles: tiles holds n / SSA_WINDOW_TILE + count + 1 entries. */
 #define SSA_WINDOW_TILE 16
 
 /*
@@ -387,9 +387,10 @@ SSA_API ssa_status ssa_sp_backward(const ssa_params* p, int32_t S, int64_t N, co
  */
 typedef struct ssa_win_plan {
   int32_t* rows;   /* [n, 2] in cell order: the token and its offset code */
-  int32_t* tiles;  /* [n / SSA_WINDOW_TILE + count, 4]: up to 16 rows of one cell: first row, rows
+  int32_t* tiles;  /* [n / SSA_WINDOW_TILE + count + 1, 4]: up to 16 rows of one cell: first row, rows
                       (+ 65536 where the cell holds two tokens in one voxel), the cell's first and
-                      end row; unused entries hold zeros */
+                      end row; unused entries hold zeros; the last entry: the most tokens that one
+                      voxel of a cell holds, and three zeros */
   int64_t n;       /* out: tokens */
   int64_t count;   /* out: cells of the partition */
   int32_t m;       /* out: window edge of the codes, 0 without coordinates */

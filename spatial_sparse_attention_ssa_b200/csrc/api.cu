@@ -731,7 +731,7 @@ ssa_status check_window(const ssa_window_params* p, const ssa_win_plan* plan, in
     return SSA_ERR_INVALID_ARG;
   if (p->d != 32 && p->d != 64 && (p->d != 128 || maps == 2)) return SSA_ERR_UNSUPPORTED;
   if (p->hq > 65535) return SSA_ERR_UNSUPPORTED;
-  if (plan->n / SSA_WINDOW_TILE + plan->count > INT32_MAX) return SSA_ERR_UNSUPPORTED;
+  if (plan->n / SSA_WINDOW_TILE + plan->count >= INT32_MAX) return SSA_ERR_UNSUPPORTED;
   if (plan->n > 0 && (plan->count < 1 || !plan->rows || !plan->tiles || !aligned16(plan->rows) || !aligned16(plan->tiles)))
     return SSA_ERR_INVALID_ARG;
   return SSA_OK;
@@ -777,18 +777,24 @@ size_t carve_window(void* base, const ssa_window_params* p, const ssa_win_plan* 
   Carver c(base);
   const int e = 2 * plan->m - 1;
   const int64_t T = plan->n / SSA_WINDOW_TILE + plan->count;
-  const int parts = ssa::window_parts(p->hq, T, plan->m);
+  const int wide = p->dtype == SSA_DTYPE_BF16 && plan->m >= ssa::kWideEdge;
+  const int parts = wide ? 1 : ssa::window_parts(p->hq, T, plan->m);
   float* lse2 = c.take<float>((size_t)p->hq * plan->n);
   float* D = c.take<float>((size_t)p->hq * plan->n);
   const size_t tab = maps == 1 && plan->m > 0 ? (size_t)p->hq * e * e * e : 0;
   float* part = c.take<float>(tab * parts);
-  float* tab2 = c.take<float>(tab);
+  float* tab2 = c.take<float>(tab ? tab + 3 * (size_t)p->hq : 0);  // rows of a multiple of 4
+  unsigned* amax = c.take<unsigned>(p->hq);
+  unsigned long long* sums = c.take<unsigned long long>(wide ? tab : 0);
   if (a) {
     a->lse2 = lse2;
     a->D = D;
     a->part = part;
     a->parts = parts;
     a->tab2 = tab2;
+    a->amax = amax;
+    a->wide = wide;
+    a->sums = sums;
   }
   return c.used;
 }
@@ -821,8 +827,6 @@ ssa_status window_backward(const ssa_window_params* p, const ssa_win_plan* plan,
   a.dv = dv;
   a.dbias = dbias;
   a.dlam = dlam;
-  a.status = status_ptr();
-  if (!a.status) return SSA_ERR_CUDA;
   cudaError_t e = a.dtype == SSA_DTYPE_BF16 ? ssa::window_bwd_mma(a, st) : ssa::window_bwd_simt(a, st);
   if (e == cudaSuccess) e = ssa::window_param_grads(a, st);
   return cuda_status(e);
@@ -837,7 +841,7 @@ SSA_API ssa_status ssa_window_plan(const int32_t* coords, int64_t N, int32_t m, 
   if (!plan || N < 0 || N > INT32_MAX - 1 || (coords && m < 1) || !partition_ok(win, N)) return SSA_ERR_INVALID_ARG;
   if (coords && m > SSA_WINDOW_MAX_EDGE) return SSA_ERR_UNSUPPORTED;
   if (win->count > N || (N > 0 && win->count < 1)) return SSA_ERR_INVALID_ARG;
-  if (N / SSA_WINDOW_TILE + win->count > INT32_MAX) return SSA_ERR_UNSUPPORTED;
+  if (N / SSA_WINDOW_TILE + win->count >= INT32_MAX) return SSA_ERR_UNSUPPORTED;
   if (N > 0 && (!plan->rows || !plan->tiles || !aligned16(plan->rows) || !aligned16(plan->tiles)))
     return SSA_ERR_INVALID_ARG;
   plan->n = N;

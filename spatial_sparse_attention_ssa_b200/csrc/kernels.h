@@ -155,7 +155,7 @@ struct WinArgs {
   float scale;
   int64_t N;
   const int2* rows;   // [N] token, code in cell order
-  const int4* tiles;  // [T] first row, rows (+ flag), cell begin, cell end
+  const int4* tiles;  // [T] first row, rows (+ flag), cell begin, cell end; [T].x: most tokens of a voxel
   int T, m;
   const float* table;  // bias [hq, nb], or null
   const int32_t* bucket;
@@ -175,10 +175,15 @@ struct WinArgs {
   float* part;      // [hq][parts][offsets] partial bias gradients
   int parts;
   float* tab2;      // [hq][offsets] the bias by offset, in units of log2
-  int* status;      // device check word
+  unsigned* amax;   // [hq] the largest |dP| of a head, as bits
+  int wide;         // bf16 and an edge from kWideEdge on: one part, summed in `sums`
+  unsigned long long* sums;  // [hq][offsets]
 };
 cudaError_t window_plan(const int32_t* coords, int64_t N, int m, const ssa_partition* win, int2* rows, int4* tiles,
                         int* status, cudaStream_t st);
+// Window edges from here on keep the bias gradient of the bf16 kernels in global memory: 8 bytes per
+// offset are 157 KB, too many beside a team's rows in shared memory.
+constexpr int kWideEdge = 14;
 // Partial bias gradients per head that the backward keeps (rows of `part`).
 int window_parts(int hq, int64_t T, int m);
 cudaError_t window_fwd_simt(const WinArgs& a, cudaStream_t st);

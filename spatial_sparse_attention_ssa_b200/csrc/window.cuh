@@ -24,6 +24,8 @@ constexpr int kDupFlag = 65536;         // tiles[].y: two tokens of the cell sha
 
 // Offsets of a window of edge m, and the number of the offset 0.
 __host__ __device__ inline int offsets(int m) { return (2 * m - 1) * (2 * m - 1) * (2 * m - 1); }
+// Floats from one head's table of offsets to the next in WinArgs::tab2.
+__host__ __device__ inline int table_pitch(int m) { return (offsets(m) + 3) & ~3; }
 __host__ __device__ inline int center(int m) { return (m - 1) * ((2 * m - 1) * (2 * m - 1) + (2 * m - 1) + 1); }
 
 // 2^x (x <= 0 here, or minus infinity, or NaN).

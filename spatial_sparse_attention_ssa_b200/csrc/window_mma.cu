@@ -1,19 +1,14 @@
 // Attention inside the cells on warp-level tensor-core MMAs (mma.sync m16n8k16, bf16 operands,
 // fp32 sums).  See window.cuh for the mathematics and the meaning of MAPS.
 //
-// A warp works alone on 16 rows of a cell and one head.  All operands go from global memory
-// (in practice L1: the warps of a CTA take neighbouring tiles, so they share a cell's keys)
-// straight into MMA fragments, with 16-byte loads and without shared memory:
-//   * a contraction over the head dim does not care about the order of the dim, as long as both
-//     operands agree, so thread (g, t) of the fragment (g = lane / 4, t = lane % 4) takes dims
-//     32 c + 8 t .. + 7 of its row as its elements of the steps 2c and 2c + 1;
-//   * a contraction over keys wants two keys in one register.  The thread loads dims 8 g .. + 7 of
-//     the keys 2t, 2t + 1, 2t + 8, 2t + 9 and pairs them with byte permutes; column g of the n-tile e
-//     is then dim 8 g + e, and a thread's accumulators are 16 consecutive dims of its rows.
-// A cell is walked in chunks of 64 keys whose scores stay in registers.  The cells of surface
-// voxels hold some 60 tokens (windows of edge 8), so most have one chunk: nothing is recomputed
-// or rescaled.  Tiles of 128 rows (tcgen05) would stand half empty on such cells and hand every
-// score through TMEM; the warps here need no barrier at all.
+// A team of TW warps takes a cell and a head: it stages the cell's keys (64 at a time) in shared
+// memory once, and its warps walk the cell's rows 16 at a time.  The cells of surface voxels hold
+// some 60 tokens (windows of edge 8), so most have one chunk of keys whose scores stay in
+// registers: nothing is recomputed or rescaled.  Tiles of 128 rows (tcgen05) would stand half
+// empty on such cells and hand every score through TMEM; here the scores never leave registers
+// and nothing but the team waits on a barrier.  What bounds these kernels is instruction issue:
+// the softmax, the bias and the masks of a score take some eight times as many issue slots as
+// its products.
 #include "tc.cuh"
 #include "window.cuh"
 
@@ -34,6 +29,45 @@ __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, ui
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// four 8x8 b16 matrices; lane l gives the address of row l % 8 of matrix l / 8
+__device__ __forceinline__ void ldsm(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void stsm(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0), "r"(r1),
+               "r"(r2), "r"(r3)
+               : "memory");
+}
+// 16 bytes to shared memory, zeros where `on` is off
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t dst, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(src)
+               : "memory");
+  return v;
+}
 
 // Four 8-bit codes (as in an int) to bf16 values times s: the byte + 128 in the low mantissa bits
 // of 2^23 is an exact float, so are the difference and the product with a power of two.
@@ -46,158 +80,120 @@ __device__ __forceinline__ uint2 codes4(uint32_t w, float s) {
   return make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
 }
 
-// Rows of one tensor, [n, heads, D]; a row of W = MAPS * D values starts at head `head`.
+// Rows of a tensor [n, heads, D] from head `head` on.
 template <typename E, int D>
 struct Rows {
   const E* p;
   const float* s;  // row scales (8-bit rows)
   int heads, head;
-  __device__ __forceinline__ size_t at(int tok) const { return (size_t)tok * heads + head; }
-  // 8 (4) values from column `col` of row `r`
-  __device__ __forceinline__ uint4 ld8(size_t r, int col) const {
-    if constexpr (sizeof(E) == 2) {
-      return __ldg(reinterpret_cast<const uint4*>(p + r * D + col));
-    } else {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(p + r * D + col));
-      const float f = __ldg(s + r + col / D);
-      const uint2 a = codes4(w.x, f), b = codes4(w.y, f);
-      return make_uint4(a.x, a.y, b.x, b.y);
-    }
-  }
-  __device__ __forceinline__ uint2 ld4(size_t r, int col) const {
-    if constexpr (sizeof(E) == 2) {
-      return __ldg(reinterpret_cast<const uint2*>(p + r * D + col));
-    } else {
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p + r * D + col));
-      return codes4(w, __ldg(s + r + col / D));
-    }
-  }
 };
 
-// A operand: 16 rows (tokens tg for row g, tg8 for row g + 8; zeros where the flag is off).
-template <int W, typename R>
-__device__ __forceinline__ void load_a(const R& src, int tg, bool vg, int tg8, bool vg8, uint32_t (*f)[4]) {
-  const int t = threadIdx.x & 3;
-  const size_t r0 = src.at(tg), r1 = src.at(tg8);
-#pragma unroll
-  for (int c = 0; c < W / 32; ++c) {
-    const uint4 z = make_uint4(0, 0, 0, 0);
-    const uint4 x = vg ? src.ld8(r0, 32 * c + 8 * t) : z, y = vg8 ? src.ld8(r1, 32 * c + 8 * t) : z;
-    f[2 * c][0] = x.x, f[2 * c][1] = y.x, f[2 * c][2] = x.y, f[2 * c][3] = y.y;
-    f[2 * c + 1][0] = x.z, f[2 * c + 1][1] = y.z, f[2 * c + 1][2] = x.w, f[2 * c + 1][3] = y.w;
+// Shared-memory tiles of rows of W bf16 (16-byte units c): the unit's place is permuted by the row
+// so that eight rows of one unit (ldmatrix) fall into different banks.
+template <int W>
+__device__ __forceinline__ uint32_t unit(int row, int c) {
+  constexpr int U = W / 8;
+  const int f = W == 32 ? (row >> 1) & 3 : row & 7;
+  return 16u * (uint32_t)(row * U + (c ^ f));
+}
+
+// Unit c of a row to row r of a staged tile, zeros where `on` is off; asynchronous for bf16
+// (cp_commit and cp_wait are the caller's).
+template <int D, int W, typename E>
+__device__ __forceinline__ void put(uint32_t dst, const Rows<E, D>& src, int r, int c, size_t row, bool on) {
+  if constexpr (sizeof(E) == 2) {
+    cp16(dst + unit<W>(r, c), src.p + row * D + 8 * c, on);
+  } else {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (on) {
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(src.p + row * D + 8 * c));
+      const float f = __ldg(src.s + row + 8 * c / D);
+      const uint2 x = codes4(w.x, f), y = codes4(w.y, f);
+      v = make_uint4(x.x, x.y, y.x, y.y);
+    }
+    sts16(dst + unit<W>(r, c), v);
   }
 }
 
-// s[j] = A B^T for the n-tiles j < NT: column g of n-tile j is the row whose token lane 8 j + g of
-// `tok` holds (32 rows per register).  Only 8-row tiles below n are computed, the others are 0.
-template <int W, int NT, typename R>
-__device__ __forceinline__ void contract_dim(const uint32_t (*a)[4], const R& src, const int* tok, int n,
-                                             float (*s)[4]) {
-  constexpr int B = W >= 128 ? 2 : 4;  // n-tiles in flight
-  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+// Rows first .. first + n - 1 of the cell order to a tile of `total` rows (zeros past n), by
+// `threads` threads.
+template <int D, int W, typename E>
+__device__ __forceinline__ void stage(uint32_t dst, const Rows<E, D>& src, const int2* __restrict__ rows, int first,
+                                      int n, int total, int tid, int threads) {
+  constexpr int U = W / 8;
+  for (int i = tid; i < total * U; i += threads) {
+    const int r = i / U;
+    const size_t row = (size_t)__ldg(&rows[first + min(r, n - 1)].x) * src.heads + src.head;
+    put<D, W>(dst, src, r, i % U, row, r < n);
+  }
+}
+
+// A operand, k-step k, from a tile of 16 rows starting at row r0 of a staged tile.
+template <int W>
+__device__ __forceinline__ void load_a(uint32_t* f, uint32_t tile, int r0, int k) {
+  const int lane = threadIdx.x & 31;
+  ldsm(f, tile + unit<W>(r0 + (lane & 15), 2 * k + (lane >> 4)));
+}
+
+// s[2 k], s[2 k + 1] = A B^T for the 16 rows 16 k .. of B, k < NK: W columns from unit u0 of a
+// staged tile of PW columns.
+template <int PW, int W, int NK>
+__device__ __forceinline__ void contract_dim(const uint32_t (*a)[4], uint32_t tile, int u0, float (*s)[4]) {
+  const int lane = threadIdx.x & 31, row = (lane & 7) + ((lane >> 4) << 3), c = (lane >> 3) & 1;
 #pragma unroll
-  for (int j0 = 0; j0 < NT; j0 += B) {
+  for (int k = 0; k < NK; ++k) {
 #pragma unroll
-    for (int j = j0; j < j0 + B; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-    if (8 * j0 < n) {
-      uint4 b[B][W / 32];
+    for (int x = 0; x < 4; ++x) s[2 * k][x] = s[2 * k + 1][x] = 0.f;
 #pragma unroll
-      for (int j = 0; j < B; ++j) {
-        const size_t r = src.at(__shfl_sync(kFull, tok[(j0 + j) / 4], (8 * (j0 + j) + g) & 31));
-#pragma unroll
-        for (int c = 0; c < W / 32; ++c) b[j][c] = src.ld8(r, 32 * c + 8 * t);
-      }
-#pragma unroll
-      for (int c = 0; c < W / 32; ++c)
-#pragma unroll
-        for (int j = 0; j < B; ++j) {
-          mma(s[j0 + j], a[2 * c], b[j][c].x, b[j][c].y);
-          mma(s[j0 + j], a[2 * c + 1], b[j][c].z, b[j][c].w);
-        }
+    for (int d = 0; d < W / 16; ++d) {
+      uint32_t b[4];
+      ldsm(b, tile + unit<PW>(16 * k + row, u0 + 2 * d + c));
+      mma(s[2 * k], a[d], b[0], b[1]);
+      mma(s[2 * k + 1], a[d], b[2], b[3]);
     }
   }
 }
 
-// acc += P B, P as A fragments over NG groups of 16 rows of B; rows from n on count as zeros.
-template <int W, int NG, typename R>
-__device__ __forceinline__ void contract_rows(const uint32_t (*p)[4], const R& src, const int* tok, int n,
-                                              float (*acc)[4]) {
-  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+// acc += P B, P as A fragments over NK groups of 16 rows of B (as above).
+template <int PW, int W, int NK>
+__device__ __forceinline__ void contract_rows(const uint32_t (*p)[4], uint32_t tile, int u0, float (*acc)[4]) {
+  const int lane = threadIdx.x & 31, row = lane & 15, c = lane >> 4;
 #pragma unroll
-  for (int k = 0; k < NG; ++k) {
-    if (16 * k < n) {
-      size_t r[4];
-      bool v[4];
+  for (int k = 0; k < NK; ++k) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = 16 * k + 2 * t + (i & 1) + 8 * (i >> 1);
-        r[i] = src.at(__shfl_sync(kFull, tok[k / 2], key & 31));
-        v[i] = key < n;
-      }
-      if constexpr (W == 32) {
-        uint2 x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = v[i] ? src.ld4(r[i], 4 * g) : make_uint2(0, 0);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t sel = e & 1 ? 0x7632 : 0x5410;
-          mma(acc[e], p[k], __byte_perm(e < 2 ? x[0].x : x[0].y, e < 2 ? x[1].x : x[1].y, sel),
-              __byte_perm(e < 2 ? x[2].x : x[2].y, e < 2 ? x[3].x : x[3].y, sel));
-        }
-      } else {
-#pragma unroll
-        for (int h = 0; h < W / 64; ++h) {
-          uint4 x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = v[i] ? src.ld8(r[i], 64 * h + 8 * g) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4][4] = {{x[0].x, x[0].y, x[0].z, x[0].w},
-                                    {x[1].x, x[1].y, x[1].z, x[1].w},
-                                    {x[2].x, x[2].y, x[2].z, x[2].w},
-                                    {x[3].x, x[3].y, x[3].z, x[3].w}};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t sel = e & 1 ? 0x7632 : 0x5410;
-            mma(acc[8 * h + e], p[k], __byte_perm(w[0][e / 2], w[1][e / 2], sel),
-                __byte_perm(w[2][e / 2], w[3][e / 2], sel));
-          }
-        }
-      }
+    for (int e = 0; e < W / 16; ++e) {
+      uint32_t b[4];
+      ldsm_t(b, tile + unit<PW>(16 * k + row, u0 + 2 * e + c));
+      mma(acc[2 * e], p[k], b[0], b[1]);
+      mma(acc[2 * e + 1], p[k], b[2], b[3]);
     }
   }
 }
 
-// Accumulators of contract_rows to rows (token tg / tg8 where the flags are on), times mul / mul8.
+// Accumulators (16 rows of W) times f (rows g) and f8 (rows g + 8), rounded to bf16, through the
+// warp's scratch tile to rows first .. first + nr - 1.
 template <int D, int W>
-__device__ __forceinline__ void store_acc(bf16* out, int heads, int head, int tg, bool vg, int tg8, bool vg8,
-                                          float (*acc)[4], float mul, float mul8) {
-  const int t = threadIdx.x & 3;
+__device__ __forceinline__ void store_acc(uint32_t scratch, float (*acc)[4], float f, float f8, bf16* out, int heads,
+                                          int head, const int2* __restrict__ rows, int first, int nr) {
+  constexpr int U = W / 8;
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (!(i ? vg8 : vg)) continue;
-    const float f = i ? mul8 : mul;
-    bf16* p = out + ((size_t)(i ? tg8 : tg) * heads + head) * D;
-    if constexpr (W == 32) {
-      uint32_t w[4];
+  for (int e = 0; e < W / 16; ++e)
+    stsm(scratch + unit<W>(lane & 15, 2 * e + (lane >> 4)), pack_bf16x2(acc[2 * e][0] * f, acc[2 * e][1] * f),
+         pack_bf16x2(acc[2 * e][2] * f8, acc[2 * e][3] * f8), pack_bf16x2(acc[2 * e + 1][0] * f, acc[2 * e + 1][1] * f),
+         pack_bf16x2(acc[2 * e + 1][2] * f8, acc[2 * e + 1][3] * f8));
+  __syncwarp();
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        w[x] = pack_bf16x2(acc[2 * (x & 1)][2 * i + x / 2] * f, acc[2 * (x & 1) + 1][2 * i + x / 2] * f);
-      *reinterpret_cast<uint4*>(p + 8 * t) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-#pragma unroll
-      for (int h = 0; h < W / 64; ++h)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t w[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            w[x] = pack_bf16x2(acc[8 * h + 2 * x][2 * i + c] * f, acc[8 * h + 2 * x + 1][2 * i + c] * f);
-          *reinterpret_cast<uint4*>(p + 64 * h + 16 * t + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-    }
+  for (int i = 0; i < U / 2; ++i) {
+    const int r = (32 * i + lane) / U, c = (32 * i + lane) % U;
+    if (r < nr)
+      *reinterpret_cast<uint4*>(out + ((size_t)__ldg(&rows[first + r].x) * heads + head) * D + 8 * c) =
+          lds16(scratch + unit<W>(r, c));
   }
 }
 
-// Scores of 8 n-tiles as A fragments of 4 groups of 16 (rounded to bf16).
+// Scores of NT n-tiles as A fragments (rounded to bf16).
 template <int NT>
 __device__ __forceinline__ void pack_a(float (*s)[4], uint32_t (*f)[4]) {
 #pragma unroll
@@ -218,436 +214,550 @@ __device__ __forceinline__ float quad_sum(float x) {
   return x + __shfl_xor_sync(kFull, x, 2);
 }
 
-// The 64 keys of a chunk: lane l holds the tokens and codes of keys l and 32 + l (those past the
-// end repeat the last one).
-struct Keys {
-  int tok[2], code[2], n;
-  __device__ __forceinline__ void load(const int2* __restrict__ rows, int k0, int hi) {
-    const int lane = threadIdx.x & 31;
-    n = min(kChunk, hi - k0);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int2 r = __ldg(&rows[k0 + min(32 * i + lane, n - 1)]);
-      tok[i] = r.x;
-      code[i] = r.y;
-    }
+// The bias gradient in fixed point.  A CTA keeps two whole numbers per offset: dS 2^s rounded, and
+// what that rounding left times 2^k, rounded; both are added by native integer atomics in shared
+// memory, whose order cannot change the sums.  Bounds: the |dS| of a row sum to at most 2 M, M the
+// largest |dP| of the head (window statistics, a.amax), so 2^s <= 2^30 / (2 M rows) keeps the first;
+// each remainder is at most 1/2, so 2^k <= 2^31 / (adds per offset) keeps the second, adds = rows times
+// the most tokens that one voxel holds (a.tiles[T].x).  With 2^13 rows the unit is M 2^-34: the table
+// is as exact as fp32 sums.  A NaN or an infinity in dP or in a softmax makes the head's gradient NaN.
+struct Limbs {
+  float s, k, unit;  // 2^s, 2^k, 2^-s
+  int kbits;
+  __device__ __forceinline__ void set(const WinArgs& a, int h) {
+    static_assert(SSA_WINDOW_TILE == 16, "rows of a slot");
+    const uint32_t bits = __ldg(a.amax + h);
+    // rows of a CTA: its share of the slots (up to one more for each of its teams), each of which
+    // can be a cell of one chunk
+    const int64_t slots = (a.T + (int64_t)gridDim.x - 1) / gridDim.x + 8;
+    const int64_t rows = min((int64_t)a.N, slots * kChunk), adds = rows * max(1, __ldg(&a.tiles[a.T].x));
+    const int rb = 64 - __clzll(rows), ab = 64 - __clzll(adds);  // rows < 2^rb, adds < 2^ab
+    const int e = (int)(bits >> 23) - 126;                       // M < 2^e
+    int sb = min(30 - rb - 1 - e, 20 - e);                       // |dS 2^s| < 2^22: see add()
+    sb = max(-100, min(100, sb));
+    kbits = max(0, min(18, 30 - ab));
+    s = __uint_as_float(bits >= 0x7f800000u ? 0x7fc00000u : (uint32_t)(sb + 127) << 23);
+    k = (float)(1 << kbits);
+    unit = 1.f / s;
+  }
+  __device__ __forceinline__ float value(int hi, int lo) const {
+    return (float)(((double)hi + (double)lo / (double)(1 << kbits)) * (double)unit);
+  }
+  // x 2^s to the nearest whole number by adding 1.5 2^23 (|x 2^s| < 2^22), and the rest
+  __device__ __forceinline__ void add(int* hi, int* lo, float x) const {
+    constexpr float kMagic = 12582912.f;
+    const float a = fmaf(x, s, kMagic);
+    const float r = fmaf(x, s, kMagic - a);
+    const float b = fmaf(r, k, kMagic);
+    atomicAdd(hi, __float_as_int(a) - __float_as_int(kMagic));
+    atomicAdd(lo, __float_as_int(b) - __float_as_int(kMagic));
   }
 };
 
-// s = s mul + bias in units of log2, minus infinity from key n on.  tab: the head's table by
-// offset (shared or global memory); ci, ci8: codes of rows g, g + 8 plus the center.
+// Edges whose two tables do not fit beside a team keep one 64-bit number per offset in global
+// memory: dS 2^s with 2^s <= 2^61 / (2 M N).
+__host__ __device__ inline int wide_bits(uint32_t amax, int64_t N) {
+  int rb = 0;
+  while (rb < 62 && (int64_t(1) << rb) <= N) ++rb;  // N < 2^rb
+  const int sb = 61 - rb - 1 - ((int)(amax >> 23) - 126);
+  return sb < -100 ? -100 : sb > 100 ? 100 : sb;
+}
+struct Wide {
+  unsigned long long* sums;  // of the head
+  double s;
+  __device__ __forceinline__ void set(const WinArgs& a, int h) {
+    sums = a.sums + (size_t)h * offsets(a.m);
+    s = (double)__uint_as_float((uint32_t)(wide_bits(__ldg(a.amax + h), a.N) + 127) << 23);
+  }
+  __device__ __forceinline__ void add(int at, float x) const {
+    atomicAdd(sums + at, (unsigned long long)__double2ll_rn((double)x * s));
+  }
+};
+
+// limbs[code of row - code of key] += dS of a fragment tile of 16 rows and 32 positions.
+template <typename F>
+__device__ __forceinline__ void add_bias_grad(const F& add, float (*ds)[4], const int* codes, int ci, int ci8, int left,
+                                              int nr) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const bool r0 = g < nr, r8 = g + 8 < nr;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int2 cj = *reinterpret_cast<const int2*>(codes + 8 * j + 2 * t);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int at = (x & 2 ? ci8 : ci) - (x & 1 ? cj.y : cj.x);
+      if ((x & 2 ? r8 : r0) && 8 * t + 2 * j + (x & 1) < left) add(at, ds[j][x]);
+    }
+  }
+}
+
+// The keys of a chunk stand in shared memory in another order than in the cell: position
+// 8 j + 2 t + x of 32 holds key 8 t + 2 j + x, so that the four lanes that share a row in a
+// fragment (t) hold keys eight apart.  Neighbours in the cell are neighbours in the voxel grid, so
+// without this such lanes would often hit one offset in one instruction (see add_bias_grad).
+__device__ __forceinline__ int key_at(int p) { return (p & 33) | (p & 6) << 2 | (p & 24) >> 2; }
+
+// Rows first .. first + n - 1 of the cell order to a tile of 64 keys in that order.
+template <int D, int W, typename E>
+__device__ __forceinline__ void stage_keys(uint32_t dst, const Rows<E, D>& src, const int2* __restrict__ rows, int first,
+                                           int n, int tid, int threads) {
+  constexpr int U = W / 8;
+  const int total = n > 32 ? kChunk : 32;
+  for (int i = tid; i < total * U; i += threads) {
+    const int p = i / U, c = i % U, k = key_at(p);
+    const size_t row = (size_t)__ldg(&rows[first + min(k, n - 1)].x) * src.heads + src.head;
+    put<D, W>(dst, src, p, c, row, k < n);
+  }
+}
+
+// s = s mul + bias in units of log2 for the 32 positions of a half chunk, minus infinity where
+// the key is not below `left`.  t0, t8: the head's table of offsets at the codes of rows g, g + 8
+// (plus the center); codes: of the positions (shared memory).
 template <bool BIAS>
-__device__ __forceinline__ void finish_scores(float (*s)[4], const Keys& k, float mul, const float* tab, int ci,
-                                              int ci8) {
+__device__ __forceinline__ void finish_scores(float (*s)[4], const int* codes, int left, float mul, const float* t0,
+                                              const float* t8) {
   const int t = threadIdx.x & 3;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int key = 8 * j + 2 * t + x;
-      float b0 = 0.f, b1 = 0.f;
-      if constexpr (BIAS) {
-        const int cj = __shfl_sync(kFull, k.code[j / 4], key & 31);
-        b0 = tab[ci - cj];
-        b1 = tab[ci8 - cj];
-      }
-      s[j][x] = key < k.n ? fmaf(s[j][x], mul, b0) : kNegInf;
-      s[j][2 + x] = key < k.n ? fmaf(s[j][2 + x], mul, b1) : kNegInf;
+  for (int j = 0; j < 4; ++j) {
+    float b[4] = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (BIAS) {
+      const int2 cj = *reinterpret_cast<const int2*>(codes + 8 * j + 2 * t);
+      b[0] = t0[-cj.x], b[1] = t0[-cj.y], b[2] = t8[-cj.x], b[3] = t8[-cj.y];
     }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) s[j][x] = fmaf(s[j][x], mul, b[x]);
+  }
+  if (left < 32) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s[j][x] = 8 * t + 2 * j + (x & 1) < left ? s[j][x] : kNegInf;
   }
 }
 
-// ---------------------------------------------------------------------------
-// forward
-// ---------------------------------------------------------------------------
+template <int TW>
+__device__ __forceinline__ void team_sync(int team) {
+  if constexpr (TW == 1)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(TW * 32) : "memory");
+}
 
-constexpr int kFwdWarps = 8;
+// Rows of a cell that the team of a tile slot takes: all of them where the cell has one chunk of
+// keys (from its first tile; the other slots have nothing to do), else TW tiles from every TW-th.
+// Returns the number of tiles, 0 for none.
+template <int TW>
+__device__ __forceinline__ int team_tiles(const int4& tile) {
+  if ((tile.y & (kDupFlag - 1)) == 0) return 0;
+  const int at = (tile.x - tile.z) / kTile, all = (tile.w - tile.z + kTile - 1) / kTile;
+  if (tile.w - tile.z <= kChunk) return at == 0 ? all : 0;
+  return at % TW == 0 ? min(TW, all - at) : 0;
+}
 
-template <int D, int MAPS, bool BIAS>
-__global__ void __launch_bounds__(32 * kFwdWarps, D == 128 || (MAPS == 2 && D == 64) ? 1 : 2)
-    window_fwd_mma_kernel(WinArgs a) {
-  constexpr int DV = MAPS * D;
-  extern __shared__ float tab_s[];
+// What a walk over the rows does with the keys.
+enum { kForward, kStats, kDq };
+
+// A team's shared memory: the staged keys and values (the maps side by side), the keys' codes; a
+// warp's: a scratch tile of 16 rows, and one more in the backward (dO).
+template <int D, int MAPS, int MODE>
+struct Shape {
+  static constexpr int DV = MAPS * D;
+  static constexpr int TW = DV == 128 ? 4 : 2;
+  static constexpr int V = kChunk * DV * 2;  // offset of the values, bytes
+  static constexpr int codes = 2 * V;        // offset of the codes
+  static constexpr int team = codes + kChunk * 4;
+  static constexpr int scratch = kTile * DV * 2;
+  static constexpr int warp = MODE == kForward ? scratch : 2 * scratch;
+  static constexpr int per_team = team + TW * warp;
+  // teams of a CTA at most, CTAs per SM: what registers and shared memory leave.  dq keeps three
+  // tables per CTA, so it takes one large CTA.
+  static constexpr int teams = MODE == kDq ? (DV == 128 ? 2 : 7) : DV == 128 ? 1 : 4;
+  static constexpr int resident = MODE == kDq ? 1 : DV == 128 && MODE == kForward ? 3 : 2;
+};
+
+// One kernel body for the forward, the row statistics of the backward, and dq with the bias
+// gradient: they share the walk over cells, keys and scores.  TAB: where the bias is read: 0 no
+// bias, 1 shared memory, 2 global memory.  E: type of q, k, v.
+template <int D, int MAPS, int TAB, typename E, int MODE>
+__global__ void __launch_bounds__(32 * Shape<D, MAPS, MODE>::TW* Shape<D, MAPS, MODE>::teams,
+                                  Shape<D, MAPS, MODE>::resident) window_rows_kernel(WinArgs a) {
+  using S = Shape<D, MAPS, MODE>;
+  constexpr int DV = S::DV, TW = S::TW;
+  constexpr bool BIAS = TAB != 0;
+  const int NT = (int)blockDim.x / (32 * TW);
+  extern __shared__ __align__(128) char sm[];
   const int h = blockIdx.y, hk = h / (a.hq / a.hkv);
   const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3, warp = threadIdx.x >> 5;
+  const int team = warp / TW, wt = warp % TW, tid = threadIdx.x % (32 * TW);
+  const int T3 = BIAS ? offsets(a.m) : 0, c0 = BIAS ? center(a.m) : 0;
+  const bool grad = MODE == kDq && BIAS && a.dbias;
+  int* limbs = reinterpret_cast<int*>(sm + NT * S::per_team);  // [2][T3] with a bias gradient, not wide
+  float* tab_s = reinterpret_cast<float*>(limbs + (grad && TAB != 3 ? 2 * T3 : 0));
+  const float* tab = TAB >= 2 ? a.tab2 + (size_t)h * table_pitch(a.m) : tab_s;
+  char* mine = sm + team * S::team;
+  const uint32_t keys = tc::smem_u32(mine), vals = keys + S::V;
+  const uint32_t scratch = tc::smem_u32(sm + NT * S::team + warp * S::warp), scratch2 = scratch + S::scratch;
+  int* codes = reinterpret_cast<int*>(mine + S::codes);
   const float mul = a.scale * kLog2e;
-  const int c0 = BIAS ? center(a.m) : 0;
   if constexpr (BIAS) {
-    for (int i = threadIdx.x; i < offsets(a.m); i += blockDim.x) tab_s[i] = bias2_at(a, h, i);
+    if (TAB == 1)
+      for (int i = threadIdx.x; i < T3; i += blockDim.x) tab_s[i] = bias2_at(a, h, i);
+    if (grad && TAB != 3)
+      for (int i = threadIdx.x; i < 2 * T3; i += blockDim.x) limbs[i] = 0;
     __syncthreads();
   }
+  Limbs fx;
+  Wide wide;
+  if (grad && TAB != 3) fx.set(a, h);
+  if (grad && TAB == 3) wide.set(a, h);
   float lam = 0.f;
   if constexpr (MAPS == 2) {
     float e1, e2;
     lambda_terms<D>(a.lam, a.hq / 2, h, e1, e2);
     lam = e1 - e2 + a.lam_init;
   }
-  const Rows<bf16, D> V = {static_cast<const bf16*>(a.v), nullptr, a.hkv, MAPS * hk};
-  for (int t = blockIdx.x * kFwdWarps + warp; t < a.T; t += gridDim.x * kFwdWarps) {
+  const Rows<E, D> Q = {static_cast<const E*>(a.q), a.sq, a.hq, MAPS * h};
+  const Rows<E, D> K = {static_cast<const E*>(a.k), a.sk, a.hkv, MAPS * hk};
+  const Rows<E, D> V = {static_cast<const E*>(a.v), a.sv, a.hkv, MAPS * hk};
+  const Rows<bf16, D> O = {static_cast<const bf16*>(a.dout), nullptr, a.hq, MAPS * h};
+  uint32_t top = 0;  // the largest |dP|, as bits: NaN above all
+  for (int t = blockIdx.x * NT + team; t < a.T; t += gridDim.x * NT) {
     const int4 tile = __ldg(&a.tiles[t]);
-    const int first = tile.x, nr = tile.y & (kDupFlag - 1), lo = tile.z, hi = tile.w;
-    if (nr == 0) continue;
-    const bool vg = g < nr, vg8 = g + 8 < nr;
-    const int2 rg = __ldg(&a.rows[first + min(g, nr - 1)]), rg8 = __ldg(&a.rows[first + min(g + 8, nr - 1)]);
-    uint32_t q[MAPS][D / 16][4];
-#pragma unroll
-    for (int u = 0; u < MAPS; ++u) {
-      const Rows<bf16, D> Q = {static_cast<const bf16*>(a.q), nullptr, a.hq, MAPS * h + u};
-      load_a<D>(Q, rg.x, vg, rg8.x, vg8, q[u]);
-    }
-    float m[MAPS][2], l[MAPS][2], acc[DV / 8][4];
-#pragma unroll
-    for (int u = 0; u < MAPS; ++u) m[u][0] = m[u][1] = kNegInf, l[u][0] = l[u][1] = 0.f;
-#pragma unroll
-    for (int e = 0; e < DV / 8; ++e) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
+    const int lo = tile.z, hi = tile.w, nt = team_tiles<TW>(tile);
+    if (nt == 0) continue;
     const bool one = hi - lo <= kChunk;
-    Keys keys;
-    float s[MAPS][8][4];
-    auto scores = [&](int k0) {
-      keys.load(a.rows, k0, hi);
+    for (int w = wt; w < (nt + TW - 1) / TW * TW; w += TW) {  // every warp of the team, for its barriers
+      const bool on = w < nt;
+      const int first = on ? tile.x + kTile * w : tile.x, nr = min(kTile, hi - first);
+      // differential attention subtracts the maps before the product with V, so both normalisers
+      // come first: its forward walks the keys twice
+      constexpr int PASSES = MODE == kForward && MAPS == 2 ? 2 : 1;
+      constexpr int NACC = MODE == kForward ? DV / 8 : MODE == kDq ? DV / 8 : 1;
+      float m[MAPS][2], l[MAPS][2], dd[MAPS][2], acc[NACC][4];
+      uint32_t q[DV / 16][4], o[MODE == kForward ? 1 : DV / 16][4];
+      const float *t0 = tab, *t8 = tab;
+      int ci = 0, ci8 = 0;
 #pragma unroll
       for (int u = 0; u < MAPS; ++u) {
-        const Rows<bf16, D> K = {static_cast<const bf16*>(a.k), nullptr, a.hkv, MAPS * hk + u};
-        contract_dim<D, 8>(q[u], K, keys.tok, keys.n, s[u]);
-        finish_scores<BIAS>(s[u], keys, mul, tab_s, rg.y + c0, rg8.y + c0);
+        m[u][0] = m[u][1] = kNegInf;
+        l[u][0] = l[u][1] = dd[u][0] = dd[u][1] = 0.f;
       }
-    };
-    // new maximum and sum of a row over the chunk; s becomes 2^(s - max); the old sum's factor comes back
-    auto softmax = [&](int u, int i) {
-      float mx = m[u][i];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fmaxf(s[u][j][2 * i], s[u][j][2 * i + 1]));
-      mx = quad_max(mx);
-      const float ms = safe_max(mx), old = ex2(safe_max(m[u][i]) - ms);
-      float e = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          s[u][j][2 * i + x] = ex2(s[u][j][2 * i + x] - ms);
-          e += s[u][j][2 * i + x];
+      for (int e = 0; e < NACC; ++e) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
+      if (on) {
+        __syncwarp();
+        stage<D, DV>(scratch, Q, a.rows, first, nr, kTile, lane, 32);
+        if (MODE != kForward) stage<D, DV>(scratch2, O, a.rows, first, nr, kTile, lane, 32);
+        if (BIAS) {
+          ci = __ldg(&a.rows[first + min(g, nr - 1)].y) + c0;
+          ci8 = __ldg(&a.rows[first + min(g + 8, nr - 1)].y) + c0;
+          t0 = tab + ci;
+          t8 = tab + ci8;
         }
-      l[u][i] = l[u][i] * old + quad_sum(e);
-      m[u][i] = mx;
-      return old;
-    };
-    uint32_t pf[4][4];
-    if constexpr (MAPS == 1) {
-      for (int k0 = lo; k0 < hi; k0 += kChunk) {
-        scores(k0);
-        const float f0 = softmax(0, 0), f1 = softmax(0, 1);
-        pack_a<8>(s[0], pf);
-        if (!one) {
+        if constexpr (MODE == kDq) {
 #pragma unroll
-          for (int e = 0; e < DV / 8; ++e) acc[e][0] *= f0, acc[e][1] *= f0, acc[e][2] *= f1, acc[e][3] *= f1;
+          for (int u = 0; u < MAPS; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const size_t at = (size_t)(MAPS * h + u) * a.N + first + min(g + 8 * i, nr - 1);
+              m[u][i] = a.lse2[at];
+              dd[u][i] = a.D[at];
+            }
         }
-        contract_rows<DV, 4>(pf, V, keys.tok, keys.n, acc);
       }
-      store_acc<D, DV>(static_cast<bf16*>(a.out), a.hq, MAPS * h, rg.x, vg, rg8.x, vg8, acc, safe_inv(l[0][0]),
-                       safe_inv(l[0][1]));
-      if (a.lse && t4 == 0) {
-        if (vg) a.lse[(size_t)rg.x * a.hq + h] = l[0][0] == 0.f ? kNegInf : (m[0][0] + log2f(l[0][0])) * kLn2;
-        if (vg8) a.lse[(size_t)rg8.x * a.hq + h] = l[0][1] == 0.f ? kNegInf : (m[0][1] + log2f(l[0][1])) * kLn2;
-      }
-    } else {
-      // the maps are subtracted before the product with V, so both normalisers come first
-      if (!one)
+#pragma unroll 1
+      for (int pass = 0; pass < PASSES; ++pass) {
+#pragma unroll 1
         for (int k0 = lo; k0 < hi; k0 += kChunk) {
-          scores(k0);
+          const int n = min(kChunk, hi - k0);
+          if (!one || (w < TW && pass == 0)) {
+            team_sync<TW>(team);
+            stage_keys<D, DV>(keys, K, a.rows, k0, n, tid, 32 * TW);
+            stage_keys<D, DV>(vals, V, a.rows, k0, n, tid, 32 * TW);
+            if (BIAS)
+              for (int i = tid; i < kChunk; i += 32 * TW) codes[i] = __ldg(&a.rows[k0 + min(key_at(i), n - 1)].y);
+            cp_commit();
+            cp_wait<0>();
+            team_sync<TW>(team);
+          } else {
+            cp_commit();
+            cp_wait<0>();
+            __syncwarp();
+          }
+          if (!on) continue;
+          if (k0 == lo && pass == 0) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) softmax(u, 0), softmax(u, 1);
+            for (int d = 0; d < DV / 16; ++d) {
+              load_a<DV>(q[d], scratch, 0, d);
+              if constexpr (MODE != kForward) load_a<DV>(o[d], scratch2, 0, d);
+            }
+          }
+#pragma unroll 1
+          for (int half = 0; half < n; half += 32) {
+            const uint32_t kt = keys + half * DV * 2, vt = vals + half * DV * 2;
+            const int* hc = codes + half;
+            float s[MAPS][4][4], dp[MODE == kForward ? 1 : 4][4];
+#pragma unroll
+            for (int u = 0; u < MAPS; ++u) {
+              contract_dim<DV, D, 2>(q + u * D / 16, kt, u * D / 8, s[u]);
+              finish_scores<BIAS>(s[u], hc, n - half, mul, t0, t8);
+            }
+            if constexpr (MODE != kForward) contract_dim<DV, DV, 2>(o, vt, 0, dp);
+            if constexpr (MODE == kDq) {
+              // p = 2^(s - lse2), dS = p (dP - D)
+#pragma unroll
+              for (int u = 0; u < MAPS; ++u) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                    const float p = ex2(s[u][j][x] - m[u][x >> 1]);
+                    s[u][j][x] = (u ? -lam * p : p) * (dp[j][x] - dd[u][x >> 1]);
+                  }
+                if (BIAS) {
+                  if (grad) {
+                    if constexpr (TAB == 3)
+                      add_bias_grad([&](int at, float x) { wide.add(at, x); }, s[0], hc, ci, ci8, n - half, nr);
+                    else
+                      add_bias_grad([&](int at, float x) { fx.add(limbs + at, limbs + T3 + at, x); }, s[0], hc, ci, ci8,
+                                    n - half, nr);
+                  }
+                }
+                uint32_t f[2][4];
+                pack_a<4>(s[u], f);
+                contract_rows<DV, D, 2>(f, kt, u * D / 8, acc + u * D / 8);
+              }
+            } else {
+              // online maximum, sum (and sum of p dP) of a row; the sums stay per lane to the end
+              float old[MAPS][2];
+#pragma unroll
+              for (int u = 0; u < MAPS; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  if (MODE == kForward && MAPS == 2 && pass == 1) {
+                    const float f = (u ? -lam : 1.f) * l[u][i], ms = safe_max(m[u][i]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                      for (int x = 0; x < 2; ++x) s[u][j][2 * i + x] = ex2(s[u][j][2 * i + x] - ms) * f;
+                    continue;
+                  }
+                  float mx = m[u][i];
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(s[u][j][2 * i], s[u][j][2 * i + 1]));
+                  mx = quad_max(mx);
+                  const float ms = safe_max(mx);
+                  old[u][i] = ex2(safe_max(m[u][i]) - ms);
+                  float e = 0.f, ed = 0.f;
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                      const float p = ex2(s[u][j][2 * i + x] - ms);
+                      s[u][j][2 * i + x] = p;
+                      e += p;
+                      if constexpr (MODE == kStats) {
+                        ed = fmaf(p, dp[j][2 * i + x], ed);
+                        if (u == 0) top = max(top, __float_as_uint(dp[j][2 * i + x]) & 0x7fffffffu);
+                      }
+                    }
+                  l[u][i] = fmaf(l[u][i], old[u][i], e);
+                  if (MODE == kStats) dd[u][i] = fmaf(dd[u][i], old[u][i], ed);
+                  m[u][i] = mx;
+                }
+              if constexpr (MODE == kForward) {
+                if (MAPS == 1 && half + k0 > lo) {
+#pragma unroll
+                  for (int e = 0; e < NACC; ++e)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) acc[e][x] *= old[0][x >> 1];
+                }
+                if (MAPS == 1 || pass == 1) {
+                  if constexpr (MAPS == 2) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                      for (int x = 0; x < 4; ++x) s[0][j][x] += s[MAPS - 1][j][x];
+                  }
+                  uint32_t p[2][4];
+                  pack_a<4>(s[0], p);
+                  contract_rows<DV, DV, 2>(p, vt, 0, acc);
+                }
+              }
+            }
+          }
         }
-      for (int k0 = lo; k0 < hi; k0 += kChunk) {
-        scores(k0);
-        float c[2][2];
+        if constexpr (MODE == kForward && MAPS == 2) {
+          if (pass == 0) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) l[u][i] = safe_inv(quad_sum(l[u][i]));
+          }
+        }
+      }
+      if (!on) continue;
+      if constexpr (MODE == kForward) {
+        float f[2] = {1.f, 1.f};
+        if constexpr (MAPS == 1) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            if (one) {
-              softmax(u, i);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) s[u][j][2 * i + x] = ex2(s[u][j][2 * i + x] - safe_max(m[u][i]));
-            }
-            c[u][i] = safe_inv(l[u][i]) * (u ? -lam : 1.f);
+            l[0][i] = quad_sum(l[0][i]);
+            f[i] = safe_inv(l[0][i]);
+            if (a.lse && t4 == 0 && g + 8 * i < nr)
+              a.lse[(size_t)__ldg(&a.rows[first + g + 8 * i].x) * a.hq + h] =
+                  l[0][i] == 0.f ? kNegInf : (m[0][i] + log2f(l[0][i])) * kLn2;
           }
+        }
+        store_acc<D, DV>(scratch, acc, f[0], f[1], static_cast<bf16*>(a.out), a.hq, MAPS * h, a.rows, first, nr);
+      } else if constexpr (MODE == kStats) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int u = 0; u < MAPS; ++u)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) s[0][j][x] = fmaf(s[1][j][x], c[1][x >> 1], s[0][j][x] * c[0][x >> 1]);
-        pack_a<8>(s[0], pf);
-        contract_rows<DV, 4>(pf, V, keys.tok, keys.n, acc);
+          for (int i = 0; i < 2; ++i) {
+            l[u][i] = quad_sum(l[u][i]);
+            dd[u][i] = quad_sum(dd[u][i]);
+            if (t4 == 0 && g + 8 * i < nr) {
+              const size_t at = (size_t)(MAPS * h + u) * a.N + first + g + 8 * i;
+              a.lse2[at] = lse2_of(m[u][i], l[u][i]);
+              a.D[at] = dd[u][i] * safe_inv(l[u][i]);
+              if (!(l[u][i] >= 0.f)) top = 0x7fffffffu;
+            }
+          }
+      } else {
+        store_acc<D, DV>(scratch, acc, a.scale, a.scale, static_cast<bf16*>(a.dq), a.hq, MAPS * h, a.rows, first, nr);
       }
-      store_acc<D, DV>(static_cast<bf16*>(a.out), a.hq, MAPS * h, rg.x, vg, rg8.x, vg8, acc, 1.f, 1.f);
     }
   }
-}
-
-template <int D, int MAPS, bool BIAS>
-cudaError_t fwd(const WinArgs& a, cudaStream_t st) {
-  const size_t smem = BIAS ? sizeof(float) * offsets(a.m) : 0;
-  auto kern = window_fwd_mma_kernel<D, MAPS, BIAS>;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
+  if constexpr (MODE == kStats && BIAS) {
+    top = __reduce_max_sync(kFull, top);
+    if (lane == 0 && a.dbias) atomicMax(a.amax + h, top);
   }
-  const int heads = a.hq / MAPS, need = (a.T + kFwdWarps - 1) / kFwdWarps;
-  int gx = (4 * 2 * 148 + heads - 1) / heads;
-  gx = gx < need ? gx : need;
-  SSA_LAUNCH("window_fwd_mma_kernel", kern, dim3(gx, heads), 32 * kFwdWarps, smem, st, a);
-  return cudaGetLastError();
-}
-
-// ---------------------------------------------------------------------------
-// backward: dq, row statistics, partial bias gradients
-// ---------------------------------------------------------------------------
-
-// Eight warps.  With a bias gradient the last one is the CTA's collector: the others hand it their
-// dS tiles (fp32, [16][64]) through a slot each, and it alone adds them to the CTA's table of
-// offsets, in a fixed order.  A row's keys have distinct offsets, so a row is one read, add and
-// write per lane without atomics (cells with two tokens in a voxel: lane by lane).
-constexpr int kDqWarps = 8;
-constexpr int kSlotStride = kChunk + 4;
-constexpr int kSlot = kTile * kSlotStride;  // floats
-
-// TAB: where the bias is read: 0 no bias, 1 shared memory, 2 global memory (the table beside the
-// collector's does not fit: edge 16).
-template <int D, int MAPS, int TAB, typename E>
-__global__ void __launch_bounds__(32 * kDqWarps, D == 128 || (MAPS == 2 && D == 64) ? 1 : 2)
-    window_dq_mma_kernel(WinArgs a) {
-  constexpr int DV = MAPS * D;
-  constexpr bool BIAS = TAB != 0;
-  extern __shared__ float sm[];
-  __shared__ uint64_t full[kDqWarps], empty[kDqWarps];
-  const int h = blockIdx.y, hk = h / (a.hq / a.hkv);
-  const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3, warp = threadIdx.x >> 5;
-  const float mul = a.scale * kLog2e;
-  const bool collect = BIAS && a.dbias;
-  const int T3 = BIAS ? offsets(a.m) : 0, c0 = BIAS ? center(a.m) : 0;
-  const float* tab = TAB == 2 ? a.tab2 + (size_t)h * T3 : sm;
-  float* dtab = sm + (TAB == 1 ? T3 : 0);
-  float* slots = dtab + (T3 + 3) / 4 * 4 + (TAB == 1 ? (4 - T3 % 4) % 4 : 0);
-  if constexpr (BIAS) {
-    for (int i = threadIdx.x; i < T3; i += blockDim.x) {
-      if (TAB == 1) sm[i] = bias2_at(a, h, i);
-      if (collect) dtab[i] = 0.f;
-    }
-    if (threadIdx.x < kDqWarps) {
-      tc::mbar_init(&full[threadIdx.x], 1);
-      tc::mbar_init(&empty[threadIdx.x], 1);
-    }
-    tc::fence_mbar_init();
+  if (grad && TAB != 3) {
     __syncthreads();
-  }
-  const int nc = collect ? kDqWarps - 1 : kDqWarps;  // computing warps
-  if (collect && warp == nc) {
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int base = blockIdx.x * nc; base < a.T && ok; base += gridDim.x * nc)
-      for (int w = 0; w < nc && base + w < a.T && ok; ++w) {
-        const int4 tile = __ldg(&a.tiles[base + w]);
-        const int nr = tile.y & (kDupFlag - 1);
-        if (nr == 0) continue;
-        const bool dup = tile.y & kDupFlag;
-        const int cr = __ldg(&a.rows[tile.x + min(lane, nr - 1)].y) + c0;
-        for (int k0 = tile.z; k0 < tile.w; k0 += kChunk) {
-          Keys k;
-          k.load(a.rows, k0, tile.w);
-          ok = tc::mbar_wait_warp(&full[w], (phase >> w) & 1);
-          if (!ok) break;
-          phase ^= 1u << w;
-          const float* slot = slots + w * kSlot;
-          if (!dup) {
-            const bool v0 = lane < k.n, v1 = lane + 32 < k.n;
-            float d0[kTile], d1[kTile];
-#pragma unroll
-            for (int r = 0; r < kTile; ++r) d0[r] = slot[r * kSlotStride + lane], d1[r] = slot[r * kSlotStride + 32 + lane];
-#pragma unroll
-            for (int r = 0; r < kTile; ++r) {
-              const int c = __shfl_sync(kFull, cr, r);
-              if (r < nr) {
-                float* p0 = dtab + c - k.code[0];
-                float* p1 = dtab + c - k.code[1];
-                const float x0 = v0 ? *p0 : 0.f, x1 = v1 ? *p1 : 0.f;
-                if (v0) *p0 = x0 + d0[r];
-                if (v1) *p1 = x1 + d1[r];
-              }
-              __syncwarp();
-            }
-          } else {
-            for (int r = 0; r < nr; ++r) {
-              const int c = __shfl_sync(kFull, cr, r);
-              for (int i = 0; i < k.n; ++i) {
-                if (lane == (i & 31)) dtab[c - k.code[i >> 5]] += slot[r * kSlotStride + i];
-                __syncwarp();
-              }
-            }
-          }
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&empty[w]);
-        }
-      }
-    __syncwarp();
-    if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
     float* part = a.part + ((size_t)h * a.parts + blockIdx.x) * T3;
-    for (int i = lane; i < T3; i += 32) part[i] = dtab[i];
-    return;
+    for (int i = threadIdx.x; i < T3; i += blockDim.x) part[i] = fx.value(limbs[i], limbs[T3 + i]);
   }
-  float lam = 0.f;
-  if constexpr (MAPS == 2) {
-    float e1, e2;
-    lambda_terms<D>(a.lam, a.hq / 2, h, e1, e2);
-    lam = e1 - e2 + a.lam_init;
-  }
-  const Rows<bf16, D> O = {static_cast<const bf16*>(a.dout), nullptr, a.hq, MAPS * h};
-  const Rows<E, D> V = {static_cast<const E*>(a.v), a.sv, a.hkv, MAPS * hk};
-  uint32_t phase = 1;  // the first wait on `empty` passes
-  for (int t = blockIdx.x * nc + warp; t < a.T; t += gridDim.x * nc) {
-    const int4 tile = __ldg(&a.tiles[t]);
-    const int first = tile.x, nr = tile.y & (kDupFlag - 1), lo = tile.z, hi = tile.w;
-    if (nr == 0) continue;
-    const bool vg = g < nr, vg8 = g + 8 < nr;
-    const int2 rg = __ldg(&a.rows[first + min(g, nr - 1)]), rg8 = __ldg(&a.rows[first + min(g + 8, nr - 1)]);
-    const bool one = hi - lo <= kChunk;
-    float m[MAPS][2], l[MAPS][2], dd[MAPS][2], acc[MAPS][D / 8][4];
-#pragma unroll
-    for (int u = 0; u < MAPS; ++u) {
-      m[u][0] = m[u][1] = kNegInf, l[u][0] = l[u][1] = dd[u][0] = dd[u][1] = 0.f;
-#pragma unroll
-      for (int e = 0; e < D / 8; ++e) acc[u][e][0] = acc[u][e][1] = acc[u][e][2] = acc[u][e][3] = 0.f;
-    }
-    Keys keys;
-    float s[MAPS][8][4], dp[8][4];
-    auto products = [&](int k0) {
-      keys.load(a.rows, k0, hi);
-#pragma unroll
-      for (int u = 0; u < MAPS; ++u) {
-        const Rows<E, D> Q = {static_cast<const E*>(a.q), a.sq, a.hq, MAPS * h + u};
-        const Rows<E, D> K = {static_cast<const E*>(a.k), a.sk, a.hkv, MAPS * hk + u};
-        uint32_t q[D / 16][4];
-        load_a<D>(Q, rg.x, vg, rg8.x, vg8, q);
-        contract_dim<D, 8>(q, K, keys.tok, keys.n, s[u]);
-        finish_scores<BIAS>(s[u], keys, mul, tab, rg.y + c0, rg8.y + c0);
-      }
-      uint32_t o[DV / 16][4];
-      load_a<DV>(O, rg.x, vg, rg8.x, vg8, o);
-      contract_dim<DV, 8>(o, V, keys.tok, keys.n, dp);
-    };
-    // maximum, sum and sum of p dP of a row over the chunk; s becomes 2^(s - max)
-    auto stats = [&](int u, int i) {
-      float mx = m[u][i];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fmaxf(s[u][j][2 * i], s[u][j][2 * i + 1]));
-      mx = quad_max(mx);
-      const float ms = safe_max(mx), old = ex2(safe_max(m[u][i]) - ms);
-      float e = 0.f, ed = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float p = ex2(s[u][j][2 * i + x] - ms);
-          s[u][j][2 * i + x] = p;
-          e += p;
-          if (8 * j + 2 * t4 + x < keys.n) ed = fmaf(p, dp[j][2 * i + x], ed);
-        }
-      l[u][i] = l[u][i] * old + quad_sum(e);
-      dd[u][i] = dd[u][i] * old + quad_sum(ed);
-      m[u][i] = mx;
-    };
-    if (!one)
-      for (int k0 = lo; k0 < hi; k0 += kChunk) {
-        products(k0);
-#pragma unroll
-        for (int u = 0; u < MAPS; ++u) stats(u, 0), stats(u, 1);
-      }
-    bool ok = true;
-    for (int k0 = lo; k0 < hi; k0 += kChunk) {
-      products(k0);
-#pragma unroll
-      for (int u = 0; u < MAPS; ++u)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (one) {
-            stats(u, i);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-              for (int x = 0; x < 2; ++x) s[u][j][2 * i + x] = ex2(s[u][j][2 * i + x] - safe_max(m[u][i]));
-          }
-          const float inv = safe_inv(l[u][i]), dm = dd[u][i] * inv, f = u ? -lam * inv : inv;
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-              s[u][j][2 * i + x] =
-                  8 * j + 2 * t4 + x < keys.n ? s[u][j][2 * i + x] * f * (dp[j][2 * i + x] - dm) : 0.f;
-        }
-      if (collect) {
-        ok = tc::mbar_wait_warp(&empty[warp], phase);
-        if (!ok) break;
-        phase ^= 1;
-        float* slot = slots + warp * kSlot;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<float2*>(slot + (g + 8 * i) * kSlotStride + 8 * j + 2 * t4) =
-                make_float2(s[0][j][2 * i], s[0][j][2 * i + 1]);
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&full[warp]);
-      }
-#pragma unroll
-      for (int u = 0; u < MAPS; ++u) {
-        const Rows<E, D> K = {static_cast<const E*>(a.k), a.sk, a.hkv, MAPS * hk + u};
-        uint32_t f[4][4];
-        pack_a<8>(s[u], f);
-        contract_rows<D, 4>(f, K, keys.tok, keys.n, acc[u]);
-      }
-    }
-    if (!ok) {
-      if (lane == 0) atomicOr(a.status, kStatusTimeout);
-      break;
-    }
-#pragma unroll
-    for (int u = 0; u < MAPS; ++u) {
-      store_acc<D, D>(static_cast<bf16*>(a.dq), a.hq, MAPS * h + u, rg.x, vg, rg8.x, vg8, acc[u], a.scale, a.scale);
-      if (t4 == 0) {
-        const size_t at = (size_t)(MAPS * h + u) * a.N + first + g;
-        if (vg) a.lse2[at] = lse2_of(m[u][0], l[u][0]), a.D[at] = dd[u][0] * safe_inv(l[u][0]);
-        if (vg8) a.lse2[at + 8] = lse2_of(m[u][1], l[u][1]), a.D[at + 8] = dd[u][1] * safe_inv(l[u][1]);
-      }
-    }
-  }
+}
+
+// CTAs along the tiles for `heads` heads: about `waves` times the resident ones, no more than the
+// tiles fill.
+int grid_x(int heads, int T, int per_cta, int resident, int waves) {
+  const int need = (T + per_cta - 1) / per_cta, want = (waves * resident * 148 + heads - 1) / heads;
+  return need < want ? need : want;
+}
+
+template <typename K>
+cudaError_t need_smem(K kern, size_t smem) {
+  return smem > 47 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
+                          : cudaSuccess;
+}
+
+template <int D, int MAPS, bool BIAS, typename E, int MODE>
+cudaError_t rows_pass(const char* name, const WinArgs& a, cudaStream_t st) {
+  using S = Shape<D, MAPS, MODE>;
+  constexpr int ON = BIAS ? 1 : 0;
+  const bool grad = MODE == kDq && BIAS && a.dbias;
+  const size_t T3 = BIAS ? offsets(a.m) : 0, fixed = grad && !a.wide ? 8 * T3 : 0;
+  // as many teams as fit beside the tables of the gradient
+  const size_t fit = (kSmemMost - fixed) / S::per_team;
+  const int NT = fit < (size_t)S::teams ? (int)fit : S::teams;
+  const size_t rest = fixed + (size_t)NT * S::per_team;
+  // the bias in shared memory where it fits; the forward has room for it always
+  const bool in_smem = rest + 4 * T3 <= kSmemMost && !(grad && a.wide);
+  auto kern = window_rows_kernel<D, MAPS, ON, E, MODE>;
+  if constexpr (MODE != kForward)
+    if (!in_smem) kern = window_rows_kernel<D, MAPS, 2 * ON, E, MODE>;
+  if constexpr (MODE == kDq)
+    if (grad && a.wide) kern = window_rows_kernel<D, MAPS, 3 * ON, E, MODE>;
+  const size_t smem = rest + (in_smem ? 4 * T3 : 0);
+  const cudaError_t e = need_smem(kern, smem);
+  if (e != cudaSuccess) return e;
+  const int heads = a.hq / MAPS;
+  const int gx = grad && !a.wide ? a.parts : grid_x(heads, a.T, NT, S::resident, 4);
+  SSA_LAUNCH(name, kern, dim3(gx, heads), 32 * S::TW * NT, smem, st, a);
+  return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------------------
 // backward: dk, dv
 // ---------------------------------------------------------------------------
 
-// A warp takes 16 keys of a cell and one key head: the transposed scores of the cell's queries, 32
-// at a time, of every query head that reads the key head.
+// A CTA of four warps takes 64 keys of a cell and one key head, 16 keys per warp: the transposed
+// scores of the cell's queries, 64 at a time, of every query head that reads the key head.  Q, dO,
+// the statistics and the head's bias table of the next step arrive while this one is computed.
 constexpr int kDkvWarps = 4;
 
-template <int D, int MAPS, bool BIAS, typename E>
-__global__ void __launch_bounds__(32 * kDkvWarps, D == 128 || (MAPS == 2 && D == 64) ? 2 : 3)
-    window_dkv_mma_kernel(WinArgs a) {
-  constexpr int DV = MAPS * D;
+template <int D, int MAPS>
+struct DkvShape {
+  static constexpr int DV = MAPS * D;
+  // K and V as fragments in registers; wide rows leave no room for them
+  static constexpr bool held = DV <= 64;
+  static constexpr int KT = kChunk * DV * 2;               // one tile of 64 rows, bytes
+  static constexpr int Q = held ? 0 : 2 * KT;              // two stages of Q, dO and the statistics
+  static constexpr int stat = 2 * KT;                      // within a stage: lse2, D of MAPS maps
+  static constexpr int stage = stat + 2 * MAPS * kChunk * 4;
+  static constexpr int codes = Q + 2 * stage;              // codes of the queries, two stages
+  static constexpr int tab = codes + 2 * kChunk * 4;       // two bias tables
+};
+
+// TAB: 0 no bias, 1 tables staged in shared memory, 2 read in global memory (the largest edges).
+template <int D, int MAPS, int TAB, typename E>
+__global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window_dkv_mma_kernel(WinArgs a) {
+  using S = DkvShape<D, MAPS>;
+  constexpr int DV = S::DV, NTH = 32 * kDkvWarps;
+  constexpr bool BIAS = TAB != 0;
+  extern __shared__ __align__(128) char sm[];
   const int G = a.hq / a.hkv, hk = blockIdx.y;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3, warp = threadIdx.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t4 = lane & 3, warp = tid >> 5;
   const float mul = a.scale * kLog2e;
-  const int c0 = BIAS ? center(a.m) : 0, T3 = BIAS ? offsets(a.m) : 0;
-  const int t = blockIdx.x * kDkvWarps + warp;
-  if (t >= a.T) return;
-  const int4 tile = __ldg(&a.tiles[t]);
-  const int first = tile.x, nr = tile.y & (kDupFlag - 1), lo = tile.z, hi = tile.w;
-  if (nr == 0) return;
-  const bool vg = g < nr, vg8 = g + 8 < nr;
-  const int2 rg = __ldg(&a.rows[first + min(g, nr - 1)]), rg8 = __ldg(&a.rows[first + min(g + 8, nr - 1)]);
-  const Rows<E, D> V = {static_cast<const E*>(a.v), a.sv, a.hkv, MAPS * hk};
+  const int c0 = BIAS ? center(a.m) : 0, T3 = BIAS ? offsets(a.m) : 0, T3p = BIAS ? table_pitch(a.m) : 0;
+  const int4 tile = __ldg(&a.tiles[blockIdx.x]);
+  const int lo = tile.z, hi = tile.w, nt = team_tiles<kDkvWarps>(tile);
+  if (nt == 0) return;
+  // K and V stay before the stages, or are in the second stage until it is needed
+  const uint32_t base = tc::smem_u32(sm), kt = base + (S::held ? S::stage : 0), vt = kt + S::KT;
+  const int chunks = (hi - lo + kChunk - 1) / kChunk, steps = G * chunks;
+  const int keys0 = tile.x, nkeys = min(kTile * nt, hi - keys0);
+
+  // step s: query head hk G + s / chunks, queries from lo + 64 (s % chunks)
+  auto load = [&](int s) {
+    const int h = hk * G + s / chunks, k0 = lo + kChunk * (s % chunks), n = min(kChunk, hi - k0);
+    const int total = (n + 31) & ~31;
+    const uint32_t st = base + S::Q + (s & 1) * S::stage;
+    stage<D, DV>(st, Rows<E, D>{static_cast<const E*>(a.q), a.sq, a.hq, MAPS * h}, a.rows, k0, n, total, tid, NTH);
+    stage<D, DV>(st + S::KT, Rows<bf16, D>{static_cast<const bf16*>(a.dout), nullptr, a.hq, MAPS * h}, a.rows, k0, n,
+                 total, tid, NTH);
+    float* stat = reinterpret_cast<float*>(sm + S::Q + (s & 1) * S::stage + S::stat);
+    for (int i = tid; i < 2 * MAPS * kChunk; i += NTH) {
+      const int u = i / (2 * kChunk), which = i / kChunk & 1, q = i % kChunk;
+      const size_t at = (size_t)(MAPS * h + u) * a.N + k0 + q;
+      stat[i] = q >= n ? (which ? 0.f : kPosInf) : which ? a.D[at] : a.lse2[at];
+    }
+    if (BIAS) {
+      int* codes = reinterpret_cast<int*>(sm + S::codes) + (s & 1) * kChunk;
+      if (tid < kChunk) codes[tid] = __ldg(&a.rows[k0 + min(tid, n - 1)].y) + c0;
+    }
+    if (TAB == 1 && s % chunks == 0) {
+      const uint32_t dst = base + S::tab + (s / chunks & 1) * T3p * 4;
+      const float* src = a.tab2 + (size_t)h * T3p;
+      for (int i = tid; i < T3p / 4; i += NTH) cp16(dst + 16 * i, src + 4 * i, true);
+    }
+    cp_commit();
+  };
+
+  stage<D, DV>(kt, Rows<E, D>{static_cast<const E*>(a.k), a.sk, a.hkv, MAPS * hk}, a.rows, keys0, nkeys, kTile * nt, tid,
+               NTH);
+  stage<D, DV>(vt, Rows<E, D>{static_cast<const E*>(a.v), a.sv, a.hkv, MAPS * hk}, a.rows, keys0, nkeys, kTile * nt, tid,
+               NTH);
+  load(0);
+  const int r0 = kTile * warp, first = keys0 + r0, nr = min(kTile, hi - first);
+  const bool on = warp < nt;
+  int ck = 0, ck8 = 0;
+  if (BIAS && on) {
+    ck = __ldg(&a.rows[first + min(g, nr - 1)].y);
+    ck8 = __ldg(&a.rows[first + min(g + 8, nr - 1)].y);
+  }
   float dk[MAPS][D / 8][4], dv[DV / 8][4];
 #pragma unroll
   for (int u = 0; u < MAPS; ++u)
@@ -655,102 +765,131 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D == 128 || (MAPS == 2 && D ==
     for (int e = 0; e < D / 8; ++e) dk[u][e][0] = dk[u][e][1] = dk[u][e][2] = dk[u][e][3] = 0.f;
 #pragma unroll
   for (int e = 0; e < DV / 8; ++e) dv[e][0] = dv[e][1] = dv[e][2] = dv[e][3] = 0.f;
-  for (int k0 = lo; k0 < hi; k0 += 32) {
-    const int n = min(32, hi - k0);
-    const int2 qr = __ldg(&a.rows[k0 + min(lane, n - 1)]);
-    const int tok[1] = {qr.x};
-    for (int h = hk * G; h < hk * G + G; ++h) {
+
+  uint32_t kf[S::held ? DV / 16 : 1][4], vf[S::held ? DV / 16 : 1][4];
+  if constexpr (S::held) {
+    cp_wait<0>();
+    __syncthreads();
+    if (on) {
+#pragma unroll
+      for (int d = 0; d < DV / 16; ++d) load_a<DV>(kf[d], kt, r0, d), load_a<DV>(vf[d], vt, r0, d);
+    }
+    __syncthreads();
+  }
+
+  for (int s = 0; s < steps; ++s) {
+    if (s + 1 < steps) {
+      load(s + 1);
+      cp_wait<1>();
+    } else {
+      cp_wait<0>();
+    }
+    __syncthreads();
+    if (on) {
+      const int h = hk * G + s / chunks, n = min(kChunk, hi - lo - kChunk * (s % chunks));
       float lam = 0.f;
       if constexpr (MAPS == 2) {
         float e1, e2;
         lambda_terms<D>(a.lam, a.hq / 2, h, e1, e2);
         lam = e1 - e2 + a.lam_init;
       }
-      const Rows<bf16, D> O = {static_cast<const bf16*>(a.dout), nullptr, a.hq, MAPS * h};
-      float dp[4][4], pv[4][4];
-      {
-        uint32_t f[DV / 16][4];
-        load_a<DV>(V, rg.x, vg, rg8.x, vg8, f);
-        contract_dim<DV, 4>(f, O, tok, n, dp);
-      }
+      const uint32_t qt = base + S::Q + (s & 1) * S::stage, ot = qt + S::KT;
+      const float* stat = reinterpret_cast<const float*>(sm + S::Q + (s & 1) * S::stage + S::stat);
+      const int* codes = reinterpret_cast<const int*>(sm + S::codes) + (s & 1) * kChunk;
+      const float* tab = TAB == 2 ? a.tab2 + (size_t)h * T3p
+                                  : reinterpret_cast<const float*>(sm + S::tab) + (s / chunks & 1) * T3p;
+      const float *tk = tab - ck, *tk8 = tab - ck8;
+#pragma unroll 1
+      for (int q0 = 0; q0 < n; q0 += 32) {
+        // rows q0 .. of the tiles: 32 rows on, the permutation of the units repeats
+        const uint32_t qq = qt + q0 * DV * 2, oo = ot + q0 * DV * 2;
+        float dp[4][4], pv[4][4];
+        if constexpr (S::held) {
+          contract_dim<DV, DV, 2>(vf, oo, 0, dp);
+        } else {
+          uint32_t f[DV / 16][4];
 #pragma unroll
-      for (int u = 0; u < MAPS; ++u) {
-        const Rows<E, D> Q = {static_cast<const E*>(a.q), a.sq, a.hq, MAPS * h + u};
-        const Rows<E, D> K = {static_cast<const E*>(a.k), a.sk, a.hkv, MAPS * hk + u};
-        float s[4][4];
-        {
-          uint32_t f[D / 16][4];
-          load_a<D>(K, rg.x, vg, rg8.x, vg8, f);
-          contract_dim<D, 4>(f, Q, tok, n, s);
+          for (int d = 0; d < DV / 16; ++d) load_a<DV>(f[d], vt, r0, d);
+          contract_dim<DV, DV, 2>(f, oo, 0, dp);
         }
-        const size_t at = (size_t)(MAPS * h + u) * a.N + k0 + min(lane, n - 1);
-        const float lse2 = lane < n ? a.lse2[at] : kPosInf, dd = a.D[at];
-        const float* tab = BIAS ? a.tab2 + (size_t)h * T3 : nullptr;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int u = 0; u < MAPS; ++u) {
+          float sc[4][4];
+          if constexpr (S::held) {
+            contract_dim<DV, D, 2>(kf + u * D / 16, qq, u * D / 8, sc);
+          } else {
+            uint32_t f[D / 16][4];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int q = 8 * j + 2 * t4 + x;
-            const float L = __shfl_sync(kFull, lse2, q), Dq = __shfl_sync(kFull, dd, q);
-            float b0 = 0.f, b1 = 0.f;
+            for (int d = 0; d < D / 16; ++d) load_a<DV>(f[d], kt, r0, u * D / 16 + d);
+            contract_dim<DV, D, 2>(f, qq, u * D / 8, sc);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int c = q0 + 8 * j + 2 * t4;
+            const float2 L = *reinterpret_cast<const float2*>(stat + 2 * u * kChunk + c);
+            const float2 Dq = *reinterpret_cast<const float2*>(stat + (2 * u + 1) * kChunk + c);
+            float b[4] = {0.f, 0.f, 0.f, 0.f};
             if constexpr (BIAS) {
-              const int cq = __shfl_sync(kFull, qr.y, q) + c0;
-              b0 = __ldg(tab + cq - rg.y);
-              b1 = __ldg(tab + cq - rg8.y);
+              const int2 cq = *reinterpret_cast<const int2*>(codes + c);
+              b[0] = tk[cq.x], b[1] = tk[cq.y], b[2] = tk8[cq.x], b[3] = tk8[cq.y];
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float p = q < n ? ex2(fmaf(s[j][2 * i + x], mul, i ? b1 : b0) - L) : 0.f;
+            for (int x = 0; x < 4; ++x) {
+              // columns past the last query: lse2 is plus infinity, so p is 0, and their dO is 0
+              const float p = ex2(fmaf(sc[j][x], mul, b[x]) - (x & 1 ? L.y : L.x));
               const float w = u ? -lam * p : p;
-              pv[j][2 * i + x] = u ? pv[j][2 * i + x] + w : w;
-              s[j][2 * i + x] = q < n ? w * (dp[j][2 * i + x] - Dq) : 0.f;
+              pv[j][x] = u ? pv[j][x] + w : w;
+              sc[j][x] = w * (dp[j][x] - (x & 1 ? Dq.y : Dq.x));
             }
           }
+          uint32_t f[2][4];
+          pack_a<4>(sc, f);
+          contract_rows<DV, D, 2>(f, qq, u * D / 8, dk[u]);
+        }
         uint32_t f[2][4];
-        pack_a<4>(s, f);
-        contract_rows<D, 2>(f, Q, tok, n, dk[u]);
+        pack_a<4>(pv, f);
+        contract_rows<DV, DV, 2>(f, oo, 0, dv);
       }
-      uint32_t f[2][4];
-      pack_a<4>(pv, f);
-      contract_rows<DV, 2>(f, O, tok, n, dv);
     }
+    __syncthreads();
   }
+  if (!on) return;
+  // the stages are free now; 16 rows of scratch per warp
+  const uint32_t scratch = base + S::Q + warp * kTile * DV * 2;
 #pragma unroll
   for (int u = 0; u < MAPS; ++u)
-    store_acc<D, D>(static_cast<bf16*>(a.dk), a.hkv, MAPS * hk + u, rg.x, vg, rg8.x, vg8, dk[u], a.scale, a.scale);
-  store_acc<D, DV>(static_cast<bf16*>(a.dv), a.hkv, MAPS * hk, rg.x, vg, rg8.x, vg8, dv, 1.f, 1.f);
+    store_acc<D, D>(scratch, dk[u], a.scale, a.scale, static_cast<bf16*>(a.dk), a.hkv, MAPS * hk + u, a.rows, first, nr);
+  store_acc<D, DV>(scratch, dv, 1.f, 1.f, static_cast<bf16*>(a.dv), a.hkv, MAPS * hk, a.rows, first, nr);
 }
 
-// tab2[h][o]: the bias of every offset in units of log2.
+// tab2[h][o]: the bias of every offset in units of log2, rows of a multiple of 4; clears amax and the
+// wide sums.
 __global__ void bias_expand_kernel(WinArgs a) {
-  const int T3 = offsets(a.m), o = blockIdx.x * blockDim.x + threadIdx.x;
-  if (o < T3) a.tab2[(size_t)blockIdx.y * T3 + o] = bias2_at(a, blockIdx.y, o);
+  const int T3 = offsets(a.m), T3p = table_pitch(a.m), o = blockIdx.x * blockDim.x + threadIdx.x;
+  if (o == 0) a.amax[blockIdx.y] = 0;
+  if (a.wide && o < T3) a.sums[(size_t)blockIdx.y * T3 + o] = 0;
+  if (o < T3p) a.tab2[(size_t)blockIdx.y * T3p + o] = o < T3 ? bias2_at(a, blockIdx.y, o) : 0.f;
 }
 
 template <int D, int MAPS, bool BIAS, typename E>
 cudaError_t bwd(const WinArgs& a, cudaStream_t st) {
-  const size_t T3 = BIAS ? offsets(a.m) : 0;
-  const size_t collect = a.dbias ? sizeof(float) * (T3 + 8 + (kDqWarps - 1) * kSlot) : 0;
-  size_t smem = sizeof(float) * T3 + collect;
-  auto dq = window_dq_mma_kernel<D, MAPS, BIAS ? 1 : 0, E>;
-  if (BIAS && smem > kSmemMost) {
-    dq = window_dq_mma_kernel<D, MAPS, BIAS ? 2 : 0, E>;
-    smem = collect;
-  }
-  if (smem > 47 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  const int heads = a.hq / MAPS, nc = a.dbias ? kDqWarps - 1 : kDqWarps;
-  const int need = (a.T + nc - 1) / nc;
-  int gx = a.dbias ? a.parts : (4 * 2 * 148 + heads - 1) / heads;
-  gx = !a.dbias && gx > need ? need : gx;
+  constexpr int ON = BIAS ? 1 : 0;
+  const size_t T3p = BIAS ? table_pitch(a.m) : 0;
   if (BIAS)
-    SSA_LAUNCH("bias_expand_kernel", bias_expand_kernel, dim3(((int)T3 + 255) / 256, a.hq), 256, 0, st, a);
-  SSA_LAUNCH("window_dq_mma_kernel", dq, dim3(gx, heads), 32 * kDqWarps, smem, st, a);
-  auto dkv = window_dkv_mma_kernel<D, MAPS, BIAS, E>;
-  SSA_LAUNCH("window_dkv_mma_kernel", dkv, dim3((a.T + kDkvWarps - 1) / kDkvWarps, a.hkv / MAPS), 32 * kDkvWarps, 0,
-             st, a);
+    SSA_LAUNCH("bias_expand_kernel", bias_expand_kernel, dim3(((int)T3p + 255) / 256, a.hq), 256, 0, st, a);
+  cudaError_t r = rows_pass<D, MAPS, BIAS, E, kStats>("window_stats_kernel", a, st);
+  if (r == cudaSuccess) r = rows_pass<D, MAPS, BIAS, E, kDq>("window_dq_kernel", a, st);
+  if (r != cudaSuccess) return r;
+  {
+    using K = DkvShape<D, MAPS>;
+    // three CTAs per SM (two for wide rows) while the tables fit beside them
+    const bool in_smem = K::tab + 2 * sizeof(float) * T3p <= (D * MAPS == 128 ? 113 : 75) * 1024;
+    const size_t smem = K::tab + (in_smem ? 2 * sizeof(float) * T3p : 0);
+    auto kern = in_smem ? window_dkv_mma_kernel<D, MAPS, ON, E> : window_dkv_mma_kernel<D, MAPS, 2 * ON, E>;
+    const cudaError_t e = need_smem(kern, smem);
+    if (e != cudaSuccess) return e;
+    SSA_LAUNCH("window_dkv_mma_kernel", kern, dim3(a.T, a.hkv / MAPS), 32 * kDkvWarps, smem, st, a);
+  }
   return cudaGetLastError();
 }
 
@@ -766,17 +905,36 @@ cudaError_t bwd_e(const WinArgs& a, cudaStream_t st) {
                      : bwd<128, 1, false, E>(a, st);
 }
 
-}  // namespace
-
-cudaError_t window_bwd_mma(const WinArgs& a, cudaStream_t st) {
-  return a.act8 ? bwd_e<int8_t>(a, st) : bwd_e<bf16>(a, st);
+// part[h][o]: the wide sums as floats; NaN where the head's dP or softmax had no finite bound.
+__global__ void bias_wide_kernel(WinArgs a) {
+  const int T3 = offsets(a.m), o = blockIdx.x * blockDim.x + threadIdx.x, h = blockIdx.y;
+  if (o >= T3) return;
+  const uint32_t amax = a.amax[h];
+  const double v = ldexp((double)(long long)a.sums[(size_t)h * T3 + o], -wide_bits(amax, a.N));
+  a.part[(size_t)h * T3 + o] = amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : (float)v;
 }
 
+}  // namespace
+
 cudaError_t window_fwd_mma(const WinArgs& a, cudaStream_t st) {
-  if (a.maps == 2) return a.d == 32 ? fwd<32, 2, false>(a, st) : fwd<64, 2, false>(a, st);
+  const char* name = "window_fwd_kernel";
+  if (a.maps == 2)
+    return a.d == 32 ? rows_pass<32, 2, false, bf16, kForward>(name, a, st)
+                     : rows_pass<64, 2, false, bf16, kForward>(name, a, st);
   if (a.table)
-    return a.d == 32 ? fwd<32, 1, true>(a, st) : a.d == 64 ? fwd<64, 1, true>(a, st) : fwd<128, 1, true>(a, st);
-  return a.d == 32 ? fwd<32, 1, false>(a, st) : a.d == 64 ? fwd<64, 1, false>(a, st) : fwd<128, 1, false>(a, st);
+    return a.d == 32   ? rows_pass<32, 1, true, bf16, kForward>(name, a, st)
+           : a.d == 64 ? rows_pass<64, 1, true, bf16, kForward>(name, a, st)
+                       : rows_pass<128, 1, true, bf16, kForward>(name, a, st);
+  return a.d == 32   ? rows_pass<32, 1, false, bf16, kForward>(name, a, st)
+         : a.d == 64 ? rows_pass<64, 1, false, bf16, kForward>(name, a, st)
+                     : rows_pass<128, 1, false, bf16, kForward>(name, a, st);
+}
+
+cudaError_t window_bwd_mma(const WinArgs& a, cudaStream_t st) {
+  const cudaError_t e = a.act8 ? bwd_e<int8_t>(a, st) : bwd_e<bf16>(a, st);
+  if (e == cudaSuccess && a.wide && a.dbias)
+    SSA_LAUNCH("bias_wide_kernel", bias_wide_kernel, dim3((offsets(a.m) + 255) / 256, a.hq), 256, 0, st, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace ssa

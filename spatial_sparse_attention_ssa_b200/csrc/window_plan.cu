@@ -45,29 +45,33 @@ __global__ void plan_rows_kernel(const int32_t* __restrict__ coords, int64_t N, 
   }
 }
 
-// One warp per cell: does it hold two tokens with one code?  A bitmap of the cell's m^3 voxels
-// (m <= 16); a cell with more tokens than voxels does without looking.
+// One warp per cell: the most tokens that one of its m^3 voxels holds (m <= 16, 16-bit counters,
+// so no more than 65535; a larger count can only come from as many tokens in the cell, which is
+// then taken instead).  Flags the cell's tiles where it is above one and keeps the maximum of all
+// cells in tiles[T].x.
 __global__ void plan_dup_kernel(int64_t N, int64_t W, int m, const int32_t* __restrict__ ptr,
-                                const int2* __restrict__ rows, int4* __restrict__ tiles) {
-  __shared__ uint32_t bits[4][128];
+                                const int2* __restrict__ rows, int4* __restrict__ tiles, int64_t T) {
+  __shared__ uint32_t count[4][2048];  // two voxels to a word
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int e = 2 * m - 1, vox = m * m * m;
+  const int e = 2 * m - 1, words = (m * m * m + 1) / 2;
   for (int64_t c = (int64_t)blockIdx.x * 4 + warp; c < W; c += (int64_t)gridDim.x * 4) {
     const int a = ptr[c], b = ptr[c + 1];
     if (a < 0 || b > N || b <= a) continue;  // reported by plan_rows_kernel
-    bool dup = b - a > vox;
-    if (!dup) {
-      for (int i = lane; i < 128; i += 32) bits[warp][i] = 0;
+    int most = b - a;
+    if (most > 1 && most <= 65535) {
+      for (int i = lane; i < words; i += 32) count[warp][i] = 0;
       __syncwarp();
+      most = 0;
       for (int i = a + lane; i < b; i += 32) {
         const int code = rows[i].y;
-        const int v = (code / (e * e) * m + code / e % e) * m + code % e;
-        dup |= (atomicOr(&bits[warp][v >> 5], 1u << (v & 31)) >> (v & 31)) & 1;
+        const int v = (code / (e * e) * m + code / e % e) * m + code % e, sh = 16 * (v & 1);
+        most = max(most, (int)((atomicAdd(&count[warp][v >> 1], 1u << sh) >> sh) & 65535u) + 1);
       }
-      dup = __any_sync(0xffffffffu, dup);
+      most = __reduce_max_sync(0xffffffffu, most);
       __syncwarp();
     }
-    if (dup) {
+    if (lane == 0) atomicMax(&tiles[T].x, most);
+    if (most > 1) {
       const int64_t slot = a / kTile + c, nt = (b - a + kTile - 1) / kTile;
       for (int64_t i = lane; i < nt; i += 32) tiles[slot + i].y |= kDupFlag;
     }
@@ -225,13 +229,13 @@ int blocks_for(int64_t threads, int per_block) {
 cudaError_t window_plan(const int32_t* coords, int64_t N, int m, const ssa_partition* part, int2* rows, int4* tiles,
                         int* status, cudaStream_t st) {
   const int64_t T = N / kTile + part->count;
-  cudaError_t e = cudaMemsetAsync(tiles, 0, sizeof(int4) * T, st);
+  cudaError_t e = cudaMemsetAsync(tiles, 0, sizeof(int4) * (T + 1), st);
   if (e != cudaSuccess) return e;
   SSA_LAUNCH("plan_rows_kernel", plan_rows_kernel, blocks_for(N, 256), 256, 0, st, coords, N, part->count, m, part->id,
              part->perm, part->ptr, rows, tiles, status);
   if (coords)
     SSA_LAUNCH("plan_dup_kernel", plan_dup_kernel, blocks_for(part->count, 4), 128, 0, st, N, part->count, m,
-               part->ptr, rows, tiles);
+               part->ptr, rows, tiles, T);
   return cudaGetLastError();
 }
 

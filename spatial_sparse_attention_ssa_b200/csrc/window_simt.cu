@@ -344,15 +344,26 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(WinArgs a) {
         for (int u = 0; u < MAPS; ++u)
           accum<D>(sm + L::P + u * kTile * kWStride, sm + L::B + u * kChunk * (D + 4), n, acc[u]);
         if (T3 && threadIdx.x < 32) {
-          const bool dup = tile.y & kDupFlag;
+          // keys of one voxel take turns, by their rank among the lanes that hold the voxel
+          const int lane = threadIdx.x, k0c = codes[lane], k1c = codes[32 + lane];
+          const bool v0 = lane < n, v1 = lane + 32 < n;
+          int r0 = 0, r1 = 0, most = 0;
+          if (tile.y & kDupFlag) {
+            const unsigned below = (1u << lane) - 1u;
+            r0 = __popc(__match_any_sync(0xffffffffu, v0 ? k0c : -1 - lane) & below);
+            r1 = __popc(__match_any_sync(0xffffffffu, v1 ? k1c : -1 - lane) & below);
+            most = __reduce_max_sync(0xffffffffu, max(r0, r1));
+          }
           for (int r = 0; r < nr; ++r) {
             const int cr = codes[kChunk + r] + c0;
-            for (int j = threadIdx.x; j < kChunk; j += 32) {
-              const float ds = sm[L::P + r * kWStride + j];
-              for (int one_lane = 0; one_lane < (dup ? 32 : 1); ++one_lane) {
-                if (j < n && (!dup || one_lane == (int)threadIdx.x)) dtab[cr - codes[j]] += ds;
-                __syncwarp();
-              }
+            const float* ds = sm + L::P + r * kWStride;
+            for (int i = 0; i <= most; ++i) {
+              if (v0 && r0 == i) dtab[cr - k0c] += ds[lane];
+              __syncwarp();
+            }
+            for (int i = 0; i <= most; ++i) {
+              if (v1 && r1 == i) dtab[cr - k1c] += ds[32 + lane];
+              __syncwarp();
             }
           }
         }

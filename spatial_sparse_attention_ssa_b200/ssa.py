@@ -610,7 +610,7 @@ class WindowPlan:
     """Work plan of one partition (see ssa_win_plan in include/ssa.h): made once per voxel
     set, read by every layer and both passes of the window and differential calls."""
     rows: torch.Tensor   # int32 [n, 2]
-    tiles: torch.Tensor  # int32 [n // 16 + count, 4]
+    tiles: torch.Tensor  # int32 [n // 16 + count + 1, 4]
     n: int
     count: int
     m: int
@@ -629,7 +629,7 @@ def ssa_window_plan(coords: torch.Tensor | None, win: Bins, m: int = 0) -> Windo
     if coords is not None:
         _want(coords, (n, 3), torch.int32, "coords")
     e = lambda *s: torch.empty(*s, dtype=torch.int32, device=dev)  # noqa: E731
-    plan = WindowPlan(e(n, 2), e(n // WINDOW_TILE + win.count, 4), n, int(win.count), int(m) if coords is not None else 0)
+    plan = WindowPlan(e(n, 2), e(n // WINDOW_TILE + win.count + 1, 4), n, int(win.count), int(m) if coords is not None else 0)
     pb = win.c()
     _call(dev, "ssa_window_plan", _ptr(coords), n, int(m), ctypes.byref(pb), plan._ref)
     return plan

@@ -130,6 +130,8 @@ def test_plan_rows_tiles_and_flags():
     assert np.array_equal(rows[:, 0], perm)
     c = coords[perm] % 5
     assert np.array_equal(rows[:, 1], (c[:, 0] * 9 + c[:, 1]) * 9 + c[:, 2])
+    assert tiles[-1].tolist() == [2, 0, 0, 0]     # the most tokens of a voxel
+    tiles = tiles[:-1]
     live = tiles[(tiles[:, 1] & 65535) > 0]
     covered = np.concatenate([np.arange(t[0], t[0] + (t[1] & 65535)) for t in live])
     assert np.array_equal(np.sort(covered), np.arange(len(coords)))
