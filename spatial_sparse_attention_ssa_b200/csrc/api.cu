@@ -773,7 +773,8 @@ ssa::WinArgs window_args(const ssa_window_params* p, const ssa_win_plan* plan, i
 }
 
 // Workspace of the backward: lse2 and D per query head and row, partial bias gradients.
-size_t carve_window(void* base, const ssa_window_params* p, const ssa_win_plan* plan, int maps, ssa::WinArgs* a) {
+size_t carve_window(void* base, const ssa_window_params* p, const ssa_win_plan* plan, int maps, bool act8,
+                    ssa::WinArgs* a) {
   Carver c(base);
   const int e = 2 * plan->m - 1;
   const int64_t T = plan->n / SSA_WINDOW_TILE + plan->count;
@@ -786,7 +787,13 @@ size_t carve_window(void* base, const ssa_window_params* p, const ssa_win_plan* 
   float* tab2 = c.take<float>(tab ? tab + 3 * (size_t)p->hq : 0);  // rows of a multiple of 4
   unsigned* amax = c.take<unsigned>(p->hq);
   unsigned long long* sums = c.take<unsigned long long>(wide ? tab : 0);
+  // K and V of 8-bit checkpoints as bf16 (the bf16 kernels read them once per query head)
+  const size_t kv = act8 && p->dtype == SSA_DTYPE_BF16 ? (size_t)p->hkv * plan->n * p->d : 0;
+  uint16_t* k16 = c.take<uint16_t>(kv);
+  uint16_t* v16 = c.take<uint16_t>(kv);
   if (a) {
+    a->k16 = k16;
+    a->v16 = v16;
     a->lse2 = lse2;
     a->D = D;
     a->part = part;
@@ -820,14 +827,22 @@ ssa_status window_backward(const ssa_window_params* p, const ssa_win_plan* plan,
   for (const void* x : {a.q, a.k, a.v, dout, (const void*)dq, (const void*)dk, (const void*)dv})
     if (!x || !aligned16(x)) return SSA_ERR_INVALID_ARG;
   if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0) return SSA_ERR_INVALID_ARG;
-  if (ws_bytes < carve_window(ws, p, plan, maps, &a)) return SSA_ERR_WORKSPACE;
+  if (ws_bytes < carve_window(ws, p, plan, maps, act8 != nullptr, &a)) return SSA_ERR_WORKSPACE;
   a.dout = dout;
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
   a.dbias = dbias;
   a.dlam = dlam;
-  cudaError_t e = a.dtype == SSA_DTYPE_BF16 ? ssa::window_bwd_mma(a, st) : ssa::window_bwd_simt(a, st);
+  cudaError_t e = cudaSuccess;
+  if (act8 && a.dtype == SSA_DTYPE_BF16) {
+    const int64_t rows = a.N * p->hkv;
+    e = ssa::act8_unpack(a.dtype, rows, a.d, act8[1].codes, act8[1].scale, a.k16, st);
+    if (e == cudaSuccess) e = ssa::act8_unpack(a.dtype, rows, a.d, act8[2].codes, act8[2].scale, a.v16, st);
+    a.k = a.k16;
+    a.v = a.v16;
+  }
+  if (e == cudaSuccess) e = a.dtype == SSA_DTYPE_BF16 ? ssa::window_bwd_mma(a, st) : ssa::window_bwd_simt(a, st);
   if (e == cudaSuccess) e = ssa::window_param_grads(a, st);
   return cuda_status(e);
 }
@@ -858,7 +873,7 @@ SSA_API ssa_status ssa_window_plan(const int32_t* coords, int64_t N, int32_t m, 
 SSA_API size_t ssa_window_workspace_size(int32_t op, const ssa_window_params* p, const ssa_win_plan* plan) {
   const int maps = op == SSA_OP_WINDOW_BACKWARD ? 1 : op == SSA_OP_DIFF_BACKWARD ? 2 : 0;
   if (!maps || check_window(p, plan, maps) != SSA_OK) return 0;
-  return carve_window(nullptr, p, plan, maps, nullptr);
+  return carve_window(nullptr, p, plan, maps, true, nullptr);
 }
 
 SSA_API ssa_status ssa_window_forward(const ssa_window_params* p, const ssa_win_plan* plan,

@@ -175,6 +175,7 @@ struct WinArgs {
   float* part;      // [hq][parts][offsets] partial bias gradients
   int parts;
   float* tab2;      // [hq][offsets] the bias by offset, in units of log2
+  void *k16, *v16;  // 8-bit checkpoints: room for K and V as bf16
   unsigned* amax;   // [hq] the largest |dP| of a head, as bits
   int wide;         // bf16 and an edge from kWideEdge on: one part, summed in `sums`
   unsigned long long* sums;  // [hq][offsets]

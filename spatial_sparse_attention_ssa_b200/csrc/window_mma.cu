@@ -115,18 +115,34 @@ __device__ __forceinline__ void put(uint32_t dst, const Rows<E, D>& src, int r, 
   }
 }
 
-// Rows first .. first + n - 1 of the cell order to a tile of `total` rows (zeros past n), by
-// `threads` threads.
-template <int D, int W, typename E>
-__device__ __forceinline__ void stage(uint32_t dst, const Rows<E, D>& src, const int2* __restrict__ rows, int first,
-                                      int n, int total, int tid, int threads) {
-  constexpr int U = W / 8;
-  for (int i = tid; i < total * U; i += threads) {
-    const int r = i / U;
-    const size_t row = (size_t)__ldg(&rows[first + min(r, n - 1)].x) * src.heads + src.head;
-    put<D, W>(dst, src, r, i % U, row, r < n);
+// Rows first .. first + n - 1 of the cell order (n <= ROWS) to the rows of a staged tile, zeros past
+// n, by THREADS threads; one or two tensors of the same heads at once.  Position of row k: at(k).
+// `seen(k, row entry)` is called by one thread per row.  Unrolled: a unit costs its copy and
+// address and little else.
+template <int D, int W, int ROWS, int THREADS, bool TWO, typename E, typename E2, typename At, typename Seen>
+__device__ __forceinline__ void stage(uint32_t dst, const Rows<E, D>& src, uint32_t dst2, const Rows<E2, D>& src2,
+                                      const int2* __restrict__ rows, int first, int n, int tid, At at, Seen seen) {
+  constexpr int U = W / 8, STEP = THREADS / U, IT = (ROWS + STEP - 1) / STEP;
+  static_assert(ROWS % STEP == 0, "whole steps");
+  const int r = tid / U, c = tid % U;
+  int2 e[IT];
+#pragma unroll
+  for (int i = 0; i < IT; ++i) e[i] = __ldg(&rows[first + min(i * STEP + r, n - 1)]);
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int k = i * STEP + r, p = at(k);
+    const size_t row = (size_t)e[i].x * src.heads + src.head;
+    put<D, W>(dst, src, p, c, row, k < n);
+    if constexpr (TWO) put<D, W>(dst2, src2, p, c, row, k < n);
+    if (c == 0) seen(p, e[i]);
   }
 }
+struct SameRow {
+  __device__ __forceinline__ int operator()(int k) const { return k; }
+};
+struct NoCode {
+  __device__ __forceinline__ void operator()(int, const int2&) const {}
+};
 
 // A operand, k-step k, from a tile of 16 rows starting at row r0 of a staged tile.
 template <int W>
@@ -184,12 +200,15 @@ __device__ __forceinline__ void store_acc(uint32_t scratch, float (*acc)[4], flo
          pack_bf16x2(acc[2 * e][2] * f8, acc[2 * e][3] * f8), pack_bf16x2(acc[2 * e + 1][0] * f, acc[2 * e + 1][1] * f),
          pack_bf16x2(acc[2 * e + 1][2] * f8, acc[2 * e + 1][3] * f8));
   __syncwarp();
+  const int r0 = lane / U, c = lane % U;
+  int tok[U / 2];
+#pragma unroll
+  for (int i = 0; i < U / 2; ++i) tok[i] = __ldg(&rows[first + min(r0 + i * (32 / U), nr - 1)].x);
 #pragma unroll
   for (int i = 0; i < U / 2; ++i) {
-    const int r = (32 * i + lane) / U, c = (32 * i + lane) % U;
+    const int r = r0 + i * (32 / U);
     if (r < nr)
-      *reinterpret_cast<uint4*>(out + ((size_t)__ldg(&rows[first + r].x) * heads + head) * D + 8 * c) =
-          lds16(scratch + unit<W>(r, c));
+      *reinterpret_cast<uint4*>(out + ((size_t)tok[i] * heads + head) * D + 8 * c) = lds16(scratch + unit<W>(r, c));
   }
 }
 
@@ -295,20 +314,11 @@ __device__ __forceinline__ void add_bias_grad(const F& add, float (*ds)[4], cons
 // 8 j + 2 t + x of 32 holds key 8 t + 2 j + x, so that the four lanes that share a row in a
 // fragment (t) hold keys eight apart.  Neighbours in the cell are neighbours in the voxel grid, so
 // without this such lanes would often hit one offset in one instruction (see add_bias_grad).
+// (The map is its own inverse.)
 __device__ __forceinline__ int key_at(int p) { return (p & 33) | (p & 6) << 2 | (p & 24) >> 2; }
-
-// Rows first .. first + n - 1 of the cell order to a tile of 64 keys in that order.
-template <int D, int W, typename E>
-__device__ __forceinline__ void stage_keys(uint32_t dst, const Rows<E, D>& src, const int2* __restrict__ rows, int first,
-                                           int n, int tid, int threads) {
-  constexpr int U = W / 8;
-  const int total = n > 32 ? kChunk : 32;
-  for (int i = tid; i < total * U; i += threads) {
-    const int p = i / U, c = i % U, k = key_at(p);
-    const size_t row = (size_t)__ldg(&rows[first + min(k, n - 1)].x) * src.heads + src.head;
-    put<D, W>(dst, src, p, c, row, k < n);
-  }
-}
+struct KeyOrder {
+  __device__ __forceinline__ int operator()(int k) const { return key_at(k); }
+};
 
 // s = s mul + bias in units of log2 for the 32 positions of a half chunk, minus infinity where
 // the key is not below `left`.  t0, t8: the head's table of offsets at the codes of rows g, g + 8
@@ -417,8 +427,8 @@ __global__ void __launch_bounds__(32 * Shape<D, MAPS, MODE>::TW* Shape<D, MAPS, 
     lam = e1 - e2 + a.lam_init;
   }
   const Rows<E, D> Q = {static_cast<const E*>(a.q), a.sq, a.hq, MAPS * h};
-  const Rows<E, D> K = {static_cast<const E*>(a.k), a.sk, a.hkv, MAPS * hk};
-  const Rows<E, D> V = {static_cast<const E*>(a.v), a.sv, a.hkv, MAPS * hk};
+  const Rows<bf16, D> K = {static_cast<const bf16*>(a.k), nullptr, a.hkv, MAPS * hk};
+  const Rows<bf16, D> V = {static_cast<const bf16*>(a.v), nullptr, a.hkv, MAPS * hk};
   const Rows<bf16, D> O = {static_cast<const bf16*>(a.dout), nullptr, a.hq, MAPS * h};
   uint32_t top = 0;  // the largest |dP|, as bits: NaN above all
   for (int t = blockIdx.x * NT + team; t < a.T; t += gridDim.x * NT) {
@@ -446,8 +456,7 @@ __global__ void __launch_bounds__(32 * Shape<D, MAPS, MODE>::TW* Shape<D, MAPS, 
       for (int e = 0; e < NACC; ++e) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
       if (on) {
         __syncwarp();
-        stage<D, DV>(scratch, Q, a.rows, first, nr, kTile, lane, 32);
-        if (MODE != kForward) stage<D, DV>(scratch2, O, a.rows, first, nr, kTile, lane, 32);
+        stage<D, DV, kTile, 32, MODE != kForward>(scratch, Q, scratch2, O, a.rows, first, nr, lane, SameRow(), NoCode());
         if (BIAS) {
           ci = __ldg(&a.rows[first + min(g, nr - 1)].y) + c0;
           ci8 = __ldg(&a.rows[first + min(g + 8, nr - 1)].y) + c0;
@@ -472,10 +481,14 @@ __global__ void __launch_bounds__(32 * Shape<D, MAPS, MODE>::TW* Shape<D, MAPS, 
           const int n = min(kChunk, hi - k0);
           if (!one || (w < TW && pass == 0)) {
             team_sync<TW>(team);
-            stage_keys<D, DV>(keys, K, a.rows, k0, n, tid, 32 * TW);
-            stage_keys<D, DV>(vals, V, a.rows, k0, n, tid, 32 * TW);
-            if (BIAS)
-              for (int i = tid; i < kChunk; i += 32 * TW) codes[i] = __ldg(&a.rows[k0 + min(key_at(i), n - 1)].y);
+#pragma unroll 1
+            for (int x = 0; x < n; x += 32) {
+              const uint32_t off = x * DV * 2;
+              stage<D, DV, 32, 32 * TW, true>(keys + off, K, vals + off, V, a.rows, k0 + x, min(32, n - x), tid, KeyOrder(),
+                                              [&](int p, const int2& e) {
+                                                if (BIAS) codes[x + p] = e.y;
+                                              });
+            }
             cp_commit();
             cp_wait<0>();
             team_sync<TW>(team);
@@ -717,40 +730,42 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
   if (nt == 0) return;
   // K and V stay before the stages, or are in the second stage until it is needed
   const uint32_t base = tc::smem_u32(sm), kt = base + (S::held ? S::stage : 0), vt = kt + S::KT;
-  const int chunks = (hi - lo + kChunk - 1) / kChunk, steps = G * chunks;
   const int keys0 = tile.x, nkeys = min(kTile * nt, hi - keys0);
 
-  // step s: query head hk G + s / chunks, queries from lo + 64 (s % chunks)
-  auto load = [&](int s) {
-    const int h = hk * G + s / chunks, k0 = lo + kChunk * (s % chunks), n = min(kChunk, hi - k0);
-    const int total = (n + 31) & ~31;
-    const uint32_t st = base + S::Q + (s & 1) * S::stage;
-    stage<D, DV>(st, Rows<E, D>{static_cast<const E*>(a.q), a.sq, a.hq, MAPS * h}, a.rows, k0, n, total, tid, NTH);
-    stage<D, DV>(st + S::KT, Rows<bf16, D>{static_cast<const bf16*>(a.dout), nullptr, a.hq, MAPS * h}, a.rows, k0, n,
-                 total, tid, NTH);
-    float* stat = reinterpret_cast<float*>(sm + S::Q + (s & 1) * S::stage + S::stat);
-    for (int i = tid; i < 2 * MAPS * kChunk; i += NTH) {
-      const int u = i / (2 * kChunk), which = i / kChunk & 1, q = i % kChunk;
-      const size_t at = (size_t)(MAPS * h + u) * a.N + k0 + q;
-      stat[i] = q >= n ? (which ? 0.f : kPosInf) : which ? a.D[at] : a.lse2[at];
+  // a step: query head h, 64 queries from k0 on, into stage `st`; a head's first step brings its table
+  auto load = [&](int h, int k0, int st) {
+    const int n = min(kChunk, hi - k0);
+    const uint32_t q = base + S::Q + st * S::stage;
+    int* codes = reinterpret_cast<int*>(sm + S::codes) + st * kChunk;
+    const Rows<E, D> Q = {static_cast<const E*>(a.q), a.sq, a.hq, MAPS * h};
+    const Rows<bf16, D> O = {static_cast<const bf16*>(a.dout), nullptr, a.hq, MAPS * h};
+#pragma unroll 1
+    for (int x = 0; x < n; x += 32) {
+      const uint32_t off = x * DV * 2;
+      stage<D, DV, 32, NTH, true>(q + off, Q, q + S::KT + off, O, a.rows, k0 + x, min(32, n - x), tid, SameRow(),
+                                  [&](int p, const int2& e) {
+                                    if (BIAS) codes[x + p] = e.y + c0;
+                                  });
     }
-    if (BIAS) {
-      int* codes = reinterpret_cast<int*>(sm + S::codes) + (s & 1) * kChunk;
-      if (tid < kChunk) codes[tid] = __ldg(&a.rows[k0 + min(tid, n - 1)].y) + c0;
+    float* stat = reinterpret_cast<float*>(sm + S::Q + st * S::stage + S::stat);
+#pragma unroll
+    for (int i = 0; i < MAPS; ++i) {  // 64 threads a row of lse2, 64 a row of D
+      const int u = i, which = tid / kChunk, c = tid % kChunk;
+      const float* src = (which ? a.D : a.lse2) + (size_t)(MAPS * h + u) * a.N + k0;
+      stat[(2 * u + which) * kChunk + c] = c < n ? src[c] : which ? 0.f : kPosInf;
     }
-    if (TAB == 1 && s % chunks == 0) {
-      const uint32_t dst = base + S::tab + (s / chunks & 1) * T3p * 4;
+    if (TAB == 1 && k0 == lo) {
+      const uint32_t dst = base + S::tab + (h & 1) * T3p * 4;
       const float* src = a.tab2 + (size_t)h * T3p;
       for (int i = tid; i < T3p / 4; i += NTH) cp16(dst + 16 * i, src + 4 * i, true);
     }
     cp_commit();
   };
 
-  stage<D, DV>(kt, Rows<E, D>{static_cast<const E*>(a.k), a.sk, a.hkv, MAPS * hk}, a.rows, keys0, nkeys, kTile * nt, tid,
-               NTH);
-  stage<D, DV>(vt, Rows<E, D>{static_cast<const E*>(a.v), a.sv, a.hkv, MAPS * hk}, a.rows, keys0, nkeys, kTile * nt, tid,
-               NTH);
-  load(0);
+  const Rows<bf16, D> K = {static_cast<const bf16*>(a.k), nullptr, a.hkv, MAPS * hk};
+  const Rows<bf16, D> V = {static_cast<const bf16*>(a.v), nullptr, a.hkv, MAPS * hk};
+  stage<D, DV, kChunk, NTH, true>(kt, K, vt, V, a.rows, keys0, nkeys, tid, SameRow(), NoCode());
+  load(hk * G, lo, 0);
   const int r0 = kTile * warp, first = keys0 + r0, nr = min(kTile, hi - first);
   const bool on = warp < nt;
   int ck = 0, ck8 = 0;
@@ -777,27 +792,31 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
     __syncthreads();
   }
 
-  for (int s = 0; s < steps; ++s) {
-    if (s + 1 < steps) {
-      load(s + 1);
+  int h = hk * G, k0 = lo, stg = 0;
+  while (true) {
+    int h2 = h, k2 = k0 + kChunk;  // the step after this one
+    if (k2 >= hi) k2 = lo, ++h2;
+    const bool more = h2 < hk * G + G;
+    if (more) {
+      load(h2, k2, stg ^ 1);
       cp_wait<1>();
     } else {
       cp_wait<0>();
     }
     __syncthreads();
     if (on) {
-      const int h = hk * G + s / chunks, n = min(kChunk, hi - lo - kChunk * (s % chunks));
+      const int n = min(kChunk, hi - k0);
       float lam = 0.f;
       if constexpr (MAPS == 2) {
         float e1, e2;
         lambda_terms<D>(a.lam, a.hq / 2, h, e1, e2);
         lam = e1 - e2 + a.lam_init;
       }
-      const uint32_t qt = base + S::Q + (s & 1) * S::stage, ot = qt + S::KT;
-      const float* stat = reinterpret_cast<const float*>(sm + S::Q + (s & 1) * S::stage + S::stat);
-      const int* codes = reinterpret_cast<const int*>(sm + S::codes) + (s & 1) * kChunk;
+      const uint32_t qt = base + S::Q + stg * S::stage, ot = qt + S::KT;
+      const float* stat = reinterpret_cast<const float*>(sm + S::Q + stg * S::stage + S::stat);
+      const int* codes = reinterpret_cast<const int*>(sm + S::codes) + stg * kChunk;
       const float* tab = TAB == 2 ? a.tab2 + (size_t)h * T3p
-                                  : reinterpret_cast<const float*>(sm + S::tab) + (s / chunks & 1) * T3p;
+                                  : reinterpret_cast<const float*>(sm + S::tab) + (h & 1) * T3p;
       const float *tk = tab - ck, *tk8 = tab - ck8;
 #pragma unroll 1
       for (int q0 = 0; q0 < n; q0 += 32) {
@@ -852,6 +871,10 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
       }
     }
     __syncthreads();
+    if (!more) break;
+    h = h2;
+    k0 = k2;
+    stg ^= 1;
   }
   if (!on) return;
   // the stages are free now; 16 rows of scratch per warp
