@@ -779,7 +779,7 @@ size_t carve_window(void* base, const ssa_window_params* p, const ssa_win_plan* 
   const int e = 2 * plan->m - 1;
   const int64_t T = plan->n / SSA_WINDOW_TILE + plan->count;
   const int wide = p->dtype == SSA_DTYPE_BF16 && plan->m >= ssa::kWideEdge;
-  const int parts = wide ? 1 : ssa::window_parts(p->hq, T, plan->m);
+  const int parts = wide ? 1 : ssa::window_parts(p->hq, T);
   float* lse2 = c.take<float>((size_t)p->hq * plan->n);
   float* D = c.take<float>((size_t)p->hq * plan->n);
   const size_t tab = maps == 1 && plan->m > 0 ? (size_t)p->hq * e * e * e : 0;
@@ -787,11 +787,15 @@ size_t carve_window(void* base, const ssa_window_params* p, const ssa_win_plan* 
   float* tab2 = c.take<float>(tab ? tab + 3 * (size_t)p->hq : 0);  // rows of a multiple of 4
   unsigned* amax = c.take<unsigned>(p->hq);
   unsigned long long* sums = c.take<unsigned long long>(wide ? tab : 0);
-  // K and V of 8-bit checkpoints as bf16 (the bf16 kernels read them once per query head)
-  const size_t kv = act8 && p->dtype == SSA_DTYPE_BF16 ? (size_t)p->hkv * plan->n * p->d : 0;
+  // the rows of 8-bit checkpoints as bf16: the bf16 kernels read them several times, K and V once
+  // per query head
+  const size_t q_values = act8 && p->dtype == SSA_DTYPE_BF16 ? (size_t)p->hq * plan->n * p->d : 0;
+  const size_t kv = q_values / p->hq * p->hkv;
+  uint16_t* q16 = c.take<uint16_t>(q_values);
   uint16_t* k16 = c.take<uint16_t>(kv);
   uint16_t* v16 = c.take<uint16_t>(kv);
   if (a) {
+    a->q16 = q16;
     a->k16 = k16;
     a->v16 = v16;
     a->lse2 = lse2;
@@ -839,6 +843,8 @@ ssa_status window_backward(const ssa_window_params* p, const ssa_win_plan* plan,
     const int64_t rows = a.N * p->hkv;
     e = ssa::act8_unpack(a.dtype, rows, a.d, act8[1].codes, act8[1].scale, a.k16, st);
     if (e == cudaSuccess) e = ssa::act8_unpack(a.dtype, rows, a.d, act8[2].codes, act8[2].scale, a.v16, st);
+    if (e == cudaSuccess) e = ssa::act8_unpack(a.dtype, a.N * p->hq, a.d, act8[0].codes, act8[0].scale, a.q16, st);
+    a.q = a.q16;
     a.k = a.k16;
     a.v = a.v16;
   }

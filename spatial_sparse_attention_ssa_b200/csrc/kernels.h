@@ -162,7 +162,7 @@ struct WinArgs {
   int nb;
   const float* lam;  // [4, hq / 2, d] (maps = 2)
   float lam_init;
-  int act8;  // q, k, v are int8 codes with the row scales below
+  int act8;  // q, k, v are int8 codes with the row scales below (the fp32 kernels)
   const void *q, *k, *v;
   const float *sq, *sk, *sv;
   void* out;
@@ -175,7 +175,7 @@ struct WinArgs {
   float* part;      // [hq][parts][offsets] partial bias gradients
   int parts;
   float* tab2;      // [hq][offsets] the bias by offset, in units of log2
-  void *k16, *v16;  // 8-bit checkpoints: room for K and V as bf16
+  void *q16, *k16, *v16;  // 8-bit checkpoints: room for their rows as bf16
   unsigned* amax;   // [hq] the largest |dP| of a head, as bits
   int wide;         // bf16 and an edge from kWideEdge on: one part, summed in `sums`
   unsigned long long* sums;  // [hq][offsets]
@@ -186,7 +186,7 @@ cudaError_t window_plan(const int32_t* coords, int64_t N, int m, const ssa_parti
 // offset are 157 KB, too many beside a team's rows in shared memory.
 constexpr int kWideEdge = 14;
 // Partial bias gradients per head that the backward keeps (rows of `part`).
-int window_parts(int hq, int64_t T, int m);
+int window_parts(int hq, int64_t T);
 cudaError_t window_fwd_simt(const WinArgs& a, cudaStream_t st);
 cudaError_t window_bwd_simt(const WinArgs& a, cudaStream_t st);
 // bf16 on warp-level MMAs

@@ -20,6 +20,7 @@ using bf16 = __nv_bfloat16;
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kChunk = 64;
+constexpr float kSlack = 8.f;
 constexpr size_t kSmemMost = 226 * 1024;  // dynamic shared memory of a CTA, beside the barriers
 
 __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -69,22 +70,9 @@ __device__ __forceinline__ uint4 lds16(uint32_t src) {
   return v;
 }
 
-// Four 8-bit codes (as in an int) to bf16 values times s: the byte + 128 in the low mantissa bits
-// of 2^23 is an exact float, so are the difference and the product with a power of two.
-__device__ __forceinline__ uint2 codes4(uint32_t w, float s) {
-  w ^= 0x80808080u;
-  float f[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    f[i] = (__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + i)) - 8388736.f) * s;
-  return make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-}
-
 // Rows of a tensor [n, heads, D] from head `head` on.
-template <typename E, int D>
 struct Rows {
-  const E* p;
-  const float* s;  // row scales (8-bit rows)
+  const void* p;
   int heads, head;
 };
 
@@ -97,30 +85,12 @@ __device__ __forceinline__ uint32_t unit(int row, int c) {
   return 16u * (uint32_t)(row * U + (c ^ f));
 }
 
-// Unit c of a row to row r of a staged tile, zeros where `on` is off; asynchronous for bf16
-// (cp_commit and cp_wait are the caller's).
-template <int D, int W, typename E>
-__device__ __forceinline__ void put(uint32_t dst, const Rows<E, D>& src, int r, int c, size_t row, bool on) {
-  if constexpr (sizeof(E) == 2) {
-    cp16(dst + unit<W>(r, c), src.p + row * D + 8 * c, on);
-  } else {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (on) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(src.p + row * D + 8 * c));
-      const float f = __ldg(src.s + row + 8 * c / D);
-      const uint2 x = codes4(w.x, f), y = codes4(w.y, f);
-      v = make_uint4(x.x, x.y, y.x, y.y);
-    }
-    sts16(dst + unit<W>(r, c), v);
-  }
-}
-
 // Rows first .. first + n - 1 of the cell order (n <= ROWS) to the rows of a staged tile, zeros past
 // n, by THREADS threads; one or two tensors of the same heads at once.  Position of row k: at(k).
 // `seen(k, row entry)` is called by one thread per row.  Unrolled: a unit costs its copy and
 // address and little else.
-template <int D, int W, int ROWS, int THREADS, bool TWO, typename E, typename E2, typename At, typename Seen>
-__device__ __forceinline__ void stage(uint32_t dst, const Rows<E, D>& src, uint32_t dst2, const Rows<E2, D>& src2,
+template <int D, int W, int ROWS, int THREADS, bool TWO, typename At, typename Seen>
+__device__ __forceinline__ void stage(uint32_t dst, const Rows& src, uint32_t dst2, const Rows& src2,
                                       const int2* __restrict__ rows, int first, int n, int tid, At at, Seen seen) {
   constexpr int U = W / 8, STEP = THREADS / U, IT = (ROWS + STEP - 1) / STEP;
   static_assert(ROWS % STEP == 0, "whole steps");
@@ -131,9 +101,9 @@ __device__ __forceinline__ void stage(uint32_t dst, const Rows<E, D>& src, uint3
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
     const int k = i * STEP + r, p = at(k);
-    const size_t row = (size_t)e[i].x * src.heads + src.head;
-    put<D, W>(dst, src, p, c, row, k < n);
-    if constexpr (TWO) put<D, W>(dst2, src2, p, c, row, k < n);
+    const size_t at_row = ((size_t)e[i].x * src.heads + src.head) * D + 8 * c;
+    cp16(dst + unit<W>(p, c), static_cast<const bf16*>(src.p) + at_row, k < n);
+    if constexpr (TWO) cp16(dst2 + unit<W>(p, c), static_cast<const bf16*>(src2.p) + at_row, k < n);
     if (c == 0) seen(p, e[i]);
   }
 }
@@ -359,10 +329,36 @@ __device__ __forceinline__ void team_sync(int team) {
 template <int TW>
 __device__ __forceinline__ int team_tiles(const int4& tile) {
   if ((tile.y & (kDupFlag - 1)) == 0) return 0;
-  const int at = (tile.x - tile.z) / kTile, all = (tile.w - tile.z + kTile - 1) / kTile;
+  const int at = (unsigned)(tile.x - tile.z) / kTile, all = (unsigned)(tile.w - tile.z + kTile - 1) / kTile;
   if (tile.w - tile.z <= kChunk) return at == 0 ? all : 0;
   return at % TW == 0 ? min(TW, all - at) : 0;
 }
+
+// The slots start, start + step, .. that hold work for a team, with tile.y the number of its tiles.
+// The warp reads 32 slots at once: most are empty or belong to another slot's team.
+template <int TW>
+struct Slots {
+  const int4* tiles;
+  int T, at, step;
+  int4 mine;
+  unsigned left = 0;
+  __device__ __forceinline__ Slots(const WinArgs& a, int start, int step_) : tiles(a.tiles), T(a.T), at(start), step(step_) {}
+  __device__ __forceinline__ bool next(int4& tile) {
+    while (left == 0) {
+      if (at >= T) return false;
+      const int64_t t = at + (int64_t)(threadIdx.x & 31) * step;
+      mine = t < T ? __ldg(&tiles[t]) : make_int4(0, 0, 0, 0);
+      mine.y = team_tiles<TW>(mine);
+      left = __ballot_sync(kFull, mine.y > 0);
+      at = (int)min((int64_t)T, at + (int64_t)32 * step);
+    }
+    const int i = __ffs(left) - 1;
+    left &= left - 1;
+    tile = make_int4(__shfl_sync(kFull, mine.x, i), __shfl_sync(kFull, mine.y, i), __shfl_sync(kFull, mine.z, i),
+                     __shfl_sync(kFull, mine.w, i));
+    return true;
+  }
+};
 
 // What a walk over the rows does with the keys.
 enum { kForward, kStats, kDq };
@@ -388,7 +384,7 @@ struct Shape {
 // One kernel body for the forward, the row statistics of the backward, and dq with the bias
 // gradient: they share the walk over cells, keys and scores.  TAB: where the bias is read: 0 no
 // bias, 1 shared memory, 2 global memory.  E: type of q, k, v.
-template <int D, int MAPS, int TAB, typename E, int MODE>
+template <int D, int MAPS, int TAB, int MODE>
 __global__ void __launch_bounds__(32 * Shape<D, MAPS, MODE>::TW* Shape<D, MAPS, MODE>::teams,
                                   Shape<D, MAPS, MODE>::resident) window_rows_kernel(WinArgs a) {
   using S = Shape<D, MAPS, MODE>;
@@ -426,15 +422,13 @@ __global__ void __launch_bounds__(32 * Shape<D, MAPS, MODE>::TW* Shape<D, MAPS, 
     lambda_terms<D>(a.lam, a.hq / 2, h, e1, e2);
     lam = e1 - e2 + a.lam_init;
   }
-  const Rows<E, D> Q = {static_cast<const E*>(a.q), a.sq, a.hq, MAPS * h};
-  const Rows<bf16, D> K = {static_cast<const bf16*>(a.k), nullptr, a.hkv, MAPS * hk};
-  const Rows<bf16, D> V = {static_cast<const bf16*>(a.v), nullptr, a.hkv, MAPS * hk};
-  const Rows<bf16, D> O = {static_cast<const bf16*>(a.dout), nullptr, a.hq, MAPS * h};
+  const Rows Q = {a.q, a.hq, MAPS * h}, O = {a.dout, a.hq, MAPS * h};
+  const Rows K = {a.k, a.hkv, MAPS * hk}, V = {a.v, a.hkv, MAPS * hk};
   uint32_t top = 0;  // the largest |dP|, as bits: NaN above all
-  for (int t = blockIdx.x * NT + team; t < a.T; t += gridDim.x * NT) {
-    const int4 tile = __ldg(&a.tiles[t]);
-    const int lo = tile.z, hi = tile.w, nt = team_tiles<TW>(tile);
-    if (nt == 0) continue;
+  Slots<TW> slots(a, blockIdx.x * NT + team, gridDim.x * NT);
+  int4 tile;
+  while (slots.next(tile)) {
+    const int lo = tile.z, hi = tile.w, nt = tile.y;
     const bool one = hi - lo <= kChunk;
     for (int w = wt; w < (nt + TW - 1) / TW * TW; w += TW) {  // every warp of the team, for its barriers
       const bool on = w < nt;
@@ -541,7 +535,9 @@ __global__ void __launch_bounds__(32 * Shape<D, MAPS, MODE>::TW* Shape<D, MAPS, 
                 contract_rows<DV, D, 2>(f, kt, u * D / 8, acc + u * D / 8);
               }
             } else {
-              // online maximum, sum (and sum of p dP) of a row; the sums stay per lane to the end
+              // online maximum, sum (and sum of p dP) of a row; the sums stay per lane to the end.  The
+              // subtracted maximum follows the true one only once that has grown by a factor of
+              // 2^kSlack, so that sums and products are rarely rescaled
               float old[MAPS][2];
 #pragma unroll
               for (int u = 0; u < MAPS; ++u)
@@ -559,6 +555,7 @@ __global__ void __launch_bounds__(32 * Shape<D, MAPS, MODE>::TW* Shape<D, MAPS, 
 #pragma unroll
                   for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(s[u][j][2 * i], s[u][j][2 * i + 1]));
                   mx = quad_max(mx);
+                  if (!(mx > m[u][i] + kSlack)) mx = m[u][i];
                   const float ms = safe_max(mx);
                   old[u][i] = ex2(safe_max(m[u][i]) - ms);
                   float e = 0.f, ed = 0.f;
@@ -579,7 +576,7 @@ __global__ void __launch_bounds__(32 * Shape<D, MAPS, MODE>::TW* Shape<D, MAPS, 
                   m[u][i] = mx;
                 }
               if constexpr (MODE == kForward) {
-                if (MAPS == 1 && half + k0 > lo) {
+                if (MAPS == 1 && __any_sync(kFull, old[0][0] != 1.f || old[0][1] != 1.f)) {
 #pragma unroll
                   for (int e = 0; e < NACC; ++e)
 #pragma unroll
@@ -666,7 +663,7 @@ cudaError_t need_smem(K kern, size_t smem) {
                           : cudaSuccess;
 }
 
-template <int D, int MAPS, bool BIAS, typename E, int MODE>
+template <int D, int MAPS, bool BIAS, int MODE>
 cudaError_t rows_pass(const char* name, const WinArgs& a, cudaStream_t st) {
   using S = Shape<D, MAPS, MODE>;
   constexpr int ON = BIAS ? 1 : 0;
@@ -678,11 +675,11 @@ cudaError_t rows_pass(const char* name, const WinArgs& a, cudaStream_t st) {
   const size_t rest = fixed + (size_t)NT * S::per_team;
   // the bias in shared memory where it fits; the forward has room for it always
   const bool in_smem = rest + 4 * T3 <= kSmemMost && !(grad && a.wide);
-  auto kern = window_rows_kernel<D, MAPS, ON, E, MODE>;
+  auto kern = window_rows_kernel<D, MAPS, ON, MODE>;
   if constexpr (MODE != kForward)
-    if (!in_smem) kern = window_rows_kernel<D, MAPS, 2 * ON, E, MODE>;
+    if (!in_smem) kern = window_rows_kernel<D, MAPS, 2 * ON, MODE>;
   if constexpr (MODE == kDq)
-    if (grad && a.wide) kern = window_rows_kernel<D, MAPS, 3 * ON, E, MODE>;
+    if (grad && a.wide) kern = window_rows_kernel<D, MAPS, 3 * ON, MODE>;
   const size_t smem = rest + (in_smem ? 4 * T3 : 0);
   const cudaError_t e = need_smem(kern, smem);
   if (e != cudaSuccess) return e;
@@ -715,7 +712,7 @@ struct DkvShape {
 };
 
 // TAB: 0 no bias, 1 tables staged in shared memory, 2 read in global memory (the largest edges).
-template <int D, int MAPS, int TAB, typename E>
+template <int D, int MAPS, int TAB>
 __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window_dkv_mma_kernel(WinArgs a) {
   using S = DkvShape<D, MAPS>;
   constexpr int DV = S::DV, NTH = 32 * kDkvWarps;
@@ -737,8 +734,7 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
     const int n = min(kChunk, hi - k0);
     const uint32_t q = base + S::Q + st * S::stage;
     int* codes = reinterpret_cast<int*>(sm + S::codes) + st * kChunk;
-    const Rows<E, D> Q = {static_cast<const E*>(a.q), a.sq, a.hq, MAPS * h};
-    const Rows<bf16, D> O = {static_cast<const bf16*>(a.dout), nullptr, a.hq, MAPS * h};
+    const Rows Q = {a.q, a.hq, MAPS * h}, O = {a.dout, a.hq, MAPS * h};
 #pragma unroll 1
     for (int x = 0; x < n; x += 32) {
       const uint32_t off = x * DV * 2;
@@ -762,8 +758,7 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
     cp_commit();
   };
 
-  const Rows<bf16, D> K = {static_cast<const bf16*>(a.k), nullptr, a.hkv, MAPS * hk};
-  const Rows<bf16, D> V = {static_cast<const bf16*>(a.v), nullptr, a.hkv, MAPS * hk};
+  const Rows K = {a.k, a.hkv, MAPS * hk}, V = {a.v, a.hkv, MAPS * hk};
   stage<D, DV, kChunk, NTH, true>(kt, K, vt, V, a.rows, keys0, nkeys, tid, SameRow(), NoCode());
   load(hk * G, lo, 0);
   const int r0 = kTile * warp, first = keys0 + r0, nr = min(kTile, hi - first);
@@ -894,21 +889,21 @@ __global__ void bias_expand_kernel(WinArgs a) {
   if (o < T3p) a.tab2[(size_t)blockIdx.y * T3p + o] = o < T3 ? bias2_at(a, blockIdx.y, o) : 0.f;
 }
 
-template <int D, int MAPS, bool BIAS, typename E>
+template <int D, int MAPS, bool BIAS>
 cudaError_t bwd(const WinArgs& a, cudaStream_t st) {
   constexpr int ON = BIAS ? 1 : 0;
   const size_t T3p = BIAS ? table_pitch(a.m) : 0;
   if (BIAS)
     SSA_LAUNCH("bias_expand_kernel", bias_expand_kernel, dim3(((int)T3p + 255) / 256, a.hq), 256, 0, st, a);
-  cudaError_t r = rows_pass<D, MAPS, BIAS, E, kStats>("window_stats_kernel", a, st);
-  if (r == cudaSuccess) r = rows_pass<D, MAPS, BIAS, E, kDq>("window_dq_kernel", a, st);
+  cudaError_t r = rows_pass<D, MAPS, BIAS, kStats>("window_stats_kernel", a, st);
+  if (r == cudaSuccess) r = rows_pass<D, MAPS, BIAS, kDq>("window_dq_kernel", a, st);
   if (r != cudaSuccess) return r;
   {
     using K = DkvShape<D, MAPS>;
     // three CTAs per SM (two for wide rows) while the tables fit beside them
     const bool in_smem = K::tab + 2 * sizeof(float) * T3p <= (D * MAPS == 128 ? 113 : 75) * 1024;
     const size_t smem = K::tab + (in_smem ? 2 * sizeof(float) * T3p : 0);
-    auto kern = in_smem ? window_dkv_mma_kernel<D, MAPS, ON, E> : window_dkv_mma_kernel<D, MAPS, 2 * ON, E>;
+    auto kern = in_smem ? window_dkv_mma_kernel<D, MAPS, ON> : window_dkv_mma_kernel<D, MAPS, 2 * ON>;
     const cudaError_t e = need_smem(kern, smem);
     if (e != cudaSuccess) return e;
     SSA_LAUNCH("window_dkv_mma_kernel", kern, dim3(a.T, a.hkv / MAPS), 32 * kDkvWarps, smem, st, a);
@@ -916,16 +911,15 @@ cudaError_t bwd(const WinArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <typename E>
-cudaError_t bwd_e(const WinArgs& a, cudaStream_t st) {
-  if (a.maps == 2) return a.d == 32 ? bwd<32, 2, false, E>(a, st) : bwd<64, 2, false, E>(a, st);
+cudaError_t bwd_any(const WinArgs& a, cudaStream_t st) {
+  if (a.maps == 2) return a.d == 32 ? bwd<32, 2, false>(a, st) : bwd<64, 2, false>(a, st);
   if (a.table)
-    return a.d == 32   ? bwd<32, 1, true, E>(a, st)
-           : a.d == 64 ? bwd<64, 1, true, E>(a, st)
-                       : bwd<128, 1, true, E>(a, st);
-  return a.d == 32   ? bwd<32, 1, false, E>(a, st)
-         : a.d == 64 ? bwd<64, 1, false, E>(a, st)
-                     : bwd<128, 1, false, E>(a, st);
+    return a.d == 32   ? bwd<32, 1, true>(a, st)
+           : a.d == 64 ? bwd<64, 1, true>(a, st)
+                       : bwd<128, 1, true>(a, st);
+  return a.d == 32   ? bwd<32, 1, false>(a, st)
+         : a.d == 64 ? bwd<64, 1, false>(a, st)
+                     : bwd<128, 1, false>(a, st);
 }
 
 // part[h][o]: the wide sums as floats; NaN where the head's dP or softmax had no finite bound.
@@ -942,19 +936,19 @@ __global__ void bias_wide_kernel(WinArgs a) {
 cudaError_t window_fwd_mma(const WinArgs& a, cudaStream_t st) {
   const char* name = "window_fwd_kernel";
   if (a.maps == 2)
-    return a.d == 32 ? rows_pass<32, 2, false, bf16, kForward>(name, a, st)
-                     : rows_pass<64, 2, false, bf16, kForward>(name, a, st);
+    return a.d == 32 ? rows_pass<32, 2, false, kForward>(name, a, st)
+                     : rows_pass<64, 2, false, kForward>(name, a, st);
   if (a.table)
-    return a.d == 32   ? rows_pass<32, 1, true, bf16, kForward>(name, a, st)
-           : a.d == 64 ? rows_pass<64, 1, true, bf16, kForward>(name, a, st)
-                       : rows_pass<128, 1, true, bf16, kForward>(name, a, st);
-  return a.d == 32   ? rows_pass<32, 1, false, bf16, kForward>(name, a, st)
-         : a.d == 64 ? rows_pass<64, 1, false, bf16, kForward>(name, a, st)
-                     : rows_pass<128, 1, false, bf16, kForward>(name, a, st);
+    return a.d == 32   ? rows_pass<32, 1, true, kForward>(name, a, st)
+           : a.d == 64 ? rows_pass<64, 1, true, kForward>(name, a, st)
+                       : rows_pass<128, 1, true, kForward>(name, a, st);
+  return a.d == 32   ? rows_pass<32, 1, false, kForward>(name, a, st)
+         : a.d == 64 ? rows_pass<64, 1, false, kForward>(name, a, st)
+                     : rows_pass<128, 1, false, kForward>(name, a, st);
 }
 
 cudaError_t window_bwd_mma(const WinArgs& a, cudaStream_t st) {
-  const cudaError_t e = a.act8 ? bwd_e<int8_t>(a, st) : bwd_e<bf16>(a, st);
+  const cudaError_t e = bwd_any(a, st);
   if (e == cudaSuccess && a.wide && a.dbias)
     SSA_LAUNCH("bias_wide_kernel", bias_wide_kernel, dim3((offsets(a.m) + 255) / 256, a.hq), 256, 0, st, a);
   return e != cudaSuccess ? e : cudaGetLastError();

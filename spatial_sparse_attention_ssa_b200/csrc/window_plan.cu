@@ -78,50 +78,46 @@ __global__ void plan_dup_kernel(int64_t N, int64_t W, int m, const int32_t* __re
   }
 }
 
-// dst[h][o] = sum over parts of part[h][i][o], in a fixed order, left in part i = 0.
-__global__ void bias_parts_kernel(float* __restrict__ part, int parts, int T) {
+// dst[h][o] = sum over parts of part[h][i][o], in a fixed order.  dst may be part i = 0.
+__global__ void bias_parts_kernel(const float* part, int parts, int T, float* dst, int pitch) {
   const int o = blockIdx.x * blockDim.x + threadIdx.x;
   if (o >= T) return;
-  float* p = part + (size_t)blockIdx.y * parts * T + o;
+  const float* p = part + (size_t)blockIdx.y * parts * T + o;
   float s = 0.f;
   for (int i = 0; i < parts; ++i) s += p[(size_t)i * T];
-  p[0] = s;
+  dst[(size_t)blockIdx.y * pitch + o] = s;
 }
 
-// dbias[h][b] = sum of the offsets o with bucket b, in order of o; one thread per bucket.
-__global__ void bias_buckets_kernel(const float* __restrict__ part, int parts, int T,
-                                    const int32_t* __restrict__ bucket, int nb, float* __restrict__ dbias) {
-  __shared__ int sb[1024];
-  __shared__ float sv[1024];
-  const int b = blockIdx.x * blockDim.x + threadIdx.x;
-  const float* p = part + (size_t)blockIdx.y * parts * T;
+// dbias[h][b] = sum of the offsets o with bucket b, in a fixed order; one warp per bucket and head.
+__global__ void bias_buckets_kernel(const float* __restrict__ sums, int pitch, int T, const int32_t* __restrict__ bucket,
+                                    int nb, float* __restrict__ dbias) {
+  const int b = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (b >= nb) return;
+  const float* p = sums + (size_t)blockIdx.y * pitch;
   float s = 0.f;
-  for (int o0 = 0; o0 < T; o0 += 1024) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < 1024 && o0 + i < T; i += blockDim.x) {
-      sb[i] = bucket ? bucket[o0 + i] : o0 + i;
-      sv[i] = p[o0 + i];
-    }
-    __syncthreads();
-    const int n = T - o0 < 1024 ? T - o0 : 1024;
-    for (int i = 0; i < n; ++i) s += sb[i] == b ? sv[i] : 0.f;
-  }
-  if (b < nb) dbias[(size_t)blockIdx.y * nb + b] = s;
+#pragma unroll 4
+  for (int o = lane; o < T; o += 32)
+    if (__ldg(bucket + o) == b) s += p[o];
+#pragma unroll
+  for (int i = 16; i; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
+  if (lane == 0) dbias[(size_t)blockIdx.y * nb + b] = s;
 }
 
 // dlambda of a head = -sum of D of its second map; then the chain rule through
 // lambda = exp(<x0, x1>) - exp(<x2, x3>) + init.  One block per head, fixed order, fp64 sums.
+constexpr int kLamThreads = 1024;
 template <int D>
-__global__ void lam_grad_kernel(const float* __restrict__ lam, const float* __restrict__ Drow, int64_t N, int heads,
+__global__ void __launch_bounds__(kLamThreads) lam_grad_kernel(const float* __restrict__ lam, const float* __restrict__ Drow, int64_t N, int heads,
                                 float* __restrict__ dlam) {
-  __shared__ double red[256];
+  __shared__ double red[kLamThreads];
   const int h = blockIdx.x, t = threadIdx.x;
   const float* p = Drow + (size_t)(2 * h + 1) * N;
   double s = 0.0;
-  for (int64_t i = t; i < N; i += 256) s += (double)p[i];
+#pragma unroll 8
+  for (int64_t i = t; i < N; i += kLamThreads) s += (double)p[i];
   red[t] = s;
   __syncthreads();
-  for (int o = 128; o; o >>= 1) {
+  for (int o = kLamThreads / 2; o; o >>= 1) {
     if (t < o) red[t] += red[t + o];
     __syncthreads();
   }
@@ -242,14 +238,18 @@ cudaError_t window_plan(const int32_t* coords, int64_t N, int m, const ssa_parti
 cudaError_t window_param_grads(const WinArgs& a, cudaStream_t st) {
   if (a.dbias) {
     const int T = offsets(a.m);
-    const dim3 g1((T + 127) / 128, a.hq), g2((a.nb + 127) / 128, a.hq);
-    SSA_LAUNCH("bias_parts_kernel", bias_parts_kernel, g1, 128, 0, st, a.part, a.parts, T);
-    SSA_LAUNCH("bias_buckets_kernel", bias_buckets_kernel, g2, 128, 0, st, a.part, a.parts, T, a.bucket, a.nb,
-               a.dbias);
+    // every offset its own bucket: the sums are the gradient
+    float* sums = a.bucket ? a.part : a.dbias;
+    const int pitch = a.bucket ? a.parts * T : T;
+    SSA_LAUNCH("bias_parts_kernel", bias_parts_kernel, dim3((T + 127) / 128, a.hq), 128, 0, st, a.part, a.parts, T,
+               sums, pitch);
+    if (a.bucket)
+      SSA_LAUNCH("bias_buckets_kernel", bias_buckets_kernel, dim3((a.nb + 7) / 8, a.hq), 256, 0, st, a.part, pitch, T,
+                 a.bucket, a.nb, a.dbias);
   }
   if (a.dlam) {
     auto kern = a.d == 32 ? lam_grad_kernel<32> : lam_grad_kernel<64>;
-    SSA_LAUNCH("lam_grad_kernel", kern, a.hq / 2, 256, 0, st, a.lam, a.D, a.N, a.hq / 2, a.dlam);
+    SSA_LAUNCH("lam_grad_kernel", kern, a.hq / 2, kLamThreads, 0, st, a.lam, a.D, a.N, a.hq / 2, a.dlam);
   }
   return cudaGetLastError();
 }

@@ -1,5 +1,4 @@
-// Attention inside the cells on the CUDA cores: fp32 products and sums from fp32, bf16 or
-// 8-bit rows.  See window.cuh for the mathematics and the meaning of MAPS.
+// Attention inside the cells on the CUDA cores: fp32 products and sums from fp32 or 8-bit rows.  See window.cuh for the mathematics and the meaning of MAPS.
 //
 // One CTA (128 threads) takes tiles of 16 rows of a cell against the cell in chunks of 64.
 // Thread (ty, tx), tid = 16 ty + tx, holds the scores of rows ty, ty + 8 against the chunk's
@@ -22,12 +21,6 @@ __device__ __forceinline__ float4 load4(const E* p, float s);
 template <>
 __device__ __forceinline__ float4 load4<float>(const float* p, float) {
   return __ldg(reinterpret_cast<const float4*>(p));
-}
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p, float) {
-  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xffff0000u));
 }
 template <>
 __device__ __forceinline__ float4 load4<int8_t>(const int8_t* p, float s) {
@@ -531,21 +524,17 @@ cudaError_t fwd_d(const WinArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t window_fwd_simt(const WinArgs& a, cudaStream_t st) {
-  return a.dtype == SSA_DTYPE_BF16 ? fwd_d<__nv_bfloat16>(a, st) : fwd_d<float>(a, st);
-}
+cudaError_t window_fwd_simt(const WinArgs& a, cudaStream_t st) { return fwd_d<float>(a, st); }
 
 cudaError_t window_bwd_simt(const WinArgs& a, cudaStream_t st) {
-  if (a.dtype == SSA_DTYPE_BF16)
-    return a.act8 ? bwd_d<int8_t, __nv_bfloat16>(a, st) : bwd_d<__nv_bfloat16, __nv_bfloat16>(a, st);
   return a.act8 ? bwd_d<int8_t, float>(a, st) : bwd_d<float, float>(a, st);
 }
 
-// Enough CTAs for about four on every SM, so that the last ones to finish leave little idle.
-int window_parts(int hq, int64_t T, int m) {
-  (void)m;
-  int64_t x = (4 * 148 + hq - 1) / hq;
-  return (int)(x < T ? x : T > 0 ? T : 1);
+// About six CTAs for every SM: few enough for the sums of their tables, enough that the last ones
+// to finish leave little idle.
+int window_parts(int hq, int64_t T) {
+  const int64_t x = (6 * 148) / hq;
+  return (int)(x < 1 || T < 1 ? 1 : x < T ? x : T);
 }
 
 }  // namespace ssa
