@@ -769,6 +769,7 @@ ssa::WinArgs window_args(const ssa_window_params* p, const ssa_win_plan* plan, i
   a.q = q;
   a.k = k;
   a.v = v;
+  a.cells = plan->count;
   return a;
 }
 
@@ -810,7 +811,9 @@ size_t carve_window(void* base, const ssa_window_params* p, const ssa_win_plan* 
   return c.used;
 }
 
-cudaError_t window_forward(const ssa::WinArgs& a, cudaStream_t st) {
+cudaError_t window_forward(ssa::WinArgs& a, cudaStream_t st) {
+  a.status = status_ptr();
+  if (!a.status) return cudaErrorUnknown;
   return a.dtype == SSA_DTYPE_BF16 ? ssa::window_fwd_mma(a, st) : ssa::window_fwd_simt(a, st);
 }
 
@@ -838,6 +841,8 @@ ssa_status window_backward(const ssa_window_params* p, const ssa_win_plan* plan,
   a.dv = dv;
   a.dbias = dbias;
   a.dlam = dlam;
+  a.status = status_ptr();
+  if (!a.status) return SSA_ERR_CUDA;
   cudaError_t e = cudaSuccess;
   if (act8 && a.dtype == SSA_DTYPE_BF16) {
     const int64_t rows = a.N * p->hkv;

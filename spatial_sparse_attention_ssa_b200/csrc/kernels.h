@@ -157,6 +157,7 @@ struct WinArgs {
   const int2* rows;   // [N] token, code in cell order
   const int4* tiles;  // [T] first row, rows (+ flag), cell begin, cell end; [T].x: most tokens of a voxel
   int T, m;
+  int64_t cells;
   const float* table;  // bias [hq, nb], or null
   const int32_t* bucket;
   int nb;
@@ -177,14 +178,15 @@ struct WinArgs {
   float* tab2;      // [hq][offsets] the bias by offset, in units of log2
   void *q16, *k16, *v16;  // 8-bit checkpoints: room for their rows as bf16
   unsigned* amax;   // [hq] the largest |dP| of a head, as bits
+  int* status;      // device check word
   int wide;         // bf16 and an edge from kWideEdge on: one part, summed in `sums`
   unsigned long long* sums;  // [hq][offsets]
 };
 cudaError_t window_plan(const int32_t* coords, int64_t N, int m, const ssa_partition* win, int2* rows, int4* tiles,
                         int* status, cudaStream_t st);
 // Window edges from here on keep the bias gradient of the bf16 kernels in global memory: 8 bytes per
-// offset are 157 KB, too many beside a team's rows in shared memory.
-constexpr int kWideEdge = 14;
+// offset are 125 KB, too many beside the ring of keys and eight warps' rows in shared memory.
+constexpr int kWideEdge = 13;
 // Partial bias gradients per head that the backward keeps (rows of `part`).
 int window_parts(int hq, int64_t T);
 cudaError_t window_fwd_simt(const WinArgs& a, cudaStream_t st);

@@ -1,14 +1,13 @@
 // Attention inside the cells on warp-level tensor-core MMAs (mma.sync m16n8k16, bf16 operands,
 // fp32 sums).  See window.cuh for the mathematics and the meaning of MAPS.
 //
-// A team of TW warps takes a cell and a head: it stages the cell's keys (64 at a time) in shared
-// memory once, and its warps walk the cell's rows 16 at a time.  The cells of surface voxels hold
-// some 60 tokens (windows of edge 8), so most have one chunk of keys whose scores stay in
-// registers: nothing is recomputed or rescaled.  Tiles of 128 rows (tcgen05) would stand half
-// empty on such cells and hand every score through TMEM; here the scores never leave registers
-// and nothing but the team waits on a barrier.  What bounds these kernels is instruction issue:
-// the softmax, the bias and the masks of a score take some eight times as many issue slots as
-// its products.
+// A CTA keeps one head (its bias table lies in shared memory) and walks cells.  The keys of the
+// cells, 64 at a time, go through a ring of stages in shared memory that one warp fills ahead
+// (cp.async, completion on an mbarrier); the cell's rows, 16 at a time, go to the other warps in
+// turn, so no warp waits for another but through the ring.  Scores never leave registers: a step is
+// 16 rows by 32 keys.  Tiles of 128 rows (tcgen05) would stand half empty on windows of some 50
+// tokens and hand every score through TMEM.  What bounds these kernels is instruction issue: the
+// softmax, the bias and the masks of a score take several times the issue slots of its products.
 #include "tc.cuh"
 #include "window.cuh"
 
@@ -20,6 +19,8 @@ using bf16 = __nv_bfloat16;
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kChunk = 64;
+// Row tiles of a cell that belong together: they take the cell's keys from one passage of the ring.
+constexpr int kItem = 8;
 constexpr float kSlack = 8.f;
 constexpr size_t kSmemMost = 226 * 1024;  // dynamic shared memory of a CTA, beside the barriers
 
@@ -51,6 +52,32 @@ __device__ __forceinline__ void stsm(uint32_t addr, uint32_t r0, uint32_t r1, ui
 // 16 bytes to shared memory, zeros where `on` is off
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// one arrival on the barrier when this thread's copies so far have landed
+__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
+}
+// Waits for a phase with the warp suspended meanwhile (not polling: the waiting warps would take issue
+// slots from the working ones); gives up as tc::mbar_wait does.
+__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  for (int i = 0; i < 4096; ++i) {  // some 0.25 ms each at most
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(tc::smem_u32(bar)), "r"(parity), "r"(250000)
+        : "memory");
+    if (__all_sync(kFull, done)) return true;
+  }
+  return tc::mbar_wait_warp(bar, parity);
+}
+__device__ __forceinline__ void prefetch(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -85,34 +112,29 @@ __device__ __forceinline__ uint32_t unit(int row, int c) {
   return 16u * (uint32_t)(row * U + (c ^ f));
 }
 
-// Rows first .. first + n - 1 of the cell order (n <= ROWS) to the rows of a staged tile, zeros past
-// n, by THREADS threads; one or two tensors of the same heads at once.  Position of row k: at(k).
-// `seen(k, row entry)` is called by one thread per row.  Unrolled: a unit costs its copy and
-// address and little else.
+// Rows first + y .. first + y + ROWS - 1 of the cell order to a staged tile, zeros from first + n on,
+// by THREADS threads; one or two tensors of the same heads at once.  Row y + k goes to position
+// at(y + k).  `seen(position, row, entry, unit)` is called for every unit.  Unrolled: a unit costs its
+// copy, its address and little else.
 template <int D, int W, int ROWS, int THREADS, bool TWO, typename At, typename Seen>
 __device__ __forceinline__ void stage(uint32_t dst, const Rows& src, uint32_t dst2, const Rows& src2,
-                                      const int2* __restrict__ rows, int first, int n, int tid, At at, Seen seen) {
-  constexpr int U = W / 8, STEP = THREADS / U, IT = (ROWS + STEP - 1) / STEP;
+                                      const int2* __restrict__ rows, int first, int n, int tid, int y, At at,
+                                      Seen seen) {
+  constexpr int U = W / 8, STEP = THREADS / U, IT = ROWS / STEP;
   static_assert(ROWS % STEP == 0, "whole steps");
   const int r = tid / U, c = tid % U;
   int2 e[IT];
 #pragma unroll
-  for (int i = 0; i < IT; ++i) e[i] = __ldg(&rows[first + min(i * STEP + r, n - 1)]);
+  for (int i = 0; i < IT; ++i) e[i] = __ldg(&rows[first + min(y + i * STEP + r, n - 1)]);
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
-    const int k = i * STEP + r, p = at(k);
+    const int k = y + i * STEP + r, p = at(k);
     const size_t at_row = ((size_t)e[i].x * src.heads + src.head) * D + 8 * c;
     cp16(dst + unit<W>(p, c), static_cast<const bf16*>(src.p) + at_row, k < n);
     if constexpr (TWO) cp16(dst2 + unit<W>(p, c), static_cast<const bf16*>(src2.p) + at_row, k < n);
-    if (c == 0) seen(p, e[i]);
+    seen(p, first + min(k, n - 1), e[i], c);
   }
 }
-struct SameRow {
-  __device__ __forceinline__ int operator()(int k) const { return k; }
-};
-struct NoCode {
-  __device__ __forceinline__ void operator()(int, const int2&) const {}
-};
 
 // A operand, k-step k, from a tile of 16 rows starting at row r0 of a staged tile.
 template <int W>
@@ -216,10 +238,9 @@ struct Limbs {
   __device__ __forceinline__ void set(const WinArgs& a, int h) {
     static_assert(SSA_WINDOW_TILE == 16, "rows of a slot");
     const uint32_t bits = __ldg(a.amax + h);
-    // rows of a CTA: its share of the slots (up to one more for each of its teams), each of which
-    // can be a cell of one chunk
-    const int64_t slots = (a.T + (int64_t)gridDim.x - 1) / gridDim.x + 8;
-    const int64_t rows = min((int64_t)a.N, slots * kChunk), adds = rows * max(1, __ldg(&a.tiles[a.T].x));
+    // rows of a CTA: its slots, each of which can start an item
+    const int64_t slots = (a.T + (int64_t)gridDim.x - 1) / gridDim.x;
+    const int64_t rows = min((int64_t)a.N, slots * (kItem * kTile)), adds = rows * max(1, __ldg(&a.tiles[a.T].x));
     const int rb = 64 - __clzll(rows), ab = 64 - __clzll(adds);  // rows < 2^rb, adds < 2^ab
     const int e = (int)(bits >> 23) - 126;                       // M < 2^e
     int sb = min(30 - rb - 1 - e, 20 - e);                       // |dS 2^s| < 2^22: see add()
@@ -263,20 +284,16 @@ struct Wide {
   }
 };
 
-// limbs[code of row - code of key] += dS of a fragment tile of 16 rows and 32 positions.
+// add(code of row - code of key, dS) for a fragment tile of 16 rows and 32 positions.  Rows and
+// positions without a token have dS 0 and the codes of others.
 template <typename F>
-__device__ __forceinline__ void add_bias_grad(const F& add, float (*ds)[4], const int* codes, int ci, int ci8, int left,
-                                              int nr) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const bool r0 = g < nr, r8 = g + 8 < nr;
+__device__ __forceinline__ void add_bias_grad(const F& add, float (*ds)[4], const int* codes, int ci, int ci8) {
+  const int t = threadIdx.x & 3;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int2 cj = *reinterpret_cast<const int2*>(codes + 8 * j + 2 * t);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int at = (x & 2 ? ci8 : ci) - (x & 1 ? cj.y : cj.x);
-      if ((x & 2 ? r8 : r0) && 8 * t + 2 * j + (x & 1) < left) add(at, ds[j][x]);
-    }
+    for (int x = 0; x < 4; ++x) add((x & 2 ? ci8 : ci) - (x & 1 ? cj.y : cj.x), ds[j][x]);
   }
 }
 
@@ -286,9 +303,7 @@ __device__ __forceinline__ void add_bias_grad(const F& add, float (*ds)[4], cons
 // without this such lanes would often hit one offset in one instruction (see add_bias_grad).
 // (The map is its own inverse.)
 __device__ __forceinline__ int key_at(int p) { return (p & 33) | (p & 6) << 2 | (p & 24) >> 2; }
-struct KeyOrder {
-  __device__ __forceinline__ int operator()(int k) const { return key_at(k); }
-};
+
 
 // s = s mul + bias in units of log2 for the 32 positions of a half chunk, minus infinity where
 // the key is not below `left`.  t0, t8: the head's table of offsets at the codes of rows g, g + 8
@@ -315,103 +330,70 @@ __device__ __forceinline__ void finish_scores(float (*s)[4], const int* codes, i
   }
 }
 
-template <int TW>
-__device__ __forceinline__ void team_sync(int team) {
-  if constexpr (TW == 1)
-    __syncwarp();
-  else
-    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(TW * 32) : "memory");
-}
 
-// Rows of a cell that the team of a tile slot takes: all of them where the cell has one chunk of
-// keys (from its first tile; the other slots have nothing to do), else TW tiles from every TW-th.
-// Returns the number of tiles, 0 for none.
-template <int TW>
-__device__ __forceinline__ int team_tiles(const int4& tile) {
+// Number of tiles of the item that starts at a slot: 0 for empty slots and those inside an item.
+template <int ITEM>
+__device__ __forceinline__ int item_tiles(const int4& tile) {
   if ((tile.y & (kDupFlag - 1)) == 0) return 0;
   const int at = (unsigned)(tile.x - tile.z) / kTile, all = (unsigned)(tile.w - tile.z + kTile - 1) / kTile;
-  if (tile.w - tile.z <= kChunk) return at == 0 ? all : 0;
-  return at % TW == 0 ? min(TW, all - at) : 0;
+  return at % ITEM == 0 ? min(ITEM, all - at) : 0;
 }
-
-// The slots start, start + step, .. that hold work for a team, with tile.y the number of its tiles.
-// The warp reads 32 slots at once: most are empty or belong to another slot's team.
-template <int TW>
-struct Slots {
-  const int4* tiles;
-  int T, at, step;
-  int4 mine;
-  unsigned left = 0;
-  __device__ __forceinline__ Slots(const WinArgs& a, int start, int step_) : tiles(a.tiles), T(a.T), at(start), step(step_) {}
-  __device__ __forceinline__ bool next(int4& tile) {
-    while (left == 0) {
-      if (at >= T) return false;
-      const int64_t t = at + (int64_t)(threadIdx.x & 31) * step;
-      mine = t < T ? __ldg(&tiles[t]) : make_int4(0, 0, 0, 0);
-      mine.y = team_tiles<TW>(mine);
-      left = __ballot_sync(kFull, mine.y > 0);
-      at = (int)min((int64_t)T, at + (int64_t)32 * step);
-    }
-    const int i = __ffs(left) - 1;
-    left &= left - 1;
-    tile = make_int4(__shfl_sync(kFull, mine.x, i), __shfl_sync(kFull, mine.y, i), __shfl_sync(kFull, mine.z, i),
-                     __shfl_sync(kFull, mine.w, i));
-    return true;
-  }
-};
 
 // What a walk over the rows does with the keys.
 enum { kForward, kStats, kDq };
 
-// A team's shared memory: the staged keys and values (the maps side by side), the keys' codes; a
-// warp's: a scratch tile of 16 rows, and one more in the backward (dO).
+// Shared memory: a stage of the ring (keys, values, codes of a chunk of 64 or 32 tokens, the maps side
+// by side), a warp's scratch tile of 16 rows (two in the backward, for dO), the list of items.
 template <int D, int MAPS, int MODE>
 struct Shape {
   static constexpr int DV = MAPS * D;
-  static constexpr int TW = DV == 128 ? 4 : 2;
-  static constexpr int V = kChunk * DV * 2;  // offset of the values, bytes
-  static constexpr int codes = 2 * V;        // offset of the codes
-  static constexpr int team = codes + kChunk * 4;
-  static constexpr int scratch = kTile * DV * 2;
+  static constexpr int row = DV * 2;          // bytes of a key or value
+  static constexpr int token = 2 * row + 4;   // of a stage, per token
+  static constexpr int scratch = kTile * row;
   static constexpr int warp = MODE == kForward ? scratch : 2 * scratch;
-  static constexpr int per_team = team + TW * warp;
-  // teams of a CTA at most, CTAs per SM: what registers and shared memory leave.  dq keeps three
-  // tables per CTA, so it takes one large CTA.
-  static constexpr int teams = MODE == kDq ? (DV == 128 ? 2 : 7) : DV == 128 ? 1 : 4;
-  static constexpr int resident = MODE == kDq ? 1 : DV == 128 && MODE == kForward ? 3 : 2;
+  static constexpr int items = 256;  // of a batch
+  // working warps of a CTA at most, as registers allow beside the filling warp; one CTA per SM, so
+  // that all stages are one ring
+  static constexpr int warps = DV == 128 || MODE == kDq ? 11 : 15;
 };
+constexpr int kStages = 8;  // of the ring at most
 
 // One kernel body for the forward, the row statistics of the backward, and dq with the bias
 // gradient: they share the walk over cells, keys and scores.  TAB: where the bias is read: 0 no
-// bias, 1 shared memory, 2 global memory.  E: type of q, k, v.
+// bias, 1 shared memory, 2 global memory; 3 as 2, the bias gradient in global memory too.  NS: stages;
+// chunk: keys of a stage.
 template <int D, int MAPS, int TAB, int MODE>
-__global__ void __launch_bounds__(32 * Shape<D, MAPS, MODE>::TW* Shape<D, MAPS, MODE>::teams,
-                                  Shape<D, MAPS, MODE>::resident) window_rows_kernel(WinArgs a) {
+__global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 1), 1) window_rows_kernel(WinArgs a, int NS, int chunk) {
   using S = Shape<D, MAPS, MODE>;
-  constexpr int DV = S::DV, TW = S::TW;
+  constexpr int DV = S::DV;
   constexpr bool BIAS = TAB != 0;
-  const int NT = (int)blockDim.x / (32 * TW);
   extern __shared__ __align__(128) char sm[];
+  __shared__ uint64_t full[kStages], empty[kStages];
+  __shared__ int n_items;
+  const int NW = (int)blockDim.x / 32 - 1;  // working warps; one more fills the ring
+  const uint32_t v_at = chunk * S::row, codes_at = 2 * v_at, stage_size = chunk * S::token;
   const int h = blockIdx.y, hk = h / (a.hq / a.hkv);
   const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3, warp = threadIdx.x >> 5;
-  const int team = warp / TW, wt = warp % TW, tid = threadIdx.x % (32 * TW);
   const int T3 = BIAS ? offsets(a.m) : 0, c0 = BIAS ? center(a.m) : 0;
   const bool grad = MODE == kDq && BIAS && a.dbias;
-  int* limbs = reinterpret_cast<int*>(sm + NT * S::per_team);  // [2][T3] with a bias gradient, not wide
+  int4* items = reinterpret_cast<int4*>(sm + NS * stage_size + NW * S::warp);
+  int* limbs = reinterpret_cast<int*>(items + S::items);  // [2][T3] with a bias gradient, not wide
   float* tab_s = reinterpret_cast<float*>(limbs + (grad && TAB != 3 ? 2 * T3 : 0));
   const float* tab = TAB >= 2 ? a.tab2 + (size_t)h * table_pitch(a.m) : tab_s;
-  char* mine = sm + team * S::team;
-  const uint32_t keys = tc::smem_u32(mine), vals = keys + S::V;
-  const uint32_t scratch = tc::smem_u32(sm + NT * S::team + warp * S::warp), scratch2 = scratch + S::scratch;
-  int* codes = reinterpret_cast<int*>(mine + S::codes);
+  const uint32_t ring = tc::smem_u32(sm);
+  const uint32_t scratch = tc::smem_u32(sm + NS * stage_size + warp * S::warp), scratch2 = scratch + S::scratch;
   const float mul = a.scale * kLog2e;
   if constexpr (BIAS) {
     if (TAB == 1)
       for (int i = threadIdx.x; i < T3; i += blockDim.x) tab_s[i] = bias2_at(a, h, i);
     if (grad && TAB != 3)
       for (int i = threadIdx.x; i < 2 * T3; i += blockDim.x) limbs[i] = 0;
-    __syncthreads();
   }
+  if (threadIdx.x < NS) {
+    tc::mbar_init(&full[threadIdx.x], 64);  // the filling warp's copies, and its stores of the codes
+    tc::mbar_init(&empty[threadIdx.x], NW);
+  }
+  tc::fence_mbar_init();
   Limbs fx;
   Wide wide;
   if (grad && TAB != 3) fx.set(a, h);
@@ -423,76 +405,141 @@ __global__ void __launch_bounds__(32 * Shape<D, MAPS, MODE>::TW* Shape<D, MAPS, 
     lam = e1 - e2 + a.lam_init;
   }
   const Rows Q = {a.q, a.hq, MAPS * h}, O = {a.dout, a.hq, MAPS * h};
-  const Rows K = {a.k, a.hkv, MAPS * hk}, V = {a.v, a.hkv, MAPS * hk};
   uint32_t top = 0;  // the largest |dP|, as bits: NaN above all
-  Slots<TW> slots(a, blockIdx.x * NT + team, gridDim.x * NT);
-  int4 tile;
-  while (slots.next(tile)) {
-    const int lo = tile.z, hi = tile.w, nt = tile.y;
-    const bool one = hi - lo <= kChunk;
-    for (int w = wt; w < (nt + TW - 1) / TW * TW; w += TW) {  // every warp of the team, for its barriers
-      const bool on = w < nt;
-      const int first = on ? tile.x + kTile * w : tile.x, nr = min(kTile, hi - first);
-      // differential attention subtracts the maps before the product with V, so both normalisers
-      // come first: its forward walks the keys twice
-      constexpr int PASSES = MODE == kForward && MAPS == 2 ? 2 : 1;
-      constexpr int NACC = MODE == kForward ? DV / 8 : MODE == kDq ? DV / 8 : 1;
+
+  // differential attention subtracts the maps before the product with V, so both normalisers come
+  // first: its forward walks the keys twice (twice through the ring where the cell has several chunks)
+  constexpr int PASSES = MODE == kForward && MAPS == 2 ? 2 : 1;
+  int rot = 0;                          // the warp that takes the next item's first tile
+  int fs = 0, fphase = warp == NW;      // stage and phase of the next fill (to make one never waits at first)
+  bool ok = true;
+  for (int64_t batch = blockIdx.x; batch < a.T && ok; batch += (int64_t)S::items * gridDim.x) {
+    // the batch's items, in the order of their slots
+    __syncthreads();
+    if (warp == NW) {
+      int n = 0;
+      for (int i0 = 0; i0 < S::items; i0 += 32) {
+        const int64_t t = batch + (int64_t)(i0 + lane) * gridDim.x;
+        int4 x = t < a.T ? __ldg(&a.tiles[t]) : make_int4(0, 0, 0, 0);
+        x.y = item_tiles<kItem>(x);
+        const unsigned some = __ballot_sync(kFull, x.y > 0);
+        if (x.y > 0) items[n + __popc(some & ((1u << lane) - 1u))] = x;
+        n += __popc(some);
+      }
+      if (lane == 0) n_items = n;
+    }
+    __syncthreads();
+    const int count = n_items;
+    if (warp == NW) {
+      // the filling warp: lane l holds the rows l and 32 + l of the coming chunk
+      int2 e[2] = {};
+      auto entries = [&](int k0, int hi) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) e[i] = __ldg(&a.rows[min(k0 + 32 * i + lane, hi - 1)]);
+      };
+      if (count > 0) entries(items[0].z, items[0].w);
+      for (int ii = 0; ii < count && ok; ++ii) {
+        const int lo = items[ii].z, hi = items[ii].w;
+        const int fills = hi - lo <= chunk ? 1 : PASSES * ((hi - lo + chunk - 1) / chunk);
+        int k0 = lo;
+        for (int i = 0; i < fills && ok; ++i) {
+          const int n = min(chunk, hi - k0);
+          ok = ring_wait(&empty[fs], fphase);
+          if (!ok) break;
+          const uint32_t kt = ring + fs * stage_size;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (32 * x < n) {
+              constexpr int U = DV / 8, STEP = 32 / U;
+              const int r = lane / U, c = lane % U;
+#pragma unroll
+              for (int y = 0; y < 32; y += STEP) {
+                const int k = 32 * x + y + r, p = key_at(k);
+                const size_t at =
+                    ((size_t)__shfl_sync(kFull, e[x].x, (y + r) & 31) * a.hkv + MAPS * hk) * D + 8 * c;
+                cp16(kt + unit<DV>(p, c), static_cast<const bf16*>(a.k) + at, k < n);
+                cp16(kt + v_at + unit<DV>(p, c), static_cast<const bf16*>(a.v) + at, k < n);
+              }
+              if (BIAS) *reinterpret_cast<int*>(sm + fs * stage_size + codes_at + 4 * key_at(32 * x + lane)) = e[x].y;
+              // the item's queries are its keys: bring their rows near
+              const size_t at = ((size_t)e[x].x * a.hq + MAPS * h) * D;
+              prefetch(static_cast<const bf16*>(a.q) + at);
+              if (MODE != kForward) prefetch(static_cast<const bf16*>(a.dout) + at);
+            }
+          }
+          cp_arrive(&full[fs]);
+          tc::mbar_arrive(&full[fs]);
+          if (++fs == NS) fs = 0, fphase ^= 1;
+          k0 += chunk;
+          if (k0 >= hi) k0 = lo;
+          if (i + 1 < fills)
+            entries(k0, hi);
+          else if (ii + 1 < count)
+            entries(items[ii + 1].z, items[ii + 1].w);
+        }
+      }
+      continue;
+    }
+    for (int ii = 0; ii < count && ok; ++ii) {
+      const int4 item = items[ii];
+      const int lo = item.z, hi = item.w;
+      int mine = warp - rot;
+      if (mine < 0) mine += NW;
+      const bool on = mine < item.y, one = hi - lo <= chunk;
+      rot += item.y;
+      if (rot >= NW) rot -= NW;
+      const int first = item.x + kTile * mine, nr = min(kTile, hi - first);
+      constexpr int NACC = MODE == kStats ? 1 : DV / 8;
       float m[MAPS][2], l[MAPS][2], dd[MAPS][2], acc[NACC][4];
       uint32_t q[DV / 16][4], o[MODE == kForward ? 1 : DV / 16][4];
       const float *t0 = tab, *t8 = tab;
       int ci = 0, ci8 = 0;
-#pragma unroll
-      for (int u = 0; u < MAPS; ++u) {
-        m[u][0] = m[u][1] = kNegInf;
-        l[u][0] = l[u][1] = dd[u][0] = dd[u][1] = 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < NACC; ++e) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
       if (on) {
         __syncwarp();
-        stage<D, DV, kTile, 32, MODE != kForward>(scratch, Q, scratch2, O, a.rows, first, nr, lane, SameRow(), NoCode());
+        stage<D, DV, kTile, 32, MODE != kForward>(scratch, Q, scratch2, O, a.rows, first, nr, lane, 0,
+                                                  [](int k) { return k; }, [](int, int, const int2&, int) {});
+        cp_commit();
         if (BIAS) {
           ci = __ldg(&a.rows[first + min(g, nr - 1)].y) + c0;
           ci8 = __ldg(&a.rows[first + min(g + 8, nr - 1)].y) + c0;
           t0 = tab + ci;
           t8 = tab + ci8;
         }
-        if constexpr (MODE == kDq) {
 #pragma unroll
-          for (int u = 0; u < MAPS; ++u)
+        for (int u = 0; u < MAPS; ++u)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < 2; ++i) {
+            m[u][i] = kNegInf;
+            l[u][i] = dd[u][i] = 0.f;
+            if constexpr (MODE == kDq) {  // rows without a token: every p is 0
               const size_t at = (size_t)(MAPS * h + u) * a.N + first + min(g + 8 * i, nr - 1);
-              m[u][i] = a.lse2[at];
-              dd[u][i] = a.D[at];
+              m[u][i] = g + 8 * i < nr ? a.lse2[at] : kPosInf;
+              dd[u][i] = g + 8 * i < nr ? a.D[at] : 0.f;
             }
-        }
+          }
+#pragma unroll
+        for (int e = 0; e < NACC; ++e) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
       }
+      bool fresh = true;
 #pragma unroll 1
-      for (int pass = 0; pass < PASSES; ++pass) {
+      for (int turn = 0; turn < (one ? 1 : PASSES); ++turn) {
 #pragma unroll 1
-        for (int k0 = lo; k0 < hi; k0 += kChunk) {
-          const int n = min(kChunk, hi - k0);
-          if (!one || (w < TW && pass == 0)) {
-            team_sync<TW>(team);
-#pragma unroll 1
-            for (int x = 0; x < n; x += 32) {
-              const uint32_t off = x * DV * 2;
-              stage<D, DV, 32, 32 * TW, true>(keys + off, K, vals + off, V, a.rows, k0 + x, min(32, n - x), tid, KeyOrder(),
-                                              [&](int p, const int2& e) {
-                                                if (BIAS) codes[x + p] = e.y;
-                                              });
-            }
-            cp_commit();
-            cp_wait<0>();
-            team_sync<TW>(team);
-          } else {
-            cp_commit();
+        for (int k0 = lo; k0 < hi; k0 += chunk) {
+          const int n = min(chunk, hi - k0);
+          ok = ok && ring_wait(&full[fs], fphase);
+          if (!ok) break;
+          const uint32_t kst = ring + fs * stage_size;
+          const int* codes = reinterpret_cast<const int*>(sm + fs * stage_size + codes_at);
+          uint64_t* done = &empty[fs];
+          if (++fs == NS) fs = 0, fphase ^= 1;
+          if (!on) {  // every warp passes every fill: none falls behind by a turn of the ring
+            if (lane == 0) tc::mbar_arrive(done);
+            continue;
+          }
+          if (fresh) {
+            fresh = false;
             cp_wait<0>();
             __syncwarp();
-          }
-          if (!on) continue;
-          if (k0 == lo && pass == 0) {
 #pragma unroll
             for (int d = 0; d < DV / 16; ++d) {
               load_a<DV>(q[d], scratch, 0, d);
@@ -500,113 +547,118 @@ __global__ void __launch_bounds__(32 * Shape<D, MAPS, MODE>::TW* Shape<D, MAPS, 
             }
           }
 #pragma unroll 1
-          for (int half = 0; half < n; half += 32) {
-            const uint32_t kt = keys + half * DV * 2, vt = vals + half * DV * 2;
-            const int* hc = codes + half;
-            float s[MAPS][4][4], dp[MODE == kForward ? 1 : 4][4];
-#pragma unroll
-            for (int u = 0; u < MAPS; ++u) {
-              contract_dim<DV, D, 2>(q + u * D / 16, kt, u * D / 8, s[u]);
-              finish_scores<BIAS>(s[u], hc, n - half, mul, t0, t8);
-            }
-            if constexpr (MODE != kForward) contract_dim<DV, DV, 2>(o, vt, 0, dp);
-            if constexpr (MODE == kDq) {
-              // p = 2^(s - lse2), dS = p (dP - D)
+          for (int pass = one ? 0 : turn; pass < (one ? PASSES : turn + 1); ++pass) {
+#pragma unroll 1
+            for (int half = 0; half < n; half += 32) {
+              const uint32_t kt = kst + half * S::row, vt = kt + v_at;
+              const int* hc = codes + half;
+              float s[MAPS][4][4], dp[MODE == kForward ? 1 : 4][4];
 #pragma unroll
               for (int u = 0; u < MAPS; ++u) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                  for (int x = 0; x < 4; ++x) {
-                    const float p = ex2(s[u][j][x] - m[u][x >> 1]);
-                    s[u][j][x] = (u ? -lam * p : p) * (dp[j][x] - dd[u][x >> 1]);
-                  }
-                if (BIAS) {
-                  if (grad) {
-                    if constexpr (TAB == 3)
-                      add_bias_grad([&](int at, float x) { wide.add(at, x); }, s[0], hc, ci, ci8, n - half, nr);
-                    else
-                      add_bias_grad([&](int at, float x) { fx.add(limbs + at, limbs + T3 + at, x); }, s[0], hc, ci, ci8,
-                                    n - half, nr);
-                  }
-                }
-                uint32_t f[2][4];
-                pack_a<4>(s[u], f);
-                contract_rows<DV, D, 2>(f, kt, u * D / 8, acc + u * D / 8);
+                contract_dim<DV, D, 2>(q + u * D / 16, kt, u * D / 8, s[u]);
+                finish_scores<BIAS>(s[u], hc, n - half, mul, t0, t8);
               }
-            } else {
-              // online maximum, sum (and sum of p dP) of a row; the sums stay per lane to the end.  The
-              // subtracted maximum follows the true one only once that has grown by a factor of
-              // 2^kSlack, so that sums and products are rarely rescaled
-              float old[MAPS][2];
+              if constexpr (MODE != kForward) contract_dim<DV, DV, 2>(o, vt, 0, dp);
+              if constexpr (MODE == kDq) {
+                // p = 2^(s - lse2), dS = p (dP - D)
 #pragma unroll
-              for (int u = 0; u < MAPS; ++u)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  if (MODE == kForward && MAPS == 2 && pass == 1) {
-                    const float f = (u ? -lam : 1.f) * l[u][i], ms = safe_max(m[u][i]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                      for (int x = 0; x < 2; ++x) s[u][j][2 * i + x] = ex2(s[u][j][2 * i + x] - ms) * f;
-                    continue;
-                  }
-                  float mx = m[u][i];
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(s[u][j][2 * i], s[u][j][2 * i + 1]));
-                  mx = quad_max(mx);
-                  if (!(mx > m[u][i] + kSlack)) mx = m[u][i];
-                  const float ms = safe_max(mx);
-                  old[u][i] = ex2(safe_max(m[u][i]) - ms);
-                  float e = 0.f, ed = 0.f;
+                for (int u = 0; u < MAPS; ++u) {
 #pragma unroll
                   for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                      const float p = ex2(s[u][j][2 * i + x] - ms);
-                      s[u][j][2 * i + x] = p;
-                      e += p;
-                      if constexpr (MODE == kStats) {
-                        ed = fmaf(p, dp[j][2 * i + x], ed);
-                        if (u == 0) top = max(top, __float_as_uint(dp[j][2 * i + x]) & 0x7fffffffu);
-                      }
+                    for (int x = 0; x < 4; ++x) {
+                      const float p = ex2(s[u][j][x] - m[u][x >> 1]);
+                      s[u][j][x] = (u ? -lam * p : p) * (dp[j][x] - dd[u][x >> 1]);
                     }
-                  l[u][i] = fmaf(l[u][i], old[u][i], e);
-                  if (MODE == kStats) dd[u][i] = fmaf(dd[u][i], old[u][i], ed);
-                  m[u][i] = mx;
+                  if (BIAS) {
+                    if (grad) {
+                      if constexpr (TAB == 3)
+                        add_bias_grad([&](int at, float x) { wide.add(at, x); }, s[0], hc, ci, ci8);
+                      else
+                        add_bias_grad([&](int at, float x) { fx.add(limbs + at, limbs + T3 + at, x); }, s[0], hc, ci,
+                                      ci8);
+                    }
+                  }
+                  uint32_t f[2][4];
+                  pack_a<4>(s[u], f);
+                  contract_rows<DV, D, 2>(f, kt, u * D / 8, acc + u * D / 8);
                 }
-              if constexpr (MODE == kForward) {
-                if (MAPS == 1 && __any_sync(kFull, old[0][0] != 1.f || old[0][1] != 1.f)) {
+              } else {
+                // online maximum, sum (and sum of p dP) of a row; the sums stay per lane to the end.
+                // The subtracted maximum follows the true one only once that has grown by a factor of
+                // 2^kSlack, so that sums and products are rarely rescaled
+                float old[MAPS][2];
 #pragma unroll
-                  for (int e = 0; e < NACC; ++e)
+                for (int u = 0; u < MAPS; ++u)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) acc[e][x] *= old[0][x >> 1];
-                }
-                if (MAPS == 1 || pass == 1) {
-                  if constexpr (MAPS == 2) {
+                  for (int i = 0; i < 2; ++i) {
+                    if (PASSES == 2 && pass == 1) {
+                      const float f = (u ? -lam : 1.f) * l[u][i], ms = safe_max(m[u][i]);
+#pragma unroll
+                      for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) s[u][j][2 * i + x] = ex2(s[u][j][2 * i + x] - ms) * f;
+                      continue;
+                    }
+                    float mx = kNegInf;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(s[u][j][2 * i], s[u][j][2 * i + 1]));
+                    mx = quad_max(mx);
+                    if (!(mx > m[u][i] + kSlack)) mx = m[u][i];
+                    const float ms = safe_max(mx);
+                    old[u][i] = ex2(safe_max(m[u][i]) - ms);
+                    float e = 0.f, ed = 0.f;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
 #pragma unroll
-                      for (int x = 0; x < 4; ++x) s[0][j][x] += s[MAPS - 1][j][x];
+                      for (int x = 0; x < 2; ++x) {
+                        const float p = ex2(s[u][j][2 * i + x] - ms);
+                        s[u][j][2 * i + x] = p;
+                        e += p;
+                        if constexpr (MODE == kStats) {
+                          ed = fmaf(p, dp[j][2 * i + x], ed);
+                          if (u == 0) top = max(top, __float_as_uint(dp[j][2 * i + x]) & 0x7fffffffu);
+                        }
+                      }
+                    l[u][i] = fmaf(l[u][i], old[u][i], e);
+                    if (MODE == kStats) dd[u][i] = fmaf(dd[u][i], old[u][i], ed);
+                    m[u][i] = mx;
                   }
-                  uint32_t p[2][4];
-                  pack_a<4>(s[0], p);
-                  contract_rows<DV, DV, 2>(p, vt, 0, acc);
+                if constexpr (MODE == kForward) {
+                  if (MAPS == 1 && half + k0 > lo && __any_sync(kFull, old[0][0] != 1.f || old[0][1] != 1.f)) {
+#pragma unroll
+                    for (int e = 0; e < NACC; ++e)
+#pragma unroll
+                      for (int x = 0; x < 4; ++x) acc[e][x] *= old[0][x >> 1];
+                  }
+                  if (PASSES == 1 || pass == 1) {
+                    if constexpr (MAPS == 2) {
+#pragma unroll
+                      for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) s[0][j][x] += s[MAPS - 1][j][x];
+                    }
+                    uint32_t p[2][4];
+                    pack_a<4>(s[0], p);
+                    contract_rows<DV, DV, 2>(p, vt, 0, acc);
+                  }
                 }
               }
             }
-          }
-        }
-        if constexpr (MODE == kForward && MAPS == 2) {
-          if (pass == 0) {
+            if constexpr (PASSES == 2) {
+              if (pass == 0 && k0 + chunk >= hi) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
-              for (int i = 0; i < 2; ++i) l[u][i] = safe_inv(quad_sum(l[u][i]));
+                  for (int i = 0; i < 2; ++i) l[u][i] = safe_inv(quad_sum(l[u][i]));
+              }
+            }
           }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(done);
         }
       }
-      if (!on) continue;
+      if (!on || !ok) continue;
       if constexpr (MODE == kForward) {
         float f[2] = {1.f, 1.f};
         if constexpr (MAPS == 1) {
@@ -639,6 +691,9 @@ __global__ void __launch_bounds__(32 * Shape<D, MAPS, MODE>::TW* Shape<D, MAPS, 
       }
     }
   }
+  cp_commit();
+  cp_wait<0>();
+  if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
   if constexpr (MODE == kStats && BIAS) {
     top = __reduce_max_sync(kFull, top);
     if (lane == 0 && a.dbias) atomicMax(a.amax + h, top);
@@ -650,11 +705,11 @@ __global__ void __launch_bounds__(32 * Shape<D, MAPS, MODE>::TW* Shape<D, MAPS, 
   }
 }
 
-// CTAs along the tiles for `heads` heads: about `waves` times the resident ones, no more than the
-// tiles fill.
-int grid_x(int heads, int T, int per_cta, int resident, int waves) {
-  const int need = (T + per_cta - 1) / per_cta, want = (waves * resident * 148 + heads - 1) / heads;
-  return need < want ? need : want;
+// CTAs along the slots for `heads` heads: about six for every SM, so that the last ones to finish
+// leave little idle, but no more than the slots fill.
+int grid_x(int heads, int T, int per_cta) {
+  const int need = (T + per_cta - 1) / per_cta, want = 6 * 148 / heads;
+  return want < 1 ? 1 : need < want ? need : want;
 }
 
 template <typename K>
@@ -668,24 +723,38 @@ cudaError_t rows_pass(const char* name, const WinArgs& a, cudaStream_t st) {
   using S = Shape<D, MAPS, MODE>;
   constexpr int ON = BIAS ? 1 : 0;
   const bool grad = MODE == kDq && BIAS && a.dbias;
-  const size_t T3 = BIAS ? offsets(a.m) : 0, fixed = grad && !a.wide ? 8 * T3 : 0;
-  // as many teams as fit beside the tables of the gradient
-  const size_t fit = (kSmemMost - fixed) / S::per_team;
-  const int NT = fit < (size_t)S::teams ? (int)fit : S::teams;
-  const size_t rest = fixed + (size_t)NT * S::per_team;
-  // the bias in shared memory where it fits; the forward has room for it always
-  const bool in_smem = rest + 4 * T3 <= kSmemMost && !(grad && a.wide);
+  const size_t T3 = BIAS ? offsets(a.m) : 0, list = sizeof(int4) * S::items;
+  const size_t limbs = grad && !a.wide ? 8 * T3 : 0;
+  // Chunks of 64 keys, of 32 where cells are so small that more of them in flight count for more
+  // than fewer steps, or where no more fits.  The bias lies in shared memory where room is left beside
+  // it for eight warps and three stages (the forward always has it there); then as many warps as may
+  // be and as many stages as fit.
+  int chunk = a.N <= 24 * (int64_t)a.cells ? 32 : kChunk, NW = 0, NS = 0;
+  bool in_smem = false;
+  size_t smem = 0;
+  for (;; chunk = 32) {
+    const size_t stage = (size_t)chunk * S::token, least = list + limbs + kItem * S::warp + 3 * stage;
+    in_smem = BIAS && !(grad && a.wide) && least + 4 * T3 <= kSmemMost;
+    const size_t fixed = list + limbs + (in_smem ? 4 * T3 : 0);
+    if (least <= kSmemMost && (in_smem || !BIAS || MODE != kForward)) {
+      NW = (int)min((size_t)S::warps, (kSmemMost - fixed - 3 * stage) / S::warp);
+      NS = (int)min((size_t)kStages, (kSmemMost - fixed - NW * S::warp) / stage);
+      smem = fixed + NW * S::warp + NS * stage;
+      break;
+    }
+    if (chunk == 32) return cudaErrorInvalidConfiguration;
+  }
   auto kern = window_rows_kernel<D, MAPS, ON, MODE>;
   if constexpr (MODE != kForward)
     if (!in_smem) kern = window_rows_kernel<D, MAPS, 2 * ON, MODE>;
   if constexpr (MODE == kDq)
     if (grad && a.wide) kern = window_rows_kernel<D, MAPS, 3 * ON, MODE>;
-  const size_t smem = rest + (in_smem ? 4 * T3 : 0);
+  if (NW < kItem || NS < 3 || smem > kSmemMost) return cudaErrorInvalidConfiguration;
   const cudaError_t e = need_smem(kern, smem);
   if (e != cudaSuccess) return e;
   const int heads = a.hq / MAPS;
-  const int gx = grad && !a.wide ? a.parts : grid_x(heads, a.T, NT, S::resident, 4);
-  SSA_LAUNCH(name, kern, dim3(gx, heads), 32 * S::TW * NT, smem, st, a);
+  const int gx = grad && !a.wide ? a.parts : grid_x(heads, a.T, NW);
+  SSA_LAUNCH(name, kern, dim3(gx, heads), 32 * (NW + 1), smem, st, a, NS, chunk);
   return cudaGetLastError();
 }
 
@@ -697,6 +766,9 @@ cudaError_t rows_pass(const char* name, const WinArgs& a, cudaStream_t st) {
 // scores of the cell's queries, 64 at a time, of every query head that reads the key head.  Q, dO,
 // the statistics and the head's bias table of the next step arrive while this one is computed.
 constexpr int kDkvWarps = 4;
+
+// Number of key tiles of the CTA of a slot: four from every fourth tile of a cell.
+__device__ __forceinline__ int dkv_tiles(const int4& tile) { return item_tiles<kDkvWarps>(tile); }
 
 template <int D, int MAPS>
 struct DkvShape {
@@ -723,7 +795,7 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
   const float mul = a.scale * kLog2e;
   const int c0 = BIAS ? center(a.m) : 0, T3 = BIAS ? offsets(a.m) : 0, T3p = BIAS ? table_pitch(a.m) : 0;
   const int4 tile = __ldg(&a.tiles[blockIdx.x]);
-  const int lo = tile.z, hi = tile.w, nt = team_tiles<kDkvWarps>(tile);
+  const int lo = tile.z, hi = tile.w, nt = dkv_tiles(tile);
   if (nt == 0) return;
   // K and V stay before the stages, or are in the second stage until it is needed
   const uint32_t base = tc::smem_u32(sm), kt = base + (S::held ? S::stage : 0), vt = kt + S::KT;
@@ -736,13 +808,11 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
     int* codes = reinterpret_cast<int*>(sm + S::codes) + st * kChunk;
     const Rows Q = {a.q, a.hq, MAPS * h}, O = {a.dout, a.hq, MAPS * h};
 #pragma unroll 1
-    for (int x = 0; x < n; x += 32) {
-      const uint32_t off = x * DV * 2;
-      stage<D, DV, 32, NTH, true>(q + off, Q, q + S::KT + off, O, a.rows, k0 + x, min(32, n - x), tid, SameRow(),
-                                  [&](int p, const int2& e) {
-                                    if (BIAS) codes[x + p] = e.y + c0;
+    for (int x = 0; x < n; x += 32)
+      stage<D, DV, 32, NTH, true>(q, Q, q + S::KT, O, a.rows, k0, n, tid, x, [](int k) { return k; },
+                                  [&](int p, int, const int2& e, int c) {
+                                    if (BIAS && c == 0) codes[p] = e.y + c0;
                                   });
-    }
     float* stat = reinterpret_cast<float*>(sm + S::Q + st * S::stage + S::stat);
 #pragma unroll
     for (int i = 0; i < MAPS; ++i) {  // 64 threads a row of lse2, 64 a row of D
@@ -759,7 +829,8 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
   };
 
   const Rows K = {a.k, a.hkv, MAPS * hk}, V = {a.v, a.hkv, MAPS * hk};
-  stage<D, DV, kChunk, NTH, true>(kt, K, vt, V, a.rows, keys0, nkeys, tid, SameRow(), NoCode());
+  stage<D, DV, kChunk, NTH, true>(kt, K, vt, V, a.rows, keys0, nkeys, tid, 0, [](int k) { return k; },
+                                  [](int, int, const int2&, int) {});
   load(hk * G, lo, 0);
   const int r0 = kTile * warp, first = keys0 + r0, nr = min(kTile, hi - first);
   const bool on = warp < nt;
