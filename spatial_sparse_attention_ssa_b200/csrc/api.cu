@@ -731,6 +731,8 @@ ssa_status check_window(const ssa_window_params* p, const ssa_win_plan* plan, in
     return SSA_ERR_INVALID_ARG;
   if (p->d != 32 && p->d != 64 && (p->d != 128 || maps == 2)) return SSA_ERR_UNSUPPORTED;
   if (p->hq > 65535) return SSA_ERR_UNSUPPORTED;
+  // places in a tensor are counted in 16-byte units in 32 bits (64 GB a tensor)
+  if ((uint64_t)plan->n * p->hq * p->d / 8 > UINT32_MAX) return SSA_ERR_UNSUPPORTED;
   if (plan->n / SSA_WINDOW_TILE + plan->count >= INT32_MAX) return SSA_ERR_UNSUPPORTED;
   if (plan->n > 0 && (plan->count < 1 || !plan->rows || !plan->tiles || !aligned16(plan->rows) || !aligned16(plan->tiles)))
     return SSA_ERR_INVALID_ARG;

@@ -2,7 +2,7 @@
 // fp32 sums).  See window.cuh for the mathematics and the meaning of MAPS.
 //
 // A CTA keeps one head (its bias table lies in shared memory) and walks cells.  The keys of the
-// cells, 64 at a time, go through a ring of stages in shared memory that one warp fills ahead
+// cells, 64 at a time, go through a ring of stages in shared memory that two warps fill ahead
 // (cp.async, completion on an mbarrier); the cell's rows, 16 at a time, go to the other warps in
 // turn, so no warp waits for another but through the ring.  Scores never leave registers: a step is
 // 16 rows by 32 keys.  Tiles of 128 rows (tcgen05) would stand half empty on windows of some 50
@@ -60,21 +60,16 @@ __device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
 __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
 }
-// Waits for a phase with the warp suspended meanwhile (not polling: the waiting warps would take issue
-// slots from the working ones); gives up as tc::mbar_wait does.
+// Waits for a phase, asleep between the looks: polling warps would take issue slots from the working
+// ones.  Gives up after the time of tc::mbar_wait.
 __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  for (int i = 0; i < 4096; ++i) {  // some 0.25 ms each at most
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(tc::smem_u32(bar)), "r"(parity), "r"(250000)
-        : "memory");
-    if (__all_sync(kFull, done)) return true;
+  if (__all_sync(kFull, tc::mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = tc::global_ns();
+  for (uint32_t i = 1;; ++i) {
+    __nanosleep(i < 4 ? 50 : 150);
+    if (__all_sync(kFull, tc::mbar_try_wait(bar, parity))) return true;
+    if ((i & 255u) == 0 && __any_sync(kFull, tc::global_ns() - t0 > tc::kWaitLimitNs)) return false;
   }
-  return tc::mbar_wait_warp(bar, parity);
 }
 __device__ __forceinline__ void prefetch(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
@@ -352,9 +347,9 @@ struct Shape {
   static constexpr int scratch = kTile * row;
   static constexpr int warp = MODE == kForward ? scratch : 2 * scratch;
   static constexpr int items = 256;  // of a batch
-  // working warps of a CTA at most, as registers allow beside the filling warp; one CTA per SM, so
+  // working warps of a CTA at most, as registers allow beside the two that fill the ring; one CTA per SM, so
   // that all stages are one ring
-  static constexpr int warps = DV == 128 || MODE == kDq ? 11 : 15;
+  static constexpr int warps = DV == 128 || MODE == kDq ? 10 : 14;
 };
 constexpr int kStages = 8;  // of the ring at most
 
@@ -363,14 +358,14 @@ constexpr int kStages = 8;  // of the ring at most
 // bias, 1 shared memory, 2 global memory; 3 as 2, the bias gradient in global memory too.  NS: stages;
 // chunk: keys of a stage.
 template <int D, int MAPS, int TAB, int MODE>
-__global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 1), 1) window_rows_kernel(WinArgs a, int NS, int chunk) {
+__global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) window_rows_kernel(WinArgs a, int NS, int chunk) {
   using S = Shape<D, MAPS, MODE>;
   constexpr int DV = S::DV;
   constexpr bool BIAS = TAB != 0;
   extern __shared__ __align__(128) char sm[];
   __shared__ uint64_t full[kStages], empty[kStages];
   __shared__ int n_items;
-  const int NW = (int)blockDim.x / 32 - 1;  // working warps; one more fills the ring
+  const int NW = (int)blockDim.x / 32 - 2;  // working warps; two more fill the ring
   const uint32_t v_at = chunk * S::row, codes_at = 2 * v_at, stage_size = chunk * S::token;
   const int h = blockIdx.y, hk = h / (a.hq / a.hkv);
   const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3, warp = threadIdx.x >> 5;
@@ -390,7 +385,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 1), 1) win
       for (int i = threadIdx.x; i < 2 * T3; i += blockDim.x) limbs[i] = 0;
   }
   if (threadIdx.x < NS) {
-    tc::mbar_init(&full[threadIdx.x], 64);  // the filling warp's copies, and its stores of the codes
+    tc::mbar_init(&full[threadIdx.x], 96);  // two filling warps' copies, and the stores of the codes
     tc::mbar_init(&empty[threadIdx.x], NW);
   }
   tc::fence_mbar_init();
@@ -411,7 +406,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 1), 1) win
   // first: its forward walks the keys twice (twice through the ring where the cell has several chunks)
   constexpr int PASSES = MODE == kForward && MAPS == 2 ? 2 : 1;
   int rot = 0;                          // the warp that takes the next item's first tile
-  int fs = 0, fphase = warp == NW;      // stage and phase of the next fill (to make one never waits at first)
+  int fs = 0, fphase = warp >= NW;      // stage and phase of the next fill (to make one never waits at first)
   bool ok = true;
   for (int64_t batch = blockIdx.x; batch < a.T && ok; batch += (int64_t)S::items * gridDim.x) {
     // the batch's items, in the order of their slots
@@ -430,12 +425,24 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 1), 1) win
     }
     __syncthreads();
     const int count = n_items;
-    if (warp == NW) {
-      // the filling warp: lane l holds the rows l and 32 + l of the coming chunk
-      int2 e[2] = {};
+    if (warp >= NW) {
+      // the filling warps, one for the keys and the codes, one for the values: lane l holds the places
+      // (in units of 16 bytes) of the rows l and 32 + l of the coming chunk
+      constexpr int U = DV / 8, STEP = 32 / U;
+      const bool is_k = warp == NW;
+      const int r = lane / U, c = lane % U;
+      const uint4* src = static_cast<const uint4*>(is_k ? a.k : a.v) + c;
+      const uint4* near = static_cast<const uint4*>(is_k ? a.q : a.dout);
+      uint32_t at[2], qat[2];
+      int code[2];
       auto entries = [&](int k0, int hi) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) e[i] = __ldg(&a.rows[min(k0 + 32 * i + lane, hi - 1)]);
+        for (int i = 0; i < 2; ++i) {
+          const int2 e = __ldg(&a.rows[min(k0 + 32 * i + lane, hi - 1)]);
+          at[i] = (uint32_t)(((size_t)e.x * a.hkv + MAPS * hk) * (D / 8));
+          qat[i] = (uint32_t)(((size_t)e.x * a.hq + MAPS * h) * (D / 8));
+          code[i] = e.y;
+        }
       };
       if (count > 0) entries(items[0].z, items[0].w);
       for (int ii = 0; ii < count && ok; ++ii) {
@@ -446,29 +453,23 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 1), 1) win
           const int n = min(chunk, hi - k0);
           ok = ring_wait(&empty[fs], fphase);
           if (!ok) break;
-          const uint32_t kt = ring + fs * stage_size;
+          const uint32_t dst = ring + fs * stage_size + (is_k ? 0 : v_at);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (32 * x < n) {
-              constexpr int U = DV / 8, STEP = 32 / U;
-              const int r = lane / U, c = lane % U;
 #pragma unroll
               for (int y = 0; y < 32; y += STEP) {
-                const int k = 32 * x + y + r, p = key_at(k);
-                const size_t at =
-                    ((size_t)__shfl_sync(kFull, e[x].x, (y + r) & 31) * a.hkv + MAPS * hk) * D + 8 * c;
-                cp16(kt + unit<DV>(p, c), static_cast<const bf16*>(a.k) + at, k < n);
-                cp16(kt + v_at + unit<DV>(p, c), static_cast<const bf16*>(a.v) + at, k < n);
+                const uint32_t u = __shfl_sync(kFull, at[x], (y + r) & 31);
+                cp16(dst + unit<DV>(key_at(32 * x + y + r), c), src + u, 32 * x + y + r < n);
               }
-              if (BIAS) *reinterpret_cast<int*>(sm + fs * stage_size + codes_at + 4 * key_at(32 * x + lane)) = e[x].y;
-              // the item's queries are its keys: bring their rows near
-              const size_t at = ((size_t)e[x].x * a.hq + MAPS * h) * D;
-              prefetch(static_cast<const bf16*>(a.q) + at);
-              if (MODE != kForward) prefetch(static_cast<const bf16*>(a.dout) + at);
+              if (BIAS && is_k)
+                *reinterpret_cast<int*>(sm + fs * stage_size + codes_at + 4 * key_at(32 * x + lane)) = code[x];
+              // the item's queries are its keys: bring their rows (and dO's) near
+              if (is_k || MODE != kForward) prefetch(near + qat[x]);
             }
           }
           cp_arrive(&full[fs]);
-          tc::mbar_arrive(&full[fs]);
+          if (is_k) tc::mbar_arrive(&full[fs]);
           if (++fs == NS) fs = 0, fphase ^= 1;
           k0 += chunk;
           if (k0 >= hi) k0 = lo;
@@ -754,7 +755,7 @@ cudaError_t rows_pass(const char* name, const WinArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int heads = a.hq / MAPS;
   const int gx = grad && !a.wide ? a.parts : grid_x(heads, a.T, NW);
-  SSA_LAUNCH(name, kern, dim3(gx, heads), 32 * (NW + 1), smem, st, a, NS, chunk);
+  SSA_LAUNCH(name, kern, dim3(gx, heads), 32 * (NW + 2), smem, st, a, NS, chunk);
   return cudaGetLastError();
 }
 
