@@ -19,8 +19,6 @@ using bf16 = __nv_bfloat16;
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kChunk = 64;
-// Row tiles of a cell that belong together: they take the cell's keys from one passage of the ring.
-constexpr int kItem = 8;
 constexpr float kSlack = 8.f;
 constexpr size_t kSmemMost = 226 * 1024;  // dynamic shared memory of a CTA, beside the barriers
 
@@ -230,12 +228,11 @@ __device__ __forceinline__ float quad_sum(float x) {
 struct Limbs {
   float s, k, unit;  // 2^s, 2^k, 2^-s
   int kbits;
-  __device__ __forceinline__ void set(const WinArgs& a, int h) {
-    static_assert(SSA_WINDOW_TILE == 16, "rows of a slot");
+  __device__ __forceinline__ void set(const WinArgs& a, int h, int item_size) {
     const uint32_t bits = __ldg(a.amax + h);
     // rows of a CTA: its slots, each of which can start an item
     const int64_t slots = (a.T + (int64_t)gridDim.x - 1) / gridDim.x;
-    const int64_t rows = min((int64_t)a.N, slots * (kItem * kTile)), adds = rows * max(1, __ldg(&a.tiles[a.T].x));
+    const int64_t rows = min((int64_t)a.N, slots * (item_size * kTile)), adds = rows * max(1, __ldg(&a.tiles[a.T].x));
     const int rb = 64 - __clzll(rows), ab = 64 - __clzll(adds);  // rows < 2^rb, adds < 2^ab
     const int e = (int)(bits >> 23) - 126;                       // M < 2^e
     int sb = min(30 - rb - 1 - e, 20 - e);                       // |dS 2^s| < 2^22: see add()
@@ -326,12 +323,12 @@ __device__ __forceinline__ void finish_scores(float (*s)[4], const int* codes, i
 }
 
 
-// Number of tiles of the item that starts at a slot: 0 for empty slots and those inside an item.
-template <int ITEM>
-__device__ __forceinline__ int item_tiles(const int4& tile) {
+// Number of tiles of the item (up to `size` row tiles of a cell, which take the cell's keys from one
+// passage of the ring) that starts at a slot: 0 for empty slots and those inside an item.
+__device__ __forceinline__ int item_tiles(const int4& tile, int size) {
   if ((tile.y & (kDupFlag - 1)) == 0) return 0;
   const int at = (unsigned)(tile.x - tile.z) / kTile, all = (unsigned)(tile.w - tile.z + kTile - 1) / kTile;
-  return at % ITEM == 0 ? min(ITEM, all - at) : 0;
+  return at % size == 0 ? min(size, all - at) : 0;
 }
 
 // What a walk over the rows does with the keys.
@@ -356,9 +353,10 @@ constexpr int kStages = 8;  // of the ring at most
 // One kernel body for the forward, the row statistics of the backward, and dq with the bias
 // gradient: they share the walk over cells, keys and scores.  TAB: where the bias is read: 0 no
 // bias, 1 shared memory, 2 global memory; 3 as 2, the bias gradient in global memory too.  NS: stages;
-// chunk: keys of a stage.
+// chunk: keys of a stage; pairs: heads of the CTA (1, or 2 that share a key head), whose tiles are
+// work of their own from the same stages.
 template <int D, int MAPS, int TAB, int MODE>
-__global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) window_rows_kernel(WinArgs a, int NS, int chunk) {
+__global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) window_rows_kernel(WinArgs a, int NS, int chunk, int pairs) {
   using S = Shape<D, MAPS, MODE>;
   constexpr int DV = S::DV;
   constexpr bool BIAS = TAB != 0;
@@ -367,22 +365,24 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
   __shared__ int n_items;
   const int NW = (int)blockDim.x / 32 - 2;  // working warps; two more fill the ring
   const uint32_t v_at = chunk * S::row, codes_at = 2 * v_at, stage_size = chunk * S::token;
-  const int h = blockIdx.y, hk = h / (a.hq / a.hkv);
+  const int h0 = pairs * blockIdx.y, hk = h0 / (a.hq / a.hkv), item_size = NW / pairs;
   const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3, warp = threadIdx.x >> 5;
   const int T3 = BIAS ? offsets(a.m) : 0, c0 = BIAS ? center(a.m) : 0;
   const bool grad = MODE == kDq && BIAS && a.dbias;
   int4* items = reinterpret_cast<int4*>(sm + NS * stage_size + NW * S::warp);
-  int* limbs = reinterpret_cast<int*>(items + S::items);  // [2][T3] with a bias gradient, not wide
-  float* tab_s = reinterpret_cast<float*>(limbs + (grad && TAB != 3 ? 2 * T3 : 0));
-  const float* tab = TAB >= 2 ? a.tab2 + (size_t)h * table_pitch(a.m) : tab_s;
+  int* limbs = reinterpret_cast<int*>(items + S::items);  // [pairs][2][T3] with a bias gradient, not wide
+  float* tab_s = reinterpret_cast<float*>(limbs + (grad && TAB != 3 ? pairs * 2 * T3 : 0));
+  const float* tab = TAB >= 2 ? a.tab2 + (size_t)h0 * table_pitch(a.m) : tab_s;
+  const int tab_pitch = TAB >= 2 ? table_pitch(a.m) : T3;
   const uint32_t ring = tc::smem_u32(sm);
   const uint32_t scratch = tc::smem_u32(sm + NS * stage_size + warp * S::warp), scratch2 = scratch + S::scratch;
   const float mul = a.scale * kLog2e;
   if constexpr (BIAS) {
     if (TAB == 1)
-      for (int i = threadIdx.x; i < T3; i += blockDim.x) tab_s[i] = bias2_at(a, h, i);
+      for (int i = threadIdx.x; i < pairs * T3; i += blockDim.x)
+        tab_s[i] = i < T3 ? bias2_at(a, h0, i) : bias2_at(a, h0 + 1, i - T3);
     if (grad && TAB != 3)
-      for (int i = threadIdx.x; i < 2 * T3; i += blockDim.x) limbs[i] = 0;
+      for (int i = threadIdx.x; i < pairs * 2 * T3; i += blockDim.x) limbs[i] = 0;
   }
   if (threadIdx.x < NS) {
     tc::mbar_init(&full[threadIdx.x], 96);  // two filling warps' copies, and the stores of the codes
@@ -391,16 +391,21 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
   tc::fence_mbar_init();
   Limbs fx;
   Wide wide;
-  if (grad && TAB != 3) fx.set(a, h);
-  if (grad && TAB == 3) wide.set(a, h);
-  float lam = 0.f;
+  float s2[2] = {0.f, 0.f};
+  if (grad && TAB != 3)
+    for (int i = pairs - 1; i >= 0; --i) {
+      fx.set(a, h0 + i, item_size);
+      (i ? s2[1] : s2[0]) = fx.s;
+    }
+  float lams[2] = {0.f, 0.f};
   if constexpr (MAPS == 2) {
-    float e1, e2;
-    lambda_terms<D>(a.lam, a.hq / 2, h, e1, e2);
-    lam = e1 - e2 + a.lam_init;
+    for (int i = 0; i < pairs; ++i) {
+      float e1, e2;
+      lambda_terms<D>(a.lam, a.hq / 2, h0 + i, e1, e2);
+      (i ? lams[1] : lams[0]) = e1 - e2 + a.lam_init;
+    }
   }
-  const Rows Q = {a.q, a.hq, MAPS * h}, O = {a.dout, a.hq, MAPS * h};
-  uint32_t top = 0;  // the largest |dP|, as bits: NaN above all
+  uint32_t tops[2] = {0, 0};  // the largest |dP| of a head, as bits: NaN above all
 
   // differential attention subtracts the maps before the product with V, so both normalisers come
   // first: its forward walks the keys twice (twice through the ring where the cell has several chunks)
@@ -416,7 +421,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
       for (int i0 = 0; i0 < S::items; i0 += 32) {
         const int64_t t = batch + (int64_t)(i0 + lane) * gridDim.x;
         int4 x = t < a.T ? __ldg(&a.tiles[t]) : make_int4(0, 0, 0, 0);
-        x.y = item_tiles<kItem>(x);
+        x.y = item_tiles(x, item_size);
         const unsigned some = __ballot_sync(kFull, x.y > 0);
         if (x.y > 0) items[n + __popc(some & ((1u << lane) - 1u))] = x;
         n += __popc(some);
@@ -440,8 +445,9 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
         for (int i = 0; i < 2; ++i) {
           const int2 e = __ldg(&a.rows[min(k0 + 32 * i + lane, hi - 1)]);
           at[i] = (uint32_t)(((size_t)e.x * a.hkv + MAPS * hk) * (D / 8));
-          qat[i] = (uint32_t)(((size_t)e.x * a.hq + MAPS * h) * (D / 8));
-          code[i] = e.y;
+          qat[i] = (uint32_t)(((size_t)e.x * a.hq + MAPS * h0) * (D / 8));
+          // places without a key: codes that spread their (zero) shares of the bias gradient
+          code[i] = k0 + 32 * i + lane < hi ? e.y : (32 * i + lane) * 17 % (c0 + 1);
         }
       };
       if (count > 0) entries(items[0].z, items[0].w);
@@ -465,7 +471,10 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
               if (BIAS && is_k)
                 *reinterpret_cast<int*>(sm + fs * stage_size + codes_at + 4 * key_at(32 * x + lane)) = code[x];
               // the item's queries are its keys: bring their rows (and dO's) near
-              if (is_k || MODE != kForward) prefetch(near + qat[x]);
+              if (is_k || MODE != kForward) {
+                prefetch(near + qat[x]);
+                if (pairs == 2 && DV >= 64) prefetch(near + qat[x] + DV / 8);
+              }
             }
           }
           cp_arrive(&full[fs]);
@@ -486,10 +495,20 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
       const int lo = item.z, hi = item.w;
       int mine = warp - rot;
       if (mine < 0) mine += NW;
-      const bool on = mine < item.y, one = hi - lo <= chunk;
-      rot += item.y;
+      const bool on = mine < pairs * item.y, one = hi - lo <= chunk;
+      rot += pairs * item.y;
       if (rot >= NW) rot -= NW;
-      const int first = item.x + kTile * mine, nr = min(kTile, hi - first);
+      const int pair = mine >= item.y ? 1 : 0;  // the head among the CTA's
+      const int first = item.x + kTile * (mine - pair * item.y), nr = min(kTile, hi - first);
+      const int h = h0 + pair;
+      const float lam = pair ? lams[1] : lams[0];
+      uint32_t top = 0;
+      if (grad && on) {
+        if (TAB == 3)
+          wide.set(a, h);
+        else
+          fx.s = pair ? s2[1] : s2[0];
+      }
       constexpr int NACC = MODE == kStats ? 1 : DV / 8;
       float m[MAPS][2], l[MAPS][2], dd[MAPS][2], acc[NACC][4];
       uint32_t q[DV / 16][4], o[MODE == kForward ? 1 : DV / 16][4];
@@ -497,14 +516,16 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
       int ci = 0, ci8 = 0;
       if (on) {
         __syncwarp();
+        const Rows Q = {a.q, a.hq, MAPS * h}, O = {a.dout, a.hq, MAPS * h};
         stage<D, DV, kTile, 32, MODE != kForward>(scratch, Q, scratch2, O, a.rows, first, nr, lane, 0,
                                                   [](int k) { return k; }, [](int, int, const int2&, int) {});
         cp_commit();
         if (BIAS) {
-          ci = __ldg(&a.rows[first + min(g, nr - 1)].y) + c0;
-          ci8 = __ldg(&a.rows[first + min(g + 8, nr - 1)].y) + c0;
-          t0 = tab + ci;
-          t8 = tab + ci8;
+          // rows without a token: codes that spread their (zero) shares of the bias gradient
+          ci = c0 + (g < nr ? __ldg(&a.rows[first + g].y) : g * 13 % (c0 + 1));
+          ci8 = c0 + (g + 8 < nr ? __ldg(&a.rows[first + g + 8].y) : (g + 8) * 13 % (c0 + 1));
+          t0 = tab + pair * tab_pitch + ci;
+          t8 = tab + pair * tab_pitch + ci8;
         }
 #pragma unroll
         for (int u = 0; u < MAPS; ++u)
@@ -573,11 +594,11 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
                     }
                   if (BIAS) {
                     if (grad) {
+                      int* to = limbs + pair * 2 * T3;
                       if constexpr (TAB == 3)
                         add_bias_grad([&](int at, float x) { wide.add(at, x); }, s[0], hc, ci, ci8);
                       else
-                        add_bias_grad([&](int at, float x) { fx.add(limbs + at, limbs + T3 + at, x); }, s[0], hc, ci,
-                                      ci8);
+                        add_bias_grad([&](int at, float x) { fx.add(to + at, to + T3 + at, x); }, s[0], hc, ci, ci8);
                     }
                   }
                   uint32_t f[2][4];
@@ -687,6 +708,10 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
               if (!(l[u][i] >= 0.f)) top = 0x7fffffffu;
             }
           }
+        if (pair)
+          tops[1] = max(tops[1], top);
+        else
+          tops[0] = max(tops[0], top);
       } else {
         store_acc<D, DV>(scratch, acc, a.scale, a.scale, static_cast<bf16*>(a.dq), a.hq, MAPS * h, a.rows, first, nr);
       }
@@ -696,13 +721,19 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
   cp_wait<0>();
   if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
   if constexpr (MODE == kStats && BIAS) {
-    top = __reduce_max_sync(kFull, top);
-    if (lane == 0 && a.dbias) atomicMax(a.amax + h, top);
+    for (int i = 0; i < pairs; ++i) {
+      const uint32_t top = __reduce_max_sync(kFull, i ? tops[1] : tops[0]);
+      if (lane == 0 && a.dbias) atomicMax(a.amax + h0 + i, top);
+    }
   }
   if (grad && TAB != 3) {
     __syncthreads();
-    float* part = a.part + ((size_t)h * a.parts + blockIdx.x) * T3;
-    for (int i = threadIdx.x; i < T3; i += blockDim.x) part[i] = fx.value(limbs[i], limbs[T3 + i]);
+    for (int p = 0; p < pairs; ++p) {
+      fx.set(a, h0 + p, item_size);
+      const int* from = limbs + p * 2 * T3;
+      float* part = a.part + ((size_t)(h0 + p) * a.parts + blockIdx.x) * T3;
+      for (int i = threadIdx.x; i < T3; i += blockDim.x) part[i] = fx.value(from[i], from[T3 + i]);
+    }
   }
 }
 
@@ -725,37 +756,37 @@ cudaError_t rows_pass(const char* name, const WinArgs& a, cudaStream_t st) {
   constexpr int ON = BIAS ? 1 : 0;
   const bool grad = MODE == kDq && BIAS && a.dbias;
   const size_t T3 = BIAS ? offsets(a.m) : 0, list = sizeof(int4) * S::items;
-  const size_t limbs = grad && !a.wide ? 8 * T3 : 0;
-  // Chunks of 64 keys, of 32 where cells are so small that more of them in flight count for more
-  // than fewer steps, or where no more fits.  The bias lies in shared memory where room is left beside
-  // it for eight warps and three stages (the forward always has it there); then as many warps as may
-  // be and as many stages as fit.
-  int chunk = a.N <= 24 * (int64_t)a.cells ? 32 : kChunk, NW = 0, NS = 0;
+  // Two heads to a CTA where they share a key head: the stages then serve twice the work.  Chunks of
+  // 64 keys, of 32 where cells are so small that more of them in flight count for more than fewer
+  // steps.  The bias lies in shared memory where room is left beside it for eight warps and four
+  // stages (the forward always has it there); then as many warps as may be, and as many stages as fit.
+  // What does not fit takes one head, then small chunks, then three stages.
+  int chunk = 0, pairs = 0, NW = 0, NS = 0;
   bool in_smem = false;
   size_t smem = 0;
-  for (;; chunk = 32) {
-    const size_t stage = (size_t)chunk * S::token, least = list + limbs + kItem * S::warp + 3 * stage;
-    in_smem = BIAS && !(grad && a.wide) && least + 4 * T3 <= kSmemMost;
-    const size_t fixed = list + limbs + (in_smem ? 4 * T3 : 0);
-    if (least <= kSmemMost && (in_smem || !BIAS || MODE != kForward)) {
-      NW = (int)min((size_t)S::warps, (kSmemMost - fixed - 3 * stage) / S::warp);
-      NS = (int)min((size_t)kStages, (kSmemMost - fixed - NW * S::warp) / stage);
-      smem = fixed + NW * S::warp + NS * stage;
-      break;
-    }
-    if (chunk == 32) return cudaErrorInvalidConfiguration;
+  for (int attempt = 0; attempt < 4 && !smem; ++attempt) {
+    pairs = attempt == 0 && a.hq / a.hkv % 2 == 0 ? 2 : 1;
+    chunk = attempt >= 2 || a.N <= 24 * (int64_t)a.cells ? 32 : kChunk;
+    const size_t stage = (size_t)chunk * S::token, table = 4 * T3 * pairs, limbs = grad && !a.wide ? 8 * T3 * pairs : 0;
+    const size_t least = list + limbs + 8 * S::warp + (attempt == 3 ? 3 : 4) * stage;
+    in_smem = BIAS && !(grad && a.wide) && least + table <= kSmemMost;
+    if (least > kSmemMost || (BIAS && !in_smem && (MODE == kForward || attempt == 0))) continue;
+    const size_t fixed = list + limbs + (in_smem ? table : 0);
+    NW = (int)min((size_t)S::warps, (kSmemMost - fixed - (attempt == 3 ? 3 : 4) * stage) / S::warp);
+    NS = (int)min((size_t)kStages, (kSmemMost - fixed - NW * S::warp) / stage);
+    smem = fixed + NW * S::warp + NS * stage;
   }
+  if (!smem) return cudaErrorInvalidConfiguration;  // no edge that a bias can have comes here
   auto kern = window_rows_kernel<D, MAPS, ON, MODE>;
   if constexpr (MODE != kForward)
     if (!in_smem) kern = window_rows_kernel<D, MAPS, 2 * ON, MODE>;
   if constexpr (MODE == kDq)
     if (grad && a.wide) kern = window_rows_kernel<D, MAPS, 3 * ON, MODE>;
-  if (NW < kItem || NS < 3 || smem > kSmemMost) return cudaErrorInvalidConfiguration;
   const cudaError_t e = need_smem(kern, smem);
   if (e != cudaSuccess) return e;
-  const int heads = a.hq / MAPS;
-  const int gx = grad && !a.wide ? a.parts : grid_x(heads, a.T, NW);
-  SSA_LAUNCH(name, kern, dim3(gx, heads), 32 * (NW + 2), smem, st, a, NS, chunk);
+  const int heads = a.hq / MAPS / pairs;
+  const int gx = grad && !a.wide ? a.parts : grid_x(heads, a.T, NW / pairs);
+  SSA_LAUNCH(name, kern, dim3(gx, heads), 32 * (NW + 2), smem, st, a, NS, chunk, pairs);
   return cudaGetLastError();
 }
 
@@ -769,7 +800,7 @@ cudaError_t rows_pass(const char* name, const WinArgs& a, cudaStream_t st) {
 constexpr int kDkvWarps = 4;
 
 // Number of key tiles of the CTA of a slot: four from every fourth tile of a cell.
-__device__ __forceinline__ int dkv_tiles(const int4& tile) { return item_tiles<kDkvWarps>(tile); }
+__device__ __forceinline__ int dkv_tiles(const int4& tile) { return item_tiles(tile, kDkvWarps); }
 
 template <int D, int MAPS>
 struct DkvShape {
