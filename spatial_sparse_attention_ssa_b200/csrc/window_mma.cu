@@ -64,7 +64,7 @@ __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity) {
   if (__all_sync(kFull, tc::mbar_try_wait(bar, parity))) return true;
   const uint64_t t0 = tc::global_ns();
   for (uint32_t i = 1;; ++i) {
-    __nanosleep(i < 4 ? 50 : 150);
+    __nanosleep(i < 4 ? 40 : 100);
     if (__all_sync(kFull, tc::mbar_try_wait(bar, parity))) return true;
     if ((i & 255u) == 0 && __any_sync(kFull, tc::global_ns() - t0 > tc::kWaitLimitNs)) return false;
   }
@@ -785,7 +785,7 @@ cudaError_t rows_pass(const char* name, const WinArgs& a, cudaStream_t st) {
   const cudaError_t e = need_smem(kern, smem);
   if (e != cudaSuccess) return e;
   const int heads = a.hq / MAPS / pairs;
-  const int gx = grad && !a.wide ? a.parts : grid_x(heads, a.T, NW / pairs);
+  const int gx = grad && !a.wide ? a.parts : grid_x(heads, a.T, 2);
   SSA_LAUNCH(name, kern, dim3(gx, heads), 32 * (NW + 2), smem, st, a, NS, chunk, pairs);
   return cudaGetLastError();
 }
@@ -833,24 +833,44 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
   const uint32_t base = tc::smem_u32(sm), kt = base + (S::held ? S::stage : 0), vt = kt + S::KT;
   const int keys0 = tile.x, nkeys = min(kTile * nt, hi - keys0);
 
-  // a step: query head h, 64 queries from k0 on, into stage `st`; a head's first step brings its table
+  // a step: query head h, 64 queries from k0 on, into stage `st`; a head's first step brings its table.
+  // The places of the queries' rows (in units of 16 bytes) and their codes stay while k0 does.
+  constexpr int U = DV / 8, STEP = NTH / U, IT = kChunk / STEP;
+  const int ur = tid / U, uc = tid % U;
+  uint32_t place[IT];
+  int k_now = -1, cst = 1;
   auto load = [&](int h, int k0, int st) {
     const int n = min(kChunk, hi - k0);
-    const uint32_t q = base + S::Q + st * S::stage;
-    int* codes = reinterpret_cast<int*>(sm + S::codes) + st * kChunk;
-    const Rows Q = {a.q, a.hq, MAPS * h}, O = {a.dout, a.hq, MAPS * h};
-#pragma unroll 1
-    for (int x = 0; x < n; x += 32)
-      stage<D, DV, 32, NTH, true>(q, Q, q + S::KT, O, a.rows, k0, n, tid, x, [](int k) { return k; },
-                                  [&](int p, int, const int2& e, int c) {
-                                    if (BIAS && c == 0) codes[p] = e.y + c0;
-                                  });
-    float* stat = reinterpret_cast<float*>(sm + S::Q + st * S::stage + S::stat);
+    if (k0 != k_now) {
+      k_now = k0;
+      cst ^= 1;
+      int* codes = reinterpret_cast<int*>(sm + S::codes) + cst * kChunk;
 #pragma unroll
-    for (int i = 0; i < MAPS; ++i) {  // 64 threads a row of lse2, 64 a row of D
-      const int u = i, which = tid / kChunk, c = tid % kChunk;
-      const float* src = (which ? a.D : a.lse2) + (size_t)(MAPS * h + u) * a.N + k0;
-      stat[(2 * u + which) * kChunk + c] = c < n ? src[c] : which ? 0.f : kPosInf;
+      for (int i = 0; i < IT; ++i) {
+        const int2 e = __ldg(&a.rows[k0 + min(i * STEP + ur, n - 1)]);
+        place[i] = (uint32_t)((size_t)e.x * a.hq * (D / 8)) + uc;
+        if (BIAS && uc == 0) codes[i * STEP + ur] = e.y + c0;
+      }
+    }
+    const uint32_t q = base + S::Q + st * S::stage;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int r = i * STEP + ur;
+      if (i * STEP < ((n + 31) & ~31)) {
+        const uint32_t at = place[i] + MAPS * h * (D / 8);
+        cp16(q + unit<DV>(r, uc), static_cast<const uint4*>(a.q) + at, r < n);
+        cp16(q + S::KT + unit<DV>(r, uc), static_cast<const uint4*>(a.dout) + at, r < n);
+      }
+    }
+    const uint32_t stat = q + S::stat;
+#pragma unroll
+    for (int u = 0; u < MAPS; ++u) {  // 64 threads a row of lse2, 64 a row of D
+      const int which = tid / kChunk, c = tid % kChunk;
+      const uint32_t dst = stat + 4 * ((2 * u + which) * kChunk + c);
+      if (c < n)
+        cp4(dst, (which ? a.D : a.lse2) + (size_t)(MAPS * h + u) * a.N + k0 + c);
+      else
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst), "f"(which ? 0.f : kPosInf) : "memory");
     }
     if (TAB == 1 && k0 == lo) {
       const uint32_t dst = base + S::tab + (h & 1) * T3p * 4;
@@ -890,7 +910,7 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
     __syncthreads();
   }
 
-  int h = hk * G, k0 = lo, stg = 0;
+  int h = hk * G, k0 = lo, stg = 0, cnow = cst;
   while (true) {
     int h2 = h, k2 = k0 + kChunk;  // the step after this one
     if (k2 >= hi) k2 = lo, ++h2;
@@ -912,7 +932,7 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
       }
       const uint32_t qt = base + S::Q + stg * S::stage, ot = qt + S::KT;
       const float* stat = reinterpret_cast<const float*>(sm + S::Q + stg * S::stage + S::stat);
-      const int* codes = reinterpret_cast<const int*>(sm + S::codes) + stg * kChunk;
+      const int* codes = reinterpret_cast<const int*>(sm + S::codes) + cnow * kChunk;
       const float* tab = TAB == 2 ? a.tab2 + (size_t)h * T3p
                                   : reinterpret_cast<const float*>(sm + S::tab) + (h & 1) * T3p;
       const float *tk = tab - ck, *tk8 = tab - ck8;
@@ -973,6 +993,7 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
     h = h2;
     k0 = k2;
     stg ^= 1;
+    cnow = cst;
   }
   if (!on) return;
   // the stages are free now; 16 rows of scratch per warp
