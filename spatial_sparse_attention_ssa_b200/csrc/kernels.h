@@ -184,6 +184,7 @@ struct WinArgs {
 };
 cudaError_t window_plan(const int32_t* coords, int64_t N, int m, const ssa_partition* win, int2* rows, int4* tiles,
                         int* status, cudaStream_t st);
+constexpr int kSms = 148;
 // Window edges from here on keep the bias gradient of the bf16 kernels in global memory: 8 bytes per
 // offset are 125 KB, too many beside the ring of keys and eight warps' rows in shared memory.
 constexpr int kWideEdge = 13;

@@ -344,9 +344,7 @@ struct Shape {
   static constexpr int scratch = kTile * row;
   static constexpr int warp = MODE == kForward ? scratch : 2 * scratch;
   static constexpr int items = 256;  // of a batch
-  // working warps of a CTA at most, as registers allow beside the two that fill the ring; one CTA per SM, so
-  // that all stages are one ring
-  static constexpr int warps = DV == 128 || MODE == kDq ? 10 : 14;
+  static constexpr int warps = DV == 128 ? 6 : MODE == kDq || MAPS == 2 ? 10 : 14;
 };
 constexpr int kStages = 8;  // of the ring at most
 
@@ -418,7 +416,8 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
     __syncthreads();
     if (warp == NW) {
       int n = 0;
-      for (int i0 = 0; i0 < S::items; i0 += 32) {
+#pragma unroll 2
+      for (int i0 = 0; i0 < S::items && batch + (int64_t)i0 * gridDim.x < a.T; i0 += 32) {
         const int64_t t = batch + (int64_t)(i0 + lane) * gridDim.x;
         int4 x = t < a.T ? __ldg(&a.tiles[t]) : make_int4(0, 0, 0, 0);
         x.y = item_tiles(x, item_size);
@@ -737,11 +736,11 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
   }
 }
 
-// CTAs along the slots for `heads` heads: about six for every SM, so that the last ones to finish
-// leave little idle, but no more than the slots fill.
-int grid_x(int heads, int T, int per_cta) {
-  const int need = (T + per_cta - 1) / per_cta, want = 6 * 148 / heads;
-  return want < 1 ? 1 : need < want ? need : want;
+// CTAs along the slots for `heads` (pairs of) heads: up to six for every SM, so that the last ones to
+// finish leave little idle, but no more than one while that gives a CTA fewer than 16 slots.
+int grid_x(int64_t heads, int64_t T) {
+  const int64_t waves = max((int64_t)1, min((int64_t)6, heads * T / (16 * kSms)));
+  return (int)max((int64_t)1, min(T, waves * kSms / heads));
 }
 
 template <typename K>
@@ -765,10 +764,10 @@ cudaError_t rows_pass(const char* name, const WinArgs& a, cudaStream_t st) {
   bool in_smem = false;
   size_t smem = 0;
   for (int attempt = 0; attempt < 4 && !smem; ++attempt) {
-    pairs = attempt == 0 && a.hq / a.hkv % 2 == 0 ? 2 : 1;
+    pairs = attempt == 0 && a.hq / a.hkv % 2 == 0 && S::warps >= 10 ? 2 : 1;
     chunk = attempt >= 2 || a.N <= 24 * (int64_t)a.cells ? 32 : kChunk;
     const size_t stage = (size_t)chunk * S::token, table = 4 * T3 * pairs, limbs = grad && !a.wide ? 8 * T3 * pairs : 0;
-    const size_t least = list + limbs + 8 * S::warp + (attempt == 3 ? 3 : 4) * stage;
+    const size_t least = list + limbs + min(8, S::warps) * S::warp + (attempt == 3 ? 3 : 4) * stage;
     in_smem = BIAS && !(grad && a.wide) && least + table <= kSmemMost;
     if (least > kSmemMost || (BIAS && !in_smem && (MODE == kForward || attempt == 0))) continue;
     const size_t fixed = list + limbs + (in_smem ? table : 0);
@@ -785,7 +784,7 @@ cudaError_t rows_pass(const char* name, const WinArgs& a, cudaStream_t st) {
   const cudaError_t e = need_smem(kern, smem);
   if (e != cudaSuccess) return e;
   const int heads = a.hq / MAPS / pairs;
-  const int gx = grad && !a.wide ? a.parts : grid_x(heads, a.T, 2);
+  const int gx = grad && !a.wide ? a.parts : grid_x(heads, a.T);
   SSA_LAUNCH(name, kern, dim3(gx, heads), 32 * (NW + 2), smem, st, a, NS, chunk, pairs);
   return cudaGetLastError();
 }

@@ -530,11 +530,12 @@ cudaError_t window_bwd_simt(const WinArgs& a, cudaStream_t st) {
   return a.act8 ? bwd_d<int8_t, float>(a, st) : bwd_d<float, float>(a, st);
 }
 
-// About six CTAs for every SM: few enough for the sums of their tables, enough that the last ones
-// to finish leave little idle.
+// Up to six CTAs for every SM (three of the bf16 kernel, which takes two heads each): few enough for
+// the sums of their tables, enough that the last ones to finish leave little idle; one or two while
+// that gives a CTA fewer than 16 slots.
 int window_parts(int hq, int64_t T) {
-  const int64_t x = (6 * 148) / hq;
-  return (int)(x < 1 || T < 1 ? 1 : x < T ? x : T);
+  const int64_t waves = max((int64_t)1, min((int64_t)3, hq * T / (32 * kSms)));
+  return (int)max((int64_t)1, min(T, 2 * waves * kSms / hq));
 }
 
 }  // namespace ssa
