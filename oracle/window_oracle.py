@@ -155,7 +155,8 @@ def diff(ids, count, q, k, v, dout, scale, lam, lam_init, u=0.0, u_out=0.0):
             w = p1 - L * p2
             ew = p1 * ep1 + abs(L) * p2 * (ep2 + 2 * EPS) + eL * p2
             o = w @ vj
-            eo = (ew + np.abs(w) * (u + add)) @ np.abs(vj)
+            # the forward rounds each map on its own: u (p1 + |lambda| p2), not u |p1 - lambda p2|
+            eo = (ew + (p1 + abs(L) * p2) * (u + add)) @ np.abs(vj)
             gv = w.T @ do
             ev = (ew + np.abs(w) * (u + g * add)).T @ np.abs(do)
             for x in (0, 1):

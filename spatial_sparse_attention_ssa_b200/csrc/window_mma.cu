@@ -155,8 +155,8 @@ __device__ __forceinline__ void contract_dim(const uint32_t (*a)[4], uint32_t ti
   }
 }
 
-// acc += P B, P as A fragments over NK groups of 16 rows of B (as above).
-template <int PW, int W, int NK>
+// acc_h += P_h B for h < NA, P_h as A fragments over NK groups of 16 rows of B (as above).
+template <int PW, int W, int NK, int NA = 1>
 __device__ __forceinline__ void contract_rows(const uint32_t (*p)[4], uint32_t tile, int u0, float (*acc)[4]) {
   const int lane = threadIdx.x & 31, row = lane & 15, c = lane >> 4;
 #pragma unroll
@@ -165,8 +165,11 @@ __device__ __forceinline__ void contract_rows(const uint32_t (*p)[4], uint32_t t
     for (int e = 0; e < W / 16; ++e) {
       uint32_t b[4];
       ldsm_t(b, tile + unit<PW>(16 * k + row, u0 + 2 * e + c));
-      mma(acc[2 * e], p[k], b[0], b[1]);
-      mma(acc[2 * e + 1], p[k], b[2], b[3]);
+#pragma unroll
+      for (int h = 0; h < NA; ++h) {
+        mma(acc[h * (W / 8) + 2 * e], p[h * NK + k], b[0], b[1]);
+        mma(acc[h * (W / 8) + 2 * e + 1], p[h * NK + k], b[2], b[3]);
+      }
     }
   }
 }
@@ -344,7 +347,7 @@ struct Shape {
   static constexpr int scratch = kTile * row;
   static constexpr int warp = MODE == kForward ? scratch : 2 * scratch;
   static constexpr int items = 256;  // of a batch
-  static constexpr int warps = DV == 128 ? 6 : MODE == kDq || MAPS == 2 ? 10 : 14;
+  static constexpr int warps = DV == 128 && MODE != kStats ? 6 : DV == 128 || MODE == kDq || MAPS == 2 ? 10 : 14;
 };
 constexpr int kStages = 8;  // of the ring at most
 
@@ -405,9 +408,6 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
   }
   uint32_t tops[2] = {0, 0};  // the largest |dP| of a head, as bits: NaN above all
 
-  // differential attention subtracts the maps before the product with V, so both normalisers come
-  // first: its forward walks the keys twice (twice through the ring where the cell has several chunks)
-  constexpr int PASSES = MODE == kForward && MAPS == 2 ? 2 : 1;
   int rot = 0;                          // the warp that takes the next item's first tile
   int fs = 0, fphase = warp >= NW;      // stage and phase of the next fill (to make one never waits at first)
   bool ok = true;
@@ -452,9 +452,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
       if (count > 0) entries(items[0].z, items[0].w);
       for (int ii = 0; ii < count && ok; ++ii) {
         const int lo = items[ii].z, hi = items[ii].w;
-        const int fills = hi - lo <= chunk ? 1 : PASSES * ((hi - lo + chunk - 1) / chunk);
-        int k0 = lo;
-        for (int i = 0; i < fills && ok; ++i) {
+        for (int k0 = lo; k0 < hi; k0 += chunk) {
           const int n = min(chunk, hi - k0);
           ok = ring_wait(&empty[fs], fphase);
           if (!ok) break;
@@ -479,10 +477,8 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
           cp_arrive(&full[fs]);
           if (is_k) tc::mbar_arrive(&full[fs]);
           if (++fs == NS) fs = 0, fphase ^= 1;
-          k0 += chunk;
-          if (k0 >= hi) k0 = lo;
-          if (i + 1 < fills)
-            entries(k0, hi);
+          if (k0 + chunk < hi)
+            entries(k0 + chunk, hi);
           else if (ii + 1 < count)
             entries(items[ii + 1].z, items[ii + 1].w);
         }
@@ -494,7 +490,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
       const int lo = item.z, hi = item.w;
       int mine = warp - rot;
       if (mine < 0) mine += NW;
-      const bool on = mine < pairs * item.y, one = hi - lo <= chunk;
+      const bool on = mine < pairs * item.y;
       rot += pairs * item.y;
       if (rot >= NW) rot -= NW;
       const int pair = mine >= item.y ? 1 : 0;  // the head among the CTA's
@@ -508,7 +504,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
         else
           fx.s = pair ? s2[1] : s2[0];
       }
-      constexpr int NACC = MODE == kStats ? 1 : DV / 8;
+      constexpr int NACC = MODE == kStats ? 1 : MODE == kForward ? MAPS * DV / 8 : DV / 8;
       float m[MAPS][2], l[MAPS][2], dd[MAPS][2], acc[NACC][4];
       uint32_t q[DV / 16][4], o[MODE == kForward ? 1 : DV / 16][4];
       const float *t0 = tab, *t8 = tab;
@@ -542,8 +538,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
         for (int e = 0; e < NACC; ++e) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
       }
       bool fresh = true;
-#pragma unroll 1
-      for (int turn = 0; turn < (one ? 1 : PASSES); ++turn) {
+      {
 #pragma unroll 1
         for (int k0 = lo; k0 < hi; k0 += chunk) {
           const int n = min(chunk, hi - k0);
@@ -567,8 +562,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
               if constexpr (MODE != kForward) load_a<DV>(o[d], scratch2, 0, d);
             }
           }
-#pragma unroll 1
-          for (int pass = one ? 0 : turn; pass < (one ? PASSES : turn + 1); ++pass) {
+          {
 #pragma unroll 1
             for (int half = 0; half < n; half += 32) {
               const uint32_t kt = kst + half * S::row, vt = kt + v_at;
@@ -613,14 +607,6 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
                 for (int u = 0; u < MAPS; ++u)
 #pragma unroll
                   for (int i = 0; i < 2; ++i) {
-                    if (PASSES == 2 && pass == 1) {
-                      const float f = (u ? -lam : 1.f) * l[u][i], ms = safe_max(m[u][i]);
-#pragma unroll
-                      for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) s[u][j][2 * i + x] = ex2(s[u][j][2 * i + x] - ms) * f;
-                      continue;
-                    }
                     float mx = kNegInf;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(s[u][j][2 * i], s[u][j][2 * i + 1]));
@@ -646,32 +632,27 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
                     m[u][i] = mx;
                   }
                 if constexpr (MODE == kForward) {
-                  if (MAPS == 1 && half + k0 > lo && __any_sync(kFull, old[0][0] != 1.f || old[0][1] != 1.f)) {
+                  if (half + k0 > lo) {
+                    bool grown = false;
 #pragma unroll
-                    for (int e = 0; e < NACC; ++e)
+                    for (int u = 0; u < MAPS; ++u) grown |= old[u][0] != 1.f || old[u][1] != 1.f;
+                    if (__any_sync(kFull, grown)) {
 #pragma unroll
-                      for (int x = 0; x < 4; ++x) acc[e][x] *= old[0][x >> 1];
-                  }
-                  if (PASSES == 1 || pass == 1) {
-                    if constexpr (MAPS == 2) {
+                      for (int u = 0; u < MAPS; ++u)
 #pragma unroll
-                      for (int j = 0; j < 4; ++j)
+                        for (int e = 0; e < DV / 8; ++e)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) s[0][j][x] += s[MAPS - 1][j][x];
+                          for (int x = 0; x < 4; ++x) acc[u * (DV / 8) + e][x] *= old[u][x >> 1];
                     }
-                    uint32_t p[2][4];
-                    pack_a<4>(s[0], p);
-                    contract_rows<DV, DV, 2>(p, vt, 0, acc);
                   }
+                  // the maps of differential attention are rounded each on its own and subtracted as
+                  // fp32 outputs: subtracting first would need both normalisers first, that is every
+                  // score and exponential twice
+                  uint32_t p[2 * MAPS][4];
+#pragma unroll
+                  for (int u = 0; u < MAPS; ++u) pack_a<4>(s[u], p + 2 * u);
+                  contract_rows<DV, DV, 2, MAPS>(p, vt, 0, acc);
                 }
-              }
-            }
-            if constexpr (PASSES == 2) {
-              if (pass == 0 && k0 + chunk >= hi) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                  for (int i = 0; i < 2; ++i) l[u][i] = safe_inv(quad_sum(l[u][i]));
               }
             }
           }
@@ -690,6 +671,17 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
             if (a.lse && t4 == 0 && g + 8 * i < nr)
               a.lse[(size_t)__ldg(&a.rows[first + g + 8 * i].x) * a.hq + h] =
                   l[0][i] == 0.f ? kNegInf : (m[0][i] + log2f(l[0][i])) * kLn2;
+          }
+        }
+        if constexpr (MAPS == 2) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float f0 = safe_inv(quad_sum(l[0][i])), f1 = lam * safe_inv(quad_sum(l[MAPS - 1][i]));
+#pragma unroll
+            for (int e = 0; e < DV / 8; ++e)
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+                acc[e][2 * i + x] = acc[e][2 * i + x] * f0 - acc[(MAPS - 1) * (DV / 8) + e][2 * i + x] * f1;
           }
         }
         store_acc<D, DV>(scratch, acc, f[0], f[1], static_cast<bf16*>(a.out), a.hq, MAPS * h, a.rows, first, nr);
