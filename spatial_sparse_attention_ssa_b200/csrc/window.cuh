@@ -40,6 +40,9 @@ constexpr float kPosInf = __builtin_inff();
 
 // The maximum to subtract: 0 for a row with nothing left (every score minus infinity).
 __device__ __forceinline__ float safe_max(float m) { return m == kNegInf ? 0.f : m; }
+// The factor of sums taken against `old` when `now` (finite) is subtracted instead; 1 while nothing
+// was summed (2^-now could be infinite, and its product with an empty sum NaN).
+__device__ __forceinline__ float rescale(float old, float now) { return old == kNegInf ? 1.f : ex2(old - now); }
 // 1 / sum, 0 for a row with nothing left; a NaN sum stays NaN.
 __device__ __forceinline__ float safe_inv(float l) { return l == 0.f ? 0.f : 1.f / l; }
 __device__ __forceinline__ float lse2_of(float m, float l) { return l == 0.f ? kPosInf : m + log2f(l); }

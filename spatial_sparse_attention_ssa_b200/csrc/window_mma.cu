@@ -77,10 +77,6 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void sts16(uint32_t dst, uint4 v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
 __device__ __forceinline__ uint4 lds16(uint32_t src) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -105,27 +101,24 @@ __device__ __forceinline__ uint32_t unit(int row, int c) {
   return 16u * (uint32_t)(row * U + (c ^ f));
 }
 
-// Rows first + y .. first + y + ROWS - 1 of the cell order to a staged tile, zeros from first + n on,
-// by THREADS threads; one or two tensors of the same heads at once.  Row y + k goes to position
-// at(y + k).  `seen(position, row, entry, unit)` is called for every unit.  Unrolled: a unit costs its
+// Rows first .. first + n - 1 (n <= ROWS) of the cell order to a staged tile of ROWS rows, zeros past
+// n, by THREADS threads; one or two tensors of the same heads at once.  Unrolled: a unit costs its
 // copy, its address and little else.
-template <int D, int W, int ROWS, int THREADS, bool TWO, typename At, typename Seen>
+template <int D, int W, int ROWS, int THREADS, bool TWO>
 __device__ __forceinline__ void stage(uint32_t dst, const Rows& src, uint32_t dst2, const Rows& src2,
-                                      const int2* __restrict__ rows, int first, int n, int tid, int y, At at,
-                                      Seen seen) {
+                                      const int2* __restrict__ rows, int first, int n, int tid) {
   constexpr int U = W / 8, STEP = THREADS / U, IT = ROWS / STEP;
   static_assert(ROWS % STEP == 0, "whole steps");
   const int r = tid / U, c = tid % U;
-  int2 e[IT];
+  int tok[IT];
 #pragma unroll
-  for (int i = 0; i < IT; ++i) e[i] = __ldg(&rows[first + min(y + i * STEP + r, n - 1)]);
+  for (int i = 0; i < IT; ++i) tok[i] = __ldg(&rows[first + min(i * STEP + r, n - 1)].x);
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
-    const int k = y + i * STEP + r, p = at(k);
-    const size_t at_row = ((size_t)e[i].x * src.heads + src.head) * D + 8 * c;
-    cp16(dst + unit<W>(p, c), static_cast<const bf16*>(src.p) + at_row, k < n);
-    if constexpr (TWO) cp16(dst2 + unit<W>(p, c), static_cast<const bf16*>(src2.p) + at_row, k < n);
-    seen(p, first + min(k, n - 1), e[i], c);
+    const int k = i * STEP + r;
+    const size_t at = ((size_t)tok[i] * src.heads + src.head) * D + 8 * c;
+    cp16(dst + unit<W>(k, c), static_cast<const bf16*>(src.p) + at, k < n);
+    if constexpr (TWO) cp16(dst2 + unit<W>(k, c), static_cast<const bf16*>(src2.p) + at, k < n);
   }
 }
 
@@ -224,10 +217,11 @@ __device__ __forceinline__ float quad_sum(float x) {
 // The bias gradient in fixed point.  A CTA keeps two whole numbers per offset: dS 2^s rounded, and
 // what that rounding left times 2^k, rounded; both are added by native integer atomics in shared
 // memory, whose order cannot change the sums.  Bounds: the |dS| of a row sum to at most 2 M, M the
-// largest |dP| of the head (window statistics, a.amax), so 2^s <= 2^30 / (2 M rows) keeps the first;
-// each remainder is at most 1/2, so 2^k <= 2^31 / (adds per offset) keeps the second, adds = rows times
-// the most tokens that one voxel holds (a.tiles[T].x).  With 2^13 rows the unit is M 2^-34: the table
-// is as exact as fp32 sums.  A NaN or an infinity in dP or in a softmax makes the head's gradient NaN.
+// largest |dP| of the head (from the row statistics, a.amax), so 2^s <= 2^29 / (2 M rows) keeps the
+// first (a rounding at most doubles a number that it does not make 0); each remainder is at most 1/2,
+// so 2^k <= 2^30 / (adds per offset) keeps the second, adds = rows times the most tokens that one voxel
+// holds (a.tiles[T].x).  With 2^13 rows the unit is M 2^-33: the table is as exact as fp32 sums.  A NaN
+// or an infinity in dP or in a softmax makes the head's gradient NaN.
 struct Limbs {
   float s, k, unit;  // 2^s, 2^k, 2^-s
   int kbits;
@@ -238,7 +232,7 @@ struct Limbs {
     const int64_t rows = min((int64_t)a.N, slots * (item_size * kTile)), adds = rows * max(1, __ldg(&a.tiles[a.T].x));
     const int rb = 64 - __clzll(rows), ab = 64 - __clzll(adds);  // rows < 2^rb, adds < 2^ab
     const int e = (int)(bits >> 23) - 126;                       // M < 2^e
-    int sb = min(30 - rb - 1 - e, 20 - e);                       // |dS 2^s| < 2^22: see add()
+    int sb = min(29 - rb - 1 - e, 20 - e);                       // |dS 2^s| < 2^22: see add()
     sb = max(-100, min(100, sb));
     kbits = max(0, min(18, 30 - ab));
     s = __uint_as_float(bits >= 0x7f800000u ? 0x7fc00000u : (uint32_t)(sb + 127) << 23);
@@ -259,7 +253,7 @@ struct Limbs {
   }
 };
 
-// Edges whose two tables do not fit beside a team keep one 64-bit number per offset in global
+// Edges whose two tables do not fit beside the ring keep one 64-bit number per offset in global
 // memory: dS 2^s with 2^s <= 2^61 / (2 M N).
 __host__ __device__ inline int wide_bits(uint32_t amax, int64_t N) {
   int rb = 0;
@@ -299,7 +293,6 @@ __device__ __forceinline__ void add_bias_grad(const F& add, float (*ds)[4], cons
 // (The map is its own inverse.)
 __device__ __forceinline__ int key_at(int p) { return (p & 33) | (p & 6) << 2 | (p & 24) >> 2; }
 
-
 // s = s mul + bias in units of log2 for the 32 positions of a half chunk, minus infinity where
 // the key is not below `left`.  t0, t8: the head's table of offsets at the codes of rows g, g + 8
 // (plus the center); codes: of the positions (shared memory).
@@ -325,7 +318,6 @@ __device__ __forceinline__ void finish_scores(float (*s)[4], const int* codes, i
   }
 }
 
-
 // Number of tiles of the item (up to `size` row tiles of a cell, which take the cell's keys from one
 // passage of the ring) that starts at a slot: 0 for empty slots and those inside an item.
 __device__ __forceinline__ int item_tiles(const int4& tile, int size) {
@@ -347,6 +339,10 @@ struct Shape {
   static constexpr int scratch = kTile * row;
   static constexpr int warp = MODE == kForward ? scratch : 2 * scratch;
   static constexpr int items = 256;  // of a batch
+  // Working warps of a CTA at most, beside the two that fill the ring; one CTA per SM, so that all
+  // stages are one ring.  As many as leave a thread the registers that its fragments need: spills
+  // cost more than warps gain (dq of rows of 128, 131072 tokens, differential: ten warps with 168
+  // registers 1.68 ms, six with 255 1.04 ms; dq of rows of 64: fourteen with 128 1.69 ms, ten 1.40 ms).
   static constexpr int warps = DV == 128 && MODE != kStats ? 6 : DV == 128 || MODE == kDq || MAPS == 2 ? 10 : 14;
 };
 constexpr int kStages = 8;  // of the ring at most
@@ -357,7 +353,8 @@ constexpr int kStages = 8;  // of the ring at most
 // chunk: keys of a stage; pairs: heads of the CTA (1, or 2 that share a key head), whose tiles are
 // work of their own from the same stages.
 template <int D, int MAPS, int TAB, int MODE>
-__global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) window_rows_kernel(WinArgs a, int NS, int chunk, int pairs) {
+__global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
+    window_rows_kernel(WinArgs a, int NS, int chunk, int pairs) {
   using S = Shape<D, MAPS, MODE>;
   constexpr int DV = S::DV;
   constexpr bool BIAS = TAB != 0;
@@ -408,8 +405,8 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
   }
   uint32_t tops[2] = {0, 0};  // the largest |dP| of a head, as bits: NaN above all
 
-  int rot = 0;                          // the warp that takes the next item's first tile
-  int fs = 0, fphase = warp >= NW;      // stage and phase of the next fill (to make one never waits at first)
+  int rot = 0;                      // the warp that takes the next item's first tile
+  int fs = 0, fphase = warp >= NW;  // stage and phase of the next fill (to make one never waits at first)
   bool ok = true;
   for (int64_t batch = blockIdx.x; batch < a.T && ok; batch += (int64_t)S::items * gridDim.x) {
     // the batch's items, in the order of their slots
@@ -512,8 +509,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
       if (on) {
         __syncwarp();
         const Rows Q = {a.q, a.hq, MAPS * h}, O = {a.dout, a.hq, MAPS * h};
-        stage<D, DV, kTile, 32, MODE != kForward>(scratch, Q, scratch2, O, a.rows, first, nr, lane, 0,
-                                                  [](int k) { return k; }, [](int, int, const int2&, int) {});
+        stage<D, DV, kTile, 32, MODE != kForward>(scratch, Q, scratch2, O, a.rows, first, nr, lane);
         cp_commit();
         if (BIAS) {
           // rows without a token: codes that spread their (zero) shares of the bias gradient
@@ -538,127 +534,123 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1) win
         for (int e = 0; e < NACC; ++e) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
       }
       bool fresh = true;
-      {
 #pragma unroll 1
-        for (int k0 = lo; k0 < hi; k0 += chunk) {
-          const int n = min(chunk, hi - k0);
-          ok = ok && ring_wait(&full[fs], fphase);
-          if (!ok) break;
-          const uint32_t kst = ring + fs * stage_size;
-          const int* codes = reinterpret_cast<const int*>(sm + fs * stage_size + codes_at);
-          uint64_t* done = &empty[fs];
-          if (++fs == NS) fs = 0, fphase ^= 1;
-          if (!on) {  // every warp passes every fill: none falls behind by a turn of the ring
-            if (lane == 0) tc::mbar_arrive(done);
-            continue;
-          }
-          if (fresh) {
-            fresh = false;
-            cp_wait<0>();
-            __syncwarp();
-#pragma unroll
-            for (int d = 0; d < DV / 16; ++d) {
-              load_a<DV>(q[d], scratch, 0, d);
-              if constexpr (MODE != kForward) load_a<DV>(o[d], scratch2, 0, d);
-            }
-          }
-          {
-#pragma unroll 1
-            for (int half = 0; half < n; half += 32) {
-              const uint32_t kt = kst + half * S::row, vt = kt + v_at;
-              const int* hc = codes + half;
-              float s[MAPS][4][4], dp[MODE == kForward ? 1 : 4][4];
-#pragma unroll
-              for (int u = 0; u < MAPS; ++u) {
-                contract_dim<DV, D, 2>(q + u * D / 16, kt, u * D / 8, s[u]);
-                finish_scores<BIAS>(s[u], hc, n - half, mul, t0, t8);
-              }
-              if constexpr (MODE != kForward) contract_dim<DV, DV, 2>(o, vt, 0, dp);
-              if constexpr (MODE == kDq) {
-                // p = 2^(s - lse2), dS = p (dP - D)
-#pragma unroll
-                for (int u = 0; u < MAPS; ++u) {
-#pragma unroll
-                  for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                      const float p = ex2(s[u][j][x] - m[u][x >> 1]);
-                      s[u][j][x] = (u ? -lam * p : p) * (dp[j][x] - dd[u][x >> 1]);
-                    }
-                  if (BIAS) {
-                    if (grad) {
-                      int* to = limbs + pair * 2 * T3;
-                      if constexpr (TAB == 3)
-                        add_bias_grad([&](int at, float x) { wide.add(at, x); }, s[0], hc, ci, ci8);
-                      else
-                        add_bias_grad([&](int at, float x) { fx.add(to + at, to + T3 + at, x); }, s[0], hc, ci, ci8);
-                    }
-                  }
-                  uint32_t f[2][4];
-                  pack_a<4>(s[u], f);
-                  contract_rows<DV, D, 2>(f, kt, u * D / 8, acc + u * D / 8);
-                }
-              } else {
-                // online maximum, sum (and sum of p dP) of a row; the sums stay per lane to the end.
-                // The subtracted maximum follows the true one only once that has grown by a factor of
-                // 2^kSlack, so that sums and products are rarely rescaled
-                float old[MAPS][2];
-#pragma unroll
-                for (int u = 0; u < MAPS; ++u)
-#pragma unroll
-                  for (int i = 0; i < 2; ++i) {
-                    float mx = kNegInf;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(s[u][j][2 * i], s[u][j][2 * i + 1]));
-                    mx = quad_max(mx);
-                    if (!(mx > m[u][i] + kSlack)) mx = m[u][i];
-                    const float ms = safe_max(mx);
-                    old[u][i] = ex2(safe_max(m[u][i]) - ms);
-                    float e = 0.f, ed = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                      for (int x = 0; x < 2; ++x) {
-                        const float p = ex2(s[u][j][2 * i + x] - ms);
-                        s[u][j][2 * i + x] = p;
-                        e += p;
-                        if constexpr (MODE == kStats) {
-                          ed = fmaf(p, dp[j][2 * i + x], ed);
-                          if (u == 0) top = max(top, __float_as_uint(dp[j][2 * i + x]) & 0x7fffffffu);
-                        }
-                      }
-                    l[u][i] = fmaf(l[u][i], old[u][i], e);
-                    if (MODE == kStats) dd[u][i] = fmaf(dd[u][i], old[u][i], ed);
-                    m[u][i] = mx;
-                  }
-                if constexpr (MODE == kForward) {
-                  if (half + k0 > lo) {
-                    bool grown = false;
-#pragma unroll
-                    for (int u = 0; u < MAPS; ++u) grown |= old[u][0] != 1.f || old[u][1] != 1.f;
-                    if (__any_sync(kFull, grown)) {
-#pragma unroll
-                      for (int u = 0; u < MAPS; ++u)
-#pragma unroll
-                        for (int e = 0; e < DV / 8; ++e)
-#pragma unroll
-                          for (int x = 0; x < 4; ++x) acc[u * (DV / 8) + e][x] *= old[u][x >> 1];
-                    }
-                  }
-                  // the maps of differential attention are rounded each on its own and subtracted as
-                  // fp32 outputs: subtracting first would need both normalisers first, that is every
-                  // score and exponential twice
-                  uint32_t p[2 * MAPS][4];
-#pragma unroll
-                  for (int u = 0; u < MAPS; ++u) pack_a<4>(s[u], p + 2 * u);
-                  contract_rows<DV, DV, 2, MAPS>(p, vt, 0, acc);
-                }
-              }
-            }
-          }
-          __syncwarp();
+      for (int k0 = lo; k0 < hi; k0 += chunk) {
+        const int n = min(chunk, hi - k0);
+        ok = ok && ring_wait(&full[fs], fphase);
+        if (!ok) break;
+        const uint32_t kst = ring + fs * stage_size;
+        const int* codes = reinterpret_cast<const int*>(sm + fs * stage_size + codes_at);
+        uint64_t* done = &empty[fs];
+        if (++fs == NS) fs = 0, fphase ^= 1;
+        if (!on) {  // every warp passes every fill: none falls behind by a turn of the ring
           if (lane == 0) tc::mbar_arrive(done);
+          continue;
         }
+        if (fresh) {
+          fresh = false;
+          cp_wait<0>();
+          __syncwarp();
+#pragma unroll
+          for (int d = 0; d < DV / 16; ++d) {
+            load_a<DV>(q[d], scratch, 0, d);
+            if constexpr (MODE != kForward) load_a<DV>(o[d], scratch2, 0, d);
+          }
+        }
+#pragma unroll 1
+        for (int half = 0; half < n; half += 32) {
+          const uint32_t kt = kst + half * S::row, vt = kt + v_at;
+          const int* hc = codes + half;
+          float s[MAPS][4][4], dp[MODE == kForward ? 1 : 4][4];
+#pragma unroll
+          for (int u = 0; u < MAPS; ++u) {
+            contract_dim<DV, D, 2>(q + u * D / 16, kt, u * D / 8, s[u]);
+            finish_scores<BIAS>(s[u], hc, n - half, mul, t0, t8);
+          }
+          if constexpr (MODE != kForward) contract_dim<DV, DV, 2>(o, vt, 0, dp);
+          if constexpr (MODE == kDq) {
+            // p = 2^(s - lse2), dS = p (dP - D)
+#pragma unroll
+            for (int u = 0; u < MAPS; ++u) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  const float p = ex2(s[u][j][x] - m[u][x >> 1]);
+                  s[u][j][x] = (u ? -lam * p : p) * (dp[j][x] - dd[u][x >> 1]);
+                }
+              if (BIAS) {
+                if (grad) {
+                  int* to = limbs + pair * 2 * T3;
+                  if constexpr (TAB == 3)
+                    add_bias_grad([&](int at, float x) { wide.add(at, x); }, s[0], hc, ci, ci8);
+                  else
+                    add_bias_grad([&](int at, float x) { fx.add(to + at, to + T3 + at, x); }, s[0], hc, ci, ci8);
+                }
+              }
+              uint32_t f[2][4];
+              pack_a<4>(s[u], f);
+              contract_rows<DV, D, 2>(f, kt, u * D / 8, acc + u * D / 8);
+            }
+          } else {
+            // online maximum, sum (and sum of p dP) of a row; the sums stay per lane to the end.
+            // The subtracted maximum follows the true one only once that has grown by a factor of
+            // 2^kSlack, so that sums and products are rarely rescaled
+            float old[MAPS][2];
+#pragma unroll
+            for (int u = 0; u < MAPS; ++u)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float mx = kNegInf;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(s[u][j][2 * i], s[u][j][2 * i + 1]));
+                mx = quad_max(mx);
+                if (!(mx > m[u][i] + kSlack)) mx = m[u][i];
+                const float ms = safe_max(mx);
+                old[u][i] = rescale(m[u][i], ms);
+                float e = 0.f, ed = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                  for (int x = 0; x < 2; ++x) {
+                    const float p = ex2(s[u][j][2 * i + x] - ms);
+                    s[u][j][2 * i + x] = p;
+                    e += p;
+                    if constexpr (MODE == kStats) {
+                      ed = fmaf(p, dp[j][2 * i + x], ed);
+                      if (u == 0) top = max(top, __float_as_uint(dp[j][2 * i + x]) & 0x7fffffffu);
+                    }
+                  }
+                l[u][i] = fmaf(l[u][i], old[u][i], e);
+                if (MODE == kStats) dd[u][i] = fmaf(dd[u][i], old[u][i], ed);
+                m[u][i] = mx;
+              }
+            if constexpr (MODE == kForward) {
+              if (half + k0 > lo) {
+                bool grown = false;
+#pragma unroll
+                for (int u = 0; u < MAPS; ++u) grown |= old[u][0] != 1.f || old[u][1] != 1.f;
+                if (__any_sync(kFull, grown)) {
+#pragma unroll
+                  for (int u = 0; u < MAPS; ++u)
+#pragma unroll
+                    for (int e = 0; e < DV / 8; ++e)
+#pragma unroll
+                      for (int x = 0; x < 4; ++x) acc[u * (DV / 8) + e][x] *= old[u][x >> 1];
+                }
+              }
+              // the maps of differential attention are rounded each on its own and subtracted as
+              // fp32 outputs: subtracting first would need both normalisers first, that is every
+              // score and exponential twice
+              uint32_t p[2 * MAPS][4];
+#pragma unroll
+              for (int u = 0; u < MAPS; ++u) pack_a<4>(s[u], p + 2 * u);
+              contract_rows<DV, DV, 2, MAPS>(p, vt, 0, acc);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(done);
       }
       if (!on || !ok) continue;
       if constexpr (MODE == kForward) {
@@ -872,8 +864,7 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
   };
 
   const Rows K = {a.k, a.hkv, MAPS * hk}, V = {a.v, a.hkv, MAPS * hk};
-  stage<D, DV, kChunk, NTH, true>(kt, K, vt, V, a.rows, keys0, nkeys, tid, 0, [](int k) { return k; },
-                                  [](int, int, const int2&, int) {});
+  stage<D, DV, kChunk, NTH, true>(kt, K, vt, V, a.rows, keys0, nkeys, tid);
   load(hk * G, lo, 0);
   const int r0 = kTile * warp, first = keys0 + r0, nr = min(kTile, hi - first);
   const bool on = warp < nt;

@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kThreads) window_fwd_kernel(WinArgs a) {
               float e = 0.f;
 #pragma unroll
               for (int j = 0; j < 4; ++j) e += ex2(s[u][i][j] - ms);
-              l[u][i] = l[u][i] * ex2(safe_max(m[u][i]) - ms) + row_sum(e);
+              l[u][i] = l[u][i] * rescale(m[u][i], ms) + row_sum(e);
               m[u][i] = mx;
             }
         }
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kThreads) window_fwd_kernel(WinArgs a) {
 
 // dq, the row statistics for window_dkv_kernel, and the partial bias gradients.  Each CTA keeps
 // one table of offsets; a row's keys have distinct offsets, so one warp adds a row's dS to it
-// without atomics (cells with two tokens in a voxel: lane by lane), rows in order.
+// without atomics (keys of one voxel take turns), rows in order.
 template <typename E, typename T, int D, int MAPS>
 __global__ void __launch_bounds__(kThreads) window_dq_kernel(WinArgs a) {
   using L = Lay<D, MAPS>;
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(WinArgs a) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float mx = fmaxf(m[u][i], row_max(fmaxf(fmaxf(s[u][i][0], s[u][i][1]), fmaxf(s[u][i][2], s[u][i][3]))));
-              const float ms = safe_max(mx), corr = ex2(safe_max(m[u][i]) - ms);
+              const float ms = safe_max(mx), corr = rescale(m[u][i], ms);
               float e = 0.f, ed = 0.f;
 #pragma unroll
               for (int j = 0; j < 4; ++j) {

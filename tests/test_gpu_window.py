@@ -165,6 +165,8 @@ DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 @pytest.mark.parametrize("hq,hkv,d,m,bias", [
     (1, 1, 32, 4, None), (4, 2, 32, 4, "offset"), (6, 2, 64, 8, "offset"), (16, 1, 64, 5, "log"), (3, 3, 128, 8, "log"),
     (2, 1, 128, 1, "offset"), (2, 2, 32, 16, "offset"), (8, 4, 64, 10, None), (2, 1, 64, 13, "log"), (5, 1, 32, 2, "log"),
+    (4, 2, 64, 12, "offset"), (2, 1, 64, 16, "log"), (2, 1, 128, 12, "offset"), (2, 2, 128, 16, "offset"),
+    (3, 1, 128, 13, "log"), (4, 1, 32, 14, "offset"), (12, 2, 64, 9, "offset"), (64, 64, 32, 3, "log"),
 ])
 def test_window_forward_backward(hq, hkv, d, m, bias, dtype):
     coords, cu = shell(3, 350, seqs=2, r=9)
@@ -192,10 +194,11 @@ def test_cell_larger_than_any_bias_window(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-def test_voxels_that_hold_several_tokens(dtype):
-    coords, cu = shell(8, 200, r=8)
-    coords = np.repeat(coords, 3, 0)
-    pr = Problem(coords, np.array([0, len(coords)], np.int32), 6, 4, 2, 32, DT[dtype], seed=9, bias="offset")
+@pytest.mark.parametrize("n,times,m", [(200, 3, 6), (3, 90, 2), (40, 7, 14)])
+def test_voxels_that_hold_several_tokens(n, times, m, dtype):
+    coords, cu = shell(8, n, r=8)
+    coords = np.repeat(coords, times, 0)
+    pr = Problem(coords, np.array([0, len(coords)], np.int32), m, 4, 2, 32, DT[dtype], seed=9, bias="offset")
     a, b = run_window(pr), run_window(pr)
     check_all(a, pr.ref_window())
     assert all(torch.equal(a[x], b[x]) for x in a)
@@ -229,6 +232,21 @@ def test_barred_buckets(dtype):
     r, ref = run_window(pr), pr.ref_window()
     assert float(r["out"][:, 1].abs().max()) == 0 and bool(torch.isneginf(r["lse"][:, 1]).all())
     assert float(r["dbias"][1].abs().max()) == 0 and float(r["dq"][:, 1].abs().max()) == 0
+    check_all(r, ref)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_scores_far_below_zero_after_a_barred_start(dtype):
+    """A cell whose first keys are barred and whose others have a bias of -300: the sums start at the
+    first key that counts, wherever it stands."""
+    coords, cu = dense(19, 480, 8)
+    pr = Problem(coords, cu, 8, 2, 1, 64, DT[dtype], seed=20, bias="offset")
+    t = pr.bias.table.view(2, 15, 15, 15)
+    t -= 300.0
+    t[0, 3:] = float("-inf")       # queries far along x see no key of their own or earlier layers
+    t[1, :12] = float("-inf")
+    r, ref = run_window(pr), pr.ref_window()
+    assert bool(torch.isfinite(r["out"]).all()) and bool(torch.isfinite(r["dbias"]).all())
     check_all(r, ref)
 
 
