@@ -181,7 +181,13 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     return t.data_ptr()
 
 
+# the current stream's handle without building a Stream object, where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device: torch.device | None = None) -> int:
+    if _raw_stream is not None and device is not None and device.index is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
@@ -582,11 +588,17 @@ def ssa_cross_backward(p: Params, q_cu: torch.Tensor, blk: Bins, q, k, v, gates,
 
 def _on_one_device(*ts: torch.Tensor | None) -> torch.device:
     """The device that all tensors share (contiguous CUDA tensors, as every call wants)."""
-    ts = [t for t in ts if t is not None]
-    _require_cuda(*ts)
-    if any(t.device != ts[0].device for t in ts):
-        raise ValueError("SSA tensors must be on one device")
-    return ts[0].device
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError("SSA tensors must be contiguous CUDA tensors")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("SSA tensors must be on one device")
+    return dev
 
 
 def _call(device: torch.device, name: str, *args) -> None:
@@ -597,11 +609,12 @@ def _call(device: torch.device, name: str, *args) -> None:
     else:
         with torch.cuda.device(device):
             st = fn(*args, _stream(device))
-    _check(st, name)
+    if st != SSA_OK:
+        raise SSAError(st, name)
 
 
 def _want(t: torch.Tensor, shape: tuple, dtype: torch.dtype, name: str) -> None:
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError("%s must be %s %s, got %s %s" % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
 
 
@@ -618,6 +631,14 @@ class WindowPlan:
     def __post_init__(self):
         self._c = WinPlanC(_ptr(self.rows), _ptr(self.tiles), self.n, self.count, self.m)
         self._ref = ctypes.byref(self._c)
+        self._ws = {}  # workspace bytes by call and heads
+
+    def workspace_size(self, op: int, p: "WindowParams") -> int:
+        """Bytes that OP_WINDOW_BACKWARD or OP_DIFF_BACKWARD needs for these heads."""
+        key = (op, p.hq, p.hkv, p.d, p.dtype)
+        if key not in self._ws:
+            self._ws[key] = int(_lib().ssa_window_workspace_size(op, p, self._ref))
+        return self._ws[key]
 
 
 def ssa_window_plan(coords: torch.Tensor | None, win: Bins, m: int = 0) -> WindowPlan:
@@ -727,7 +748,7 @@ def _window_backward(op: int, name: str, p: WindowParams, plan: WindowPlan, extr
     else:
         for g, s in zip(grads, shapes):
             _want(g, s, p._dtype, "grads")
-    need = int(_lib().ssa_window_workspace_size(op, p, plan._ref))
+    need = plan.workspace_size(op, p)
     ws = workspace if workspace is not None and workspace.numel() >= need else _workspace(need, dev)
     _call(dev, name, p, plan._ref, *extra, *ptrs, a8, _ptr(dout), *(_ptr(g) for g in grads), _ptr(last), _ptr(ws),
           ws.numel())
@@ -786,14 +807,15 @@ def ssa_act8_pack(x: torch.Tensor, out: Act8 | None = None) -> Act8:
     if x.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("x must be bfloat16 or float32")
     if out is None:
-        _require_cuda(x)
-        out = Act8(torch.empty(x.shape, dtype=torch.int8, device=x.device),
-                   torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device))
-    _want(out.codes, x.shape, torch.int8, "codes")
-    _want(out.scale, x.shape[:-1], torch.float32, "scale")
-    dev = _on_one_device(x, out.codes, out.scale)
+        dev = _on_one_device(x)
+        out = Act8(torch.empty(x.shape, dtype=torch.int8, device=dev),
+                   torch.empty(x.shape[:-1], dtype=torch.float32, device=dev))
+    else:
+        _want(out.codes, x.shape, torch.int8, "codes")
+        _want(out.scale, x.shape[:-1], torch.float32, "scale")
+        dev = _on_one_device(x, out.codes, out.scale)
     _call(dev, "ssa_act8_pack", DTYPE_BF16 if x.dtype == torch.bfloat16 else DTYPE_F32, out.scale.numel(),
-          int(x.shape[-1]), _ptr(x), _ptr(out.codes), _ptr(out.scale))
+          x.shape[-1], _ptr(x), _ptr(out.codes), _ptr(out.scale))
     return out
 
 
@@ -801,14 +823,16 @@ def ssa_act8_unpack(held: Act8, dtype: torch.dtype, out: torch.Tensor | None = N
     """The values that `held` stands for, in bf16 (exact) or fp32."""
     if dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("dtype must be torch.bfloat16 or torch.float32")
-    if out is None:
-        out = torch.empty(held.codes.shape, dtype=dtype, device=held.codes.device)
-    _want(out, held.codes.shape, dtype, "out")
-    _want(held.codes, out.shape, torch.int8, "codes")
-    _want(held.scale, out.shape[:-1], torch.float32, "scale")
+    shape = held.codes.shape
+    _want(held.codes, shape, torch.int8, "codes")
+    _want(held.scale, shape[:-1], torch.float32, "scale")
+    if out is not None:
+        _want(out, shape, dtype, "out")
     dev = _on_one_device(held.codes, held.scale, out)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
     _call(dev, "ssa_act8_unpack", DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32, held.scale.numel(),
-          int(out.shape[-1]), _ptr(held.codes), _ptr(held.scale), _ptr(out))
+          shape[-1], _ptr(held.codes), _ptr(held.scale), _ptr(out))
     return out
 
 
