@@ -373,7 +373,8 @@ SSA_API ssa_status ssa_sp_backward(const ssa_params* p, int32_t S, int64_t N, co
  * the bias, the difference of maps and the checkpoints have no counterpart on the pages):
  * every token attends the tokens of its own cell (window or block) of any partition that
  * ssa_bin made.  All of them are asynchronous, allocate nothing, find argument errors on
- * the host before anything is enqueued, and give the same bits on every run.
+ * the host before anything is enqueued, and give the same bits on every run.  A tensor of
+ * 64 GB or more (n * hq * d / 8 above 2^32 - 1) is SSA_ERR_UNSUPPORTED.
  */
 
 /* The largest window edge a relative position bias can have ((2*16-1)^3 offsets). */
@@ -456,8 +457,11 @@ SSA_API ssa_status ssa_window_forward(const ssa_window_params* p, const ssa_win_
  * ssa_window_backward -- gradients of sum(dout * out): dq [N, hq, d], dk, dv [N, hkv, d] in
  * dtype (each summed in fp32 and rounded once), dbias fp32 [hq, nb] (NULL: not wanted, or
  * no bias); all written.  It recomputes the probabilities and needs nothing the forward left.
+ *          A NaN or an infinity in the inputs of a head makes all of its dbias NaN in
+ *          SSA_DTYPE_BF16; dq, dk, dv show it in its own cell only.
  *   act8   NULL, or an array of three: Q, K, V from 8-bit checkpoints (q, k, v are then
- *          ignored); the gradients are those at the values the codes hold, in dtype
+ *          ignored); the gradients are those at the values the codes hold, in dtype.  In
+ *          SSA_DTYPE_BF16 the workspace holds them as bf16 during the call
  *   ws     device workspace, 256-byte aligned, ssa_window_workspace_size(SSA_OP_WINDOW_BACKWARD,
  *          p, plan) bytes (SSA_ERR_WORKSPACE if ws_bytes is less)
  */
