@@ -219,22 +219,21 @@ __device__ __forceinline__ float quad_sum(float x) {
 // memory, whose order cannot change the sums.  Bounds: the |dS| of a row sum to at most 2 M, M the
 // largest |dP| of the head (from the row statistics, a.amax), so 2^s <= 2^29 / (2 M rows) keeps the
 // first (a rounding at most doubles a number that it does not make 0); each remainder is at most 1/2,
-// so 2^k <= 2^30 / (adds per offset) keeps the second, adds = rows times the most tokens that one voxel
-// holds (a.tiles[T].x).  With 2^13 rows the unit is M 2^-33: the table is as exact as fp32 sums.  A NaN
-// or an infinity in dP or in a softmax makes the head's gradient NaN.
+// so 2^k <= 2^31 / (adds per offset) keeps the second, adds = rows times the most tokens that one voxel
+// holds (a.tiles[T].x).  The rows of the CTA are counted, not bounded by its slots: at 131072 tokens
+// that is two bits more for each number.  Below 2^12 rows and without shared voxels the unit is at most
+// M 2^-34.  A NaN or an infinity in dP or in a softmax makes the head's gradient NaN.
 struct Limbs {
   float s, k, unit;  // 2^s, 2^k, 2^-s
   int kbits;
-  __device__ __forceinline__ void set(const WinArgs& a, int h, int item_size) {
+  __device__ __forceinline__ void set(const WinArgs& a, int h, int rows) {
     const uint32_t bits = __ldg(a.amax + h);
-    // rows of a CTA: its slots, each of which can start an item
-    const int64_t slots = (a.T + (int64_t)gridDim.x - 1) / gridDim.x;
-    const int64_t rows = min((int64_t)a.N, slots * (item_size * kTile)), adds = rows * max(1, __ldg(&a.tiles[a.T].x));
-    const int rb = 64 - __clzll(rows), ab = 64 - __clzll(adds);  // rows < 2^rb, adds < 2^ab
-    const int e = (int)(bits >> 23) - 126;                       // M < 2^e
-    int sb = min(29 - rb - 1 - e, 20 - e);                       // |dS 2^s| < 2^22: see add()
+    const int64_t adds = (int64_t)rows * max(1, __ldg(&a.tiles[a.T].x));
+    const int rb = 32 - __clz(rows), ab = 64 - __clzll(adds);  // rows < 2^rb, adds < 2^ab
+    const int e = (int)(bits >> 23) - 126;                      // M < 2^e
+    int sb = min(29 - rb - 1 - e, 20 - e);                      // |dS 2^s| < 2^22: see add()
     sb = max(-100, min(100, sb));
-    kbits = max(0, min(18, 30 - ab));
+    kbits = max(0, min(21, 31 - ab));
     s = __uint_as_float(bits >= 0x7f800000u ? 0x7fc00000u : (uint32_t)(sb + 127) << 23);
     k = (float)(1 << kbits);
     unit = 1.f / s;
@@ -360,7 +359,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
   constexpr bool BIAS = TAB != 0;
   extern __shared__ __align__(128) char sm[];
   __shared__ uint64_t full[kStages], empty[kStages];
-  __shared__ int n_items;
+  __shared__ int n_items, n_rows;  // items of the batch; rows of all of the CTA's items
   const int NW = (int)blockDim.x / 32 - 2;  // working warps; two more fill the ring
   const uint32_t v_at = chunk * S::row, codes_at = 2 * v_at, stage_size = chunk * S::token;
   const int h0 = pairs * blockIdx.y, hk = h0 / (a.hq / a.hkv), item_size = NW / pairs;
@@ -390,11 +389,22 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
   Limbs fx;
   Wide wide;
   float s2[2] = {0.f, 0.f};
-  if (grad && TAB != 3)
+  if (grad && TAB != 3) {
+    if (threadIdx.x == 0) n_rows = 0;
+    __syncthreads();
+    int mine = 0;
+    for (int64_t t = blockIdx.x + (int64_t)threadIdx.x * gridDim.x; t < a.T; t += (int64_t)blockDim.x * gridDim.x) {
+      const int4 x = __ldg(&a.tiles[t]);
+      if (item_tiles(x, item_size)) mine += min(item_size * kTile, x.w - x.x);
+    }
+    mine = __reduce_add_sync(kFull, mine);
+    if (lane == 0) atomicAdd(&n_rows, mine);
+    __syncthreads();
     for (int i = pairs - 1; i >= 0; --i) {
-      fx.set(a, h0 + i, item_size);
+      fx.set(a, h0 + i, n_rows);
       (i ? s2[1] : s2[0]) = fx.s;
     }
+  }
   float lams[2] = {0.f, 0.f};
   if constexpr (MAPS == 2) {
     for (int i = 0; i < pairs; ++i) {
@@ -712,7 +722,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
   if (grad && TAB != 3) {
     __syncthreads();
     for (int p = 0; p < pairs; ++p) {
-      fx.set(a, h0 + p, item_size);
+      fx.set(a, h0 + p, n_rows);
       const int* from = limbs + p * 2 * T3;
       float* part = a.part + ((size_t)(h0 + p) * a.parts + blockIdx.x) * T3;
       for (int i = threadIdx.x; i < T3; i += blockDim.x) part[i] = fx.value(from[i], from[T3 + i]);

@@ -279,6 +279,41 @@ def test_what_is_not_finite_stays_in_its_cell(op, bad, dtype):
     assert not bool(torch.isfinite(dirty["dq"][tok]).any()) and not bool(torch.isfinite(dirty["dk"][tok]).any())
 
 
+def test_bias_gradient_of_many_rows_keeps_fp32_precision():
+    """A full cube of 262144 tokens and 32 heads: many rows add to one CTA's table.  Relative error of
+    two heads' dbias in the 2-norm.  Per dS, roundings as random numbers of their largest sizes: ex2
+    2^-22; score, lse2 and their difference, all below 8 in units of log2, 2^-22 ln 2 each; together
+    2^-22 (1 + 2.1), over sqrt 3 for the root mean square: 4.3e-7.  dP is a sum of two tensor core steps
+    that may cut off rather than round: 2 x 2^-23.  Together below 7e-7, which the sums' own unit must
+    not add to.  (A unit that only bounds the rows by the CTA's slots is 8.6e-7 off by itself.)"""
+    side, m, hq, hkv, d = 64, 4, 32, 2, 32
+    n, w = side ** 3, side // m
+    key = np.arange(n)
+    coords = np.stack([key // side ** 2, key // side % side, key % side], 1).astype(np.int32)
+    coords, cu = torch.from_numpy(coords).cuda(), torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    _, win = ssa.ssa_bin(coords, cu, 1024, m, m)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    f = lambda h: torch.randn(n, h, d, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    q, k, v, dout = f(hq), f(hkv), f(hkv), f(hq)
+    table = 0.5 * torch.randn(hq, (2 * m - 1) ** 3, generator=gen, device="cuda")
+    p = ssa.make_window_params(hq, hkv, d, torch.bfloat16)
+    got = ssa.ssa_window_backward(p, ssa.ssa_window_plan(coords, win, m), q, k, v, dout, bias=ssa.WindowBias(table))[3]
+    x = torch.cartesian_prod(*[torch.arange(m, device="cuda")] * 3)
+    x = x[:, None] - x[None] + m - 1
+    off = (x[..., 0] * (2 * m - 1) + x[..., 1]) * (2 * m - 1) + x[..., 2]
+    cells = lambda t, h: (t[:, h].reshape(w, m, w, m, w, m, d).permute(0, 2, 4, 1, 3, 5, 6)  # noqa: E731
+                          .reshape(w ** 3, m ** 3, d).double())
+    for h in (0, 29):
+        g = h // (hq // hkv)
+        s = cells(q, h) @ cells(k, g).transpose(1, 2) / np.sqrt(d) + table[h].double()[off]
+        s = torch.softmax(s, -1)
+        dp = cells(dout, h) @ cells(v, g).transpose(1, 2)
+        ds = s * (dp - (s * dp).sum(-1, keepdim=True))
+        ref = torch.zeros((2 * m - 1) ** 3, dtype=torch.float64, device="cuda")
+        ref.index_add_(0, off.reshape(-1), ds.sum(0).reshape(-1))
+        assert float((got[h].double() - ref).norm() / ref.norm()) < 7e-7
+
+
 def test_bias_and_values_move_the_output_as_the_gradient_says():
     """The gradients against differences of the operator itself (fp32): one direction each."""
     coords, cu = shell(17, 300, r=9)
