@@ -29,6 +29,14 @@ __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, ui
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// the same onto zeros
+__device__ __forceinline__ void mma0(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 // four 8x8 b16 matrices; lane l gives the address of row l % 8 of matrix l / 8
 __device__ __forceinline__ void ldsm(uint32_t* r, uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -130,21 +138,37 @@ __device__ __forceinline__ void load_a(uint32_t* f, uint32_t tile, int r0, int k
 }
 
 // s[2 k], s[2 k + 1] = A B^T for the 16 rows 16 k .. of B, k < NK: W columns from unit u0 of a
-// staged tile of PW columns.
+// staged tile of PW columns; A as fragments, or (below) W columns from unit a0 of a staged tile of
+// 16 rows, read for the occasion.
 template <int PW, int W, int NK>
-__device__ __forceinline__ void contract_dim(const uint32_t (*a)[4], uint32_t tile, int u0, float (*s)[4]) {
+__device__ __forceinline__ void contract_step(const uint32_t* a, int d, uint32_t tile, int u0, float (*s)[4]) {
   const int lane = threadIdx.x & 31, row = (lane & 7) + ((lane >> 4) << 3), c = (lane >> 3) & 1;
 #pragma unroll
   for (int k = 0; k < NK; ++k) {
-#pragma unroll
-    for (int x = 0; x < 4; ++x) s[2 * k][x] = s[2 * k + 1][x] = 0.f;
-#pragma unroll
-    for (int d = 0; d < W / 16; ++d) {
-      uint32_t b[4];
-      ldsm(b, tile + unit<PW>(16 * k + row, u0 + 2 * d + c));
-      mma(s[2 * k], a[d], b[0], b[1]);
-      mma(s[2 * k + 1], a[d], b[2], b[3]);
+    uint32_t b[4];
+    ldsm(b, tile + unit<PW>(16 * k + row, u0 + 2 * d + c));
+    if (d == 0) {
+      mma0(s[2 * k], a, b[0], b[1]);
+      mma0(s[2 * k + 1], a, b[2], b[3]);
+    } else {
+      mma(s[2 * k], a, b[0], b[1]);
+      mma(s[2 * k + 1], a, b[2], b[3]);
     }
+  }
+}
+template <int PW, int W, int NK>
+__device__ __forceinline__ void contract_dim(const uint32_t (*a)[4], uint32_t tile, int u0, float (*s)[4]) {
+#pragma unroll
+  for (int d = 0; d < W / 16; ++d) contract_step<PW, W, NK>(a[d], d, tile, u0, s);
+}
+template <int PW, int W, int NK>
+__device__ __forceinline__ void contract_dim(uint32_t atile, int a0, uint32_t tile, int u0, float (*s)[4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 0; d < W / 16; ++d) {
+    uint32_t a[4];
+    ldsm(a, atile + unit<PW>(lane & 15, a0 + 2 * d + (lane >> 4)));
+    contract_step<PW, W, NK>(a, d, tile, u0, s);
   }
 }
 
@@ -342,7 +366,12 @@ struct Shape {
   // stages are one ring.  As many as leave a thread the registers that its fragments need: spills
   // cost more than warps gain (dq of rows of 128, 131072 tokens, differential: ten warps with 168
   // registers 1.68 ms, six with 255 1.04 ms; dq of rows of 64: fourteen with 128 1.69 ms, ten 1.40 ms).
-  static constexpr int warps = DV == 128 && MODE != kStats ? 6 : DV == 128 || MODE == kDq || MAPS == 2 ? 10 : 14;
+  static constexpr int warps = DV == 128 ? (MODE == kDq || (MODE == kForward && MAPS == 2) ? 6 : 10)
+                                         : MODE == kDq || MAPS == 2 ? 10 : 14;
+  // Q and dO stay in registers as fragments, or are read again from the scratch tiles for every step
+  // where that leaves registers for more warps (forward of rows of 128: six warps 452 us, ten 404 us;
+  // differential, both maps' sums: 1259 -> 1112 us; its statistics 787 -> 704 us)
+  static constexpr bool held = MODE == kDq || (MODE == kStats && MAPS == 1);
 };
 constexpr int kStages = 8;  // of the ring at most
 
@@ -513,7 +542,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
       }
       constexpr int NACC = MODE == kStats ? 1 : MODE == kForward ? MAPS * DV / 8 : DV / 8;
       float m[MAPS][2], l[MAPS][2], dd[MAPS][2], acc[NACC][4];
-      uint32_t q[DV / 16][4], o[MODE == kForward ? 1 : DV / 16][4];
+      uint32_t q[S::held ? DV / 16 : 1][4], o[S::held ? DV / 16 : 1][4];
       const float *t0 = tab, *t8 = tab;
       int ci = 0, ci8 = 0;
       if (on) {
@@ -561,10 +590,12 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
           fresh = false;
           cp_wait<0>();
           __syncwarp();
+          if constexpr (S::held) {
 #pragma unroll
-          for (int d = 0; d < DV / 16; ++d) {
-            load_a<DV>(q[d], scratch, 0, d);
-            if constexpr (MODE != kForward) load_a<DV>(o[d], scratch2, 0, d);
+            for (int d = 0; d < DV / 16; ++d) {
+              load_a<DV>(q[d], scratch, 0, d);
+              load_a<DV>(o[d], scratch2, 0, d);
+            }
           }
         }
 #pragma unroll 1
@@ -574,10 +605,18 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
           float s[MAPS][4][4], dp[MODE == kForward ? 1 : 4][4];
 #pragma unroll
           for (int u = 0; u < MAPS; ++u) {
-            contract_dim<DV, D, 2>(q + u * D / 16, kt, u * D / 8, s[u]);
+            if constexpr (S::held)
+              contract_dim<DV, D, 2>(q + u * D / 16, kt, u * D / 8, s[u]);
+            else
+              contract_dim<DV, D, 2>(scratch, u * D / 8, kt, u * D / 8, s[u]);
             finish_scores<BIAS>(s[u], hc, n - half, mul, t0, t8);
           }
-          if constexpr (MODE != kForward) contract_dim<DV, DV, 2>(o, vt, 0, dp);
+          if constexpr (MODE != kForward) {
+            if constexpr (S::held)
+              contract_dim<DV, DV, 2>(o, vt, 0, dp);
+            else
+              contract_dim<DV, DV, 2>(scratch2, 0, vt, 0, dp);
+          }
           if constexpr (MODE == kDq) {
             // p = 2^(s - lse2), dS = p (dP - D)
 #pragma unroll
@@ -605,19 +644,45 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
           } else {
             // online maximum, sum (and sum of p dP) of a row; the sums stay per lane to the end.
             // The subtracted maximum follows the true one only once that has grown by a factor of
-            // 2^kSlack, so that sums and products are rarely rescaled
-            float old[MAPS][2];
+            // 2^kSlack; until then a step asks no neighbour for its maximum and rescales nothing
+            bool grown = false;
+            float mx[MAPS][2];
 #pragma unroll
             for (int u = 0; u < MAPS; ++u)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                float mx = kNegInf;
+                mx[u][i] = kNegInf;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(s[u][j][2 * i], s[u][j][2 * i + 1]));
-                mx = quad_max(mx);
-                if (!(mx > m[u][i] + kSlack)) mx = m[u][i];
-                const float ms = safe_max(mx);
-                old[u][i] = rescale(m[u][i], ms);
+                for (int j = 0; j < 4; ++j) mx[u][i] = fmaxf(mx[u][i], fmaxf(s[u][j][2 * i], s[u][j][2 * i + 1]));
+                grown |= mx[u][i] > m[u][i] + kSlack;
+              }
+            if (__any_sync(kFull, grown)) {
+#pragma unroll
+              for (int u = 0; u < MAPS; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  float to = quad_max(mx[u][i]);
+                  if (!(to > m[u][i] + kSlack)) to = m[u][i];
+                  const float old = rescale(m[u][i], safe_max(to));
+                  m[u][i] = to;
+                  l[u][i] *= old;
+                  if constexpr (MODE == kStats) dd[u][i] *= old;
+                  if constexpr (MODE == kForward) {
+                    if (half + k0 > lo) {
+#pragma unroll
+                      for (int e = 0; e < DV / 8; ++e) {
+                        acc[u * (DV / 8) + e][2 * i] *= old;
+                        acc[u * (DV / 8) + e][2 * i + 1] *= old;
+                      }
+                    }
+                  }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < MAPS; ++u)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float ms = safe_max(m[u][i]);
                 float e = 0.f, ed = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -631,24 +696,10 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
                       if (u == 0) top = max(top, __float_as_uint(dp[j][2 * i + x]) & 0x7fffffffu);
                     }
                   }
-                l[u][i] = fmaf(l[u][i], old[u][i], e);
-                if (MODE == kStats) dd[u][i] = fmaf(dd[u][i], old[u][i], ed);
-                m[u][i] = mx;
+                l[u][i] += e;
+                if constexpr (MODE == kStats) dd[u][i] += ed;
               }
             if constexpr (MODE == kForward) {
-              if (half + k0 > lo) {
-                bool grown = false;
-#pragma unroll
-                for (int u = 0; u < MAPS; ++u) grown |= old[u][0] != 1.f || old[u][1] != 1.f;
-                if (__any_sync(kFull, grown)) {
-#pragma unroll
-                  for (int u = 0; u < MAPS; ++u)
-#pragma unroll
-                    for (int e = 0; e < DV / 8; ++e)
-#pragma unroll
-                      for (int x = 0; x < 4; ++x) acc[u * (DV / 8) + e][x] *= old[u][x >> 1];
-                }
-              }
               // the maps of differential attention are rounded each on its own and subtracted as
               // fp32 outputs: subtracting first would need both normalisers first, that is every
               // score and exponential twice
