@@ -109,6 +109,16 @@ __device__ __forceinline__ uint32_t unit(int row, int c) {
   return 16u * (uint32_t)(row * U + (c ^ f));
 }
 
+// Address of unit e + c (e even, c 0 or 1) of a row of a staged tile: units that differ in e differ by
+// an exclusive or, one instruction for the place of the first (tiles lie on multiples of 128 bytes,
+// so up to eight units to a row its bits are those of the unit alone).
+template <int W, bool XOR = true>
+__device__ __forceinline__ uint32_t unit_pair(uint32_t tile, int row, int c, int e) {
+  if (!XOR) return tile + unit<W>(row, e + c);
+  const uint32_t first = unit<W>(row, c);
+  return W <= 64 ? (tile + first) ^ (16u * e) : tile + (first ^ (16u * e));
+}
+
 // Rows first .. first + n - 1 (n <= ROWS) of the cell order to a staged tile of ROWS rows, zeros past
 // n, by THREADS threads; one or two tensors of the same heads at once.  Unrolled: a unit costs its
 // copy, its address and little else.
@@ -131,22 +141,22 @@ __device__ __forceinline__ void stage(uint32_t dst, const Rows& src, uint32_t ds
 }
 
 // A operand, k-step k, from a tile of 16 rows starting at row r0 of a staged tile.
-template <int W>
+template <int W, bool XOR = true>
 __device__ __forceinline__ void load_a(uint32_t* f, uint32_t tile, int r0, int k) {
   const int lane = threadIdx.x & 31;
-  ldsm(f, tile + unit<W>(r0 + (lane & 15), 2 * k + (lane >> 4)));
+  ldsm(f, unit_pair<W, XOR>(tile + r0 * W * 2, lane & 15, lane >> 4, 2 * k));
 }
 
 // s[2 k], s[2 k + 1] = A B^T for the 16 rows 16 k .. of B, k < NK: W columns from unit u0 of a
 // staged tile of PW columns; A as fragments, or (below) W columns from unit a0 of a staged tile of
 // 16 rows, read for the occasion.
-template <int PW, int W, int NK>
+template <int PW, int W, int NK, bool XOR = true>
 __device__ __forceinline__ void contract_step(const uint32_t* a, int d, uint32_t tile, int u0, float (*s)[4]) {
   const int lane = threadIdx.x & 31, row = (lane & 7) + ((lane >> 4) << 3), c = (lane >> 3) & 1;
 #pragma unroll
   for (int k = 0; k < NK; ++k) {
     uint32_t b[4];
-    ldsm(b, tile + unit<PW>(16 * k + row, u0 + 2 * d + c));
+    ldsm(b, unit_pair<PW, XOR>(tile, row, c, u0 + 2 * d) + k * 32 * PW);
     if (d == 0) {
       mma0(s[2 * k], a, b[0], b[1]);
       mma0(s[2 * k + 1], a, b[2], b[3]);
@@ -156,10 +166,10 @@ __device__ __forceinline__ void contract_step(const uint32_t* a, int d, uint32_t
     }
   }
 }
-template <int PW, int W, int NK>
+template <int PW, int W, int NK, bool XOR = true>
 __device__ __forceinline__ void contract_dim(const uint32_t (*a)[4], uint32_t tile, int u0, float (*s)[4]) {
 #pragma unroll
-  for (int d = 0; d < W / 16; ++d) contract_step<PW, W, NK>(a[d], d, tile, u0, s);
+  for (int d = 0; d < W / 16; ++d) contract_step<PW, W, NK, XOR>(a[d], d, tile, u0, s);
 }
 template <int PW, int W, int NK>
 __device__ __forceinline__ void contract_dim(uint32_t atile, int a0, uint32_t tile, int u0, float (*s)[4]) {
@@ -167,13 +177,13 @@ __device__ __forceinline__ void contract_dim(uint32_t atile, int a0, uint32_t ti
 #pragma unroll
   for (int d = 0; d < W / 16; ++d) {
     uint32_t a[4];
-    ldsm(a, atile + unit<PW>(lane & 15, a0 + 2 * d + (lane >> 4)));
+    ldsm(a, unit_pair<PW>(atile, lane & 15, lane >> 4, a0 + 2 * d));
     contract_step<PW, W, NK>(a, d, tile, u0, s);
   }
 }
 
 // acc_h += P_h B for h < NA, P_h as A fragments over NK groups of 16 rows of B (as above).
-template <int PW, int W, int NK, int NA = 1>
+template <int PW, int W, int NK, int NA = 1, bool XOR = true>
 __device__ __forceinline__ void contract_rows(const uint32_t (*p)[4], uint32_t tile, int u0, float (*acc)[4]) {
   const int lane = threadIdx.x & 31, row = lane & 15, c = lane >> 4;
 #pragma unroll
@@ -181,7 +191,7 @@ __device__ __forceinline__ void contract_rows(const uint32_t (*p)[4], uint32_t t
 #pragma unroll
     for (int e = 0; e < W / 16; ++e) {
       uint32_t b[4];
-      ldsm_t(b, tile + unit<PW>(16 * k + row, u0 + 2 * e + c));
+      ldsm_t(b, unit_pair<PW, XOR>(tile, row, c, u0 + 2 * e) + k * 32 * PW);
 #pragma unroll
       for (int h = 0; h < NA; ++h) {
         mma(acc[h * (W / 8) + 2 * e], p[h * NK + k], b[0], b[1]);
@@ -238,6 +248,26 @@ __device__ __forceinline__ float quad_sum(float x) {
   return x + __shfl_xor_sync(kFull, x, 2);
 }
 
+// A place in a head's table of offsets, in shared or in global memory; its neighbours by bytes.  The
+// codes of a stage are held times four, so that a lookup costs one subtraction and the load.
+template <bool SHARED>
+struct Place {
+  uint32_t p;
+  __device__ __forceinline__ float at(int off) const {
+    float v;
+    asm("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(p + off));
+    return v;
+  }
+};
+template <>
+struct Place<false> {
+  const char* p;
+  __device__ __forceinline__ float at(int off) const { return __ldg(reinterpret_cast<const float*>(p + off)); }
+};
+__device__ __forceinline__ void red_shared(uint32_t at, int x) {
+  asm volatile("red.shared.add.u32 [%0], %1;" ::"r"(at), "r"(x));
+}
+
 // The bias gradient in fixed point.  A CTA keeps two whole numbers per offset: dS 2^s rounded, and
 // what that rounding left times 2^k, rounded; both are added by native integer atomics in shared
 // memory, whose order cannot change the sums.  Bounds: the |dS| of a row sum to at most 2 M, M the
@@ -266,13 +296,13 @@ struct Limbs {
     return (float)(((double)hi + (double)lo / (double)(1 << kbits)) * (double)unit);
   }
   // x 2^s to the nearest whole number by adding 1.5 2^23 (|x 2^s| < 2^22), and the rest
-  __device__ __forceinline__ void add(int* hi, int* lo, float x) const {
+  __device__ __forceinline__ void add(uint32_t hi, uint32_t lo, float x) const {
     constexpr float kMagic = 12582912.f;
     const float a = fmaf(x, s, kMagic);
     const float r = fmaf(x, s, kMagic - a);
     const float b = fmaf(r, k, kMagic);
-    atomicAdd(hi, __float_as_int(a) - __float_as_int(kMagic));
-    atomicAdd(lo, __float_as_int(b) - __float_as_int(kMagic));
+    red_shared(hi, __float_as_int(a) - __float_as_int(kMagic));
+    red_shared(lo, __float_as_int(b) - __float_as_int(kMagic));
   }
 };
 
@@ -285,18 +315,18 @@ __host__ __device__ inline int wide_bits(uint32_t amax, int64_t N) {
   return sb < -100 ? -100 : sb > 100 ? 100 : sb;
 }
 struct Wide {
-  unsigned long long* sums;  // of the head
+  char* sums;  // of the head
   double s;
   __device__ __forceinline__ void set(const WinArgs& a, int h) {
-    sums = a.sums + (size_t)h * offsets(a.m);
+    sums = reinterpret_cast<char*>(a.sums + (size_t)h * offsets(a.m));
     s = (double)__uint_as_float((uint32_t)(wide_bits(__ldg(a.amax + h), a.N) + 127) << 23);
   }
-  __device__ __forceinline__ void add(int at, float x) const {
-    atomicAdd(sums + at, (unsigned long long)__double2ll_rn((double)x * s));
+  __device__ __forceinline__ void add(int at, float x) const {  // at: four times the offset
+    atomicAdd(reinterpret_cast<unsigned long long*>(sums + 2 * (int64_t)at), (unsigned long long)__double2ll_rn((double)x * s));
   }
 };
 
-// add(code of row - code of key, dS) for a fragment tile of 16 rows and 32 positions.  Rows and
+// add(4 (code of row - code of key), dS) for a fragment tile of 16 rows and 32 positions.  Rows and
 // positions without a token have dS 0 and the codes of others.
 template <typename F>
 __device__ __forceinline__ void add_bias_grad(const F& add, float (*ds)[4], const int* codes, int ci, int ci8) {
@@ -318,17 +348,17 @@ __device__ __forceinline__ int key_at(int p) { return (p & 33) | (p & 6) << 2 | 
 
 // s = s mul + bias in units of log2 for the 32 positions of a half chunk, minus infinity where
 // the key is not below `left`.  t0, t8: the head's table of offsets at the codes of rows g, g + 8
-// (plus the center); codes: of the positions (shared memory).
-template <bool BIAS>
-__device__ __forceinline__ void finish_scores(float (*s)[4], const int* codes, int left, float mul, const float* t0,
-                                              const float* t8) {
+// (plus the center); codes: four times those of the positions (shared memory).
+template <bool BIAS, typename P>
+__device__ __forceinline__ void finish_scores(float (*s)[4], const int* codes, int left, float mul, const P& t0,
+                                              const P& t8) {
   const int t = threadIdx.x & 3;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     float b[4] = {0.f, 0.f, 0.f, 0.f};
     if constexpr (BIAS) {
       const int2 cj = *reinterpret_cast<const int2*>(codes + 8 * j + 2 * t);
-      b[0] = t0[-cj.x], b[1] = t0[-cj.y], b[2] = t8[-cj.x], b[3] = t8[-cj.y];
+      b[0] = t0.at(-cj.x), b[1] = t0.at(-cj.y), b[2] = t8.at(-cj.x), b[3] = t8.at(-cj.y);
     }
 #pragma unroll
     for (int x = 0; x < 4; ++x) s[j][x] = fmaf(s[j][x], mul, b[x]);
@@ -398,7 +428,11 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
   int4* items = reinterpret_cast<int4*>(sm + NS * stage_size + NW * S::warp);
   int* limbs = reinterpret_cast<int*>(items + S::items);  // [pairs][2][T3] with a bias gradient, not wide
   float* tab_s = reinterpret_cast<float*>(limbs + (grad && TAB != 3 ? pairs * 2 * T3 : 0));
-  const float* tab = TAB >= 2 ? a.tab2 + (size_t)h0 * table_pitch(a.m) : tab_s;
+  Place<TAB < 2> tab;
+  if constexpr (TAB >= 2)
+    tab.p = reinterpret_cast<const char*>(a.tab2 + (size_t)h0 * table_pitch(a.m));
+  else
+    tab.p = tc::smem_u32(tab_s);
   const int tab_pitch = TAB >= 2 ? table_pitch(a.m) : T3;
   const uint32_t ring = tc::smem_u32(sm);
   const uint32_t scratch = tc::smem_u32(sm + NS * stage_size + warp * S::warp), scratch2 = scratch + S::scratch;
@@ -502,7 +536,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
                 cp16(dst + unit<DV>(key_at(32 * x + y + r), c), src + u, 32 * x + y + r < n);
               }
               if (BIAS && is_k)
-                *reinterpret_cast<int*>(sm + fs * stage_size + codes_at + 4 * key_at(32 * x + lane)) = code[x];
+                *reinterpret_cast<int*>(sm + fs * stage_size + codes_at + 4 * key_at(32 * x + lane)) = 4 * code[x];
               // the item's queries are its keys: bring their rows (and dO's) near
               if (is_k || MODE != kForward) {
                 prefetch(near + qat[x]);
@@ -543,7 +577,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
       constexpr int NACC = MODE == kStats ? 1 : MODE == kForward ? MAPS * DV / 8 : DV / 8;
       float m[MAPS][2], l[MAPS][2], dd[MAPS][2], acc[NACC][4];
       uint32_t q[S::held ? DV / 16 : 1][4], o[S::held ? DV / 16 : 1][4];
-      const float *t0 = tab, *t8 = tab;
+      Place<TAB < 2> t0 = tab, t8 = tab;
       int ci = 0, ci8 = 0;
       if (on) {
         __syncwarp();
@@ -552,10 +586,10 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
         cp_commit();
         if (BIAS) {
           // rows without a token: codes that spread their (zero) shares of the bias gradient
-          ci = c0 + (g < nr ? __ldg(&a.rows[first + g].y) : g * 13 % (c0 + 1));
-          ci8 = c0 + (g + 8 < nr ? __ldg(&a.rows[first + g + 8].y) : (g + 8) * 13 % (c0 + 1));
-          t0 = tab + pair * tab_pitch + ci;
-          t8 = tab + pair * tab_pitch + ci8;
+          ci = 4 * (c0 + (g < nr ? __ldg(&a.rows[first + g].y) : g * 13 % (c0 + 1)));
+          ci8 = 4 * (c0 + (g + 8 < nr ? __ldg(&a.rows[first + g + 8].y) : (g + 8) * 13 % (c0 + 1)));
+          t0.p = tab.p + 4 * pair * tab_pitch + ci;
+          t8.p = tab.p + 4 * pair * tab_pitch + ci8;
         }
 #pragma unroll
         for (int u = 0; u < MAPS; ++u)
@@ -630,11 +664,11 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
                 }
               if (BIAS) {
                 if (grad) {
-                  int* to = limbs + pair * 2 * T3;
+                  const uint32_t to = tc::smem_u32(limbs) + 8 * pair * T3;
                   if constexpr (TAB == 3)
                     add_bias_grad([&](int at, float x) { wide.add(at, x); }, s[0], hc, ci, ci8);
                   else
-                    add_bias_grad([&](int at, float x) { fx.add(to + at, to + T3 + at, x); }, s[0], hc, ci, ci8);
+                    add_bias_grad([&](int at, float x) { fx.add(to + at, to + at + 4 * T3, x); }, s[0], hc, ci, ci8);
                 }
               }
               uint32_t f[2][4];
@@ -865,6 +899,9 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
   using S = DkvShape<D, MAPS>;
   constexpr int DV = S::DV, NTH = 32 * kDkvWarps;
   constexpr bool BIAS = TAB != 0;
+  // unit_pair's exclusive or holds the first unit's place in a register, which rows of 64 and two maps
+  // have not left (rows of 64, 131072 tokens: 928 us without, 1064 with; d = 128, full cube: 576, 567)
+  constexpr bool XOR = DV == 128 && MAPS == 1;
   extern __shared__ __align__(128) char sm[];
   const int G = a.hq / a.hkv, hk = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t4 = lane & 3, warp = tid >> 5;
@@ -893,7 +930,7 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
       for (int i = 0; i < IT; ++i) {
         const int2 e = __ldg(&a.rows[k0 + min(i * STEP + ur, n - 1)]);
         place[i] = (uint32_t)((size_t)e.x * a.hq * (D / 8)) + uc;
-        if (BIAS && uc == 0) codes[i * STEP + ur] = e.y + c0;
+        if (BIAS && uc == 0) codes[i * STEP + ur] = 4 * (e.y + c0);
       }
     }
     const uint32_t q = base + S::Q + st * S::stage;
@@ -948,7 +985,7 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
     __syncthreads();
     if (on) {
 #pragma unroll
-      for (int d = 0; d < DV / 16; ++d) load_a<DV>(kf[d], kt, r0, d), load_a<DV>(vf[d], vt, r0, d);
+      for (int d = 0; d < DV / 16; ++d) load_a<DV, XOR>(kf[d], kt, r0, d), load_a<DV, XOR>(vf[d], vt, r0, d);
     }
     __syncthreads();
   }
@@ -976,32 +1013,36 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
       const uint32_t qt = base + S::Q + stg * S::stage, ot = qt + S::KT;
       const float* stat = reinterpret_cast<const float*>(sm + S::Q + stg * S::stage + S::stat);
       const int* codes = reinterpret_cast<const int*>(sm + S::codes) + cnow * kChunk;
-      const float* tab = TAB == 2 ? a.tab2 + (size_t)h * T3p
-                                  : reinterpret_cast<const float*>(sm + S::tab) + (h & 1) * T3p;
-      const float *tk = tab - ck, *tk8 = tab - ck8;
+      Place<TAB != 2> tk, tk8;
+      if constexpr (TAB == 2)
+        tk.p = reinterpret_cast<const char*>(a.tab2 + (size_t)h * T3p);
+      else
+        tk.p = base + S::tab + 4 * (h & 1) * T3p;
+      tk8.p = tk.p - 4 * ck8;
+      tk.p -= 4 * ck;
 #pragma unroll 1
       for (int q0 = 0; q0 < n; q0 += 32) {
         // rows q0 .. of the tiles: 32 rows on, the permutation of the units repeats
         const uint32_t qq = qt + q0 * DV * 2, oo = ot + q0 * DV * 2;
         float dp[4][4], pv[4][4];
         if constexpr (S::held) {
-          contract_dim<DV, DV, 2>(vf, oo, 0, dp);
+          contract_dim<DV, DV, 2, XOR>(vf, oo, 0, dp);
         } else {
           uint32_t f[DV / 16][4];
 #pragma unroll
-          for (int d = 0; d < DV / 16; ++d) load_a<DV>(f[d], vt, r0, d);
-          contract_dim<DV, DV, 2>(f, oo, 0, dp);
+          for (int d = 0; d < DV / 16; ++d) load_a<DV, XOR>(f[d], vt, r0, d);
+          contract_dim<DV, DV, 2, XOR>(f, oo, 0, dp);
         }
 #pragma unroll
         for (int u = 0; u < MAPS; ++u) {
           float sc[4][4];
           if constexpr (S::held) {
-            contract_dim<DV, D, 2>(kf + u * D / 16, qq, u * D / 8, sc);
+            contract_dim<DV, D, 2, XOR>(kf + u * D / 16, qq, u * D / 8, sc);
           } else {
             uint32_t f[D / 16][4];
 #pragma unroll
-            for (int d = 0; d < D / 16; ++d) load_a<DV>(f[d], kt, r0, u * D / 16 + d);
-            contract_dim<DV, D, 2>(f, qq, u * D / 8, sc);
+            for (int d = 0; d < D / 16; ++d) load_a<DV, XOR>(f[d], kt, r0, u * D / 16 + d);
+            contract_dim<DV, D, 2, XOR>(f, qq, u * D / 8, sc);
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -1011,7 +1052,7 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
             float b[4] = {0.f, 0.f, 0.f, 0.f};
             if constexpr (BIAS) {
               const int2 cq = *reinterpret_cast<const int2*>(codes + c);
-              b[0] = tk[cq.x], b[1] = tk[cq.y], b[2] = tk8[cq.x], b[3] = tk8[cq.y];
+              b[0] = tk.at(cq.x), b[1] = tk.at(cq.y), b[2] = tk8.at(cq.x), b[3] = tk8.at(cq.y);
             }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -1024,11 +1065,11 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
           }
           uint32_t f[2][4];
           pack_a<4>(sc, f);
-          contract_rows<DV, D, 2>(f, qq, u * D / 8, dk[u]);
+          contract_rows<DV, D, 2, 1, XOR>(f, qq, u * D / 8, dk[u]);
         }
         uint32_t f[2][4];
         pack_a<4>(pv, f);
-        contract_rows<DV, DV, 2>(f, oo, 0, dv);
+        contract_rows<DV, DV, 2, 1, XOR>(f, oo, 0, dv);
       }
     }
     __syncthreads();
