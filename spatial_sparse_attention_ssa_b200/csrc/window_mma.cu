@@ -397,11 +397,11 @@ struct Shape {
   // cost more than warps gain (dq of rows of 128, 131072 tokens, differential: ten warps with 168
   // registers 1.68 ms, six with 255 1.04 ms; dq of rows of 64: fourteen with 128 1.69 ms, ten 1.40 ms).
   static constexpr int warps = DV == 128 ? (MODE == kDq || (MODE == kForward && MAPS == 2) ? 6 : 10)
-                                         : MODE == kDq || MAPS == 2 ? 10 : 14;
+                                         : MAPS == 2 || (MODE == kDq && DV == 64) ? 10 : 14;
   // Q and dO stay in registers as fragments, or are read again from the scratch tiles for every step
   // where that leaves registers for more warps (forward of rows of 128: six warps 452 us, ten 404 us;
   // differential, both maps' sums: 1259 -> 1112 us; its statistics 787 -> 704 us)
-  static constexpr bool held = MODE == kDq || (MODE == kStats && MAPS == 1);
+  static constexpr bool held = (MODE == kDq && DV >= 64) || (MODE == kStats && MAPS == 1);
 };
 constexpr int kStages = 8;  // of the ring at most
 

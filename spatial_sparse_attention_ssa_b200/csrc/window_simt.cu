@@ -45,9 +45,9 @@ __device__ __forceinline__ void fill(float* dst, const void* src, const float* s
   }
 }
 
-// s[i][j] = <A[ty + 8 i], B[tx + 16 j]>
-template <int W>
-__device__ __forceinline__ void dots(const float* A, const float* B, float s[2][4]) {
+// s[i][j] = <A[ty + 8 i], B[tx + 16 j]> for j < NJ, 0 for the others
+template <int W, int NJ>
+__device__ __forceinline__ void dots_of(const float* A, const float* B, float s[2][4]) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -55,21 +55,31 @@ __device__ __forceinline__ void dots(const float* A, const float* B, float s[2][
     for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
 #pragma unroll 4
   for (int c = 0; c < W; c += 4) {
-    float4 a[2], b[4];
+    float4 a[2], b[NJ];
 #pragma unroll
     for (int i = 0; i < 2; ++i) a[i] = *reinterpret_cast<const float4*>(A + (ty + 8 * i) * (W + 4) + c);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * (W + 4) + c);
+    for (int j = 0; j < NJ; ++j) b[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * (W + 4) + c);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < NJ; ++j) {
         s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
         s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
         s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
         s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
       }
   }
+}
+// The rows of a chunk of n that are filled and multiplied: half a chunk, where that holds all (cells
+// of the shells hold some 30 tokens at an edge of 6).
+__device__ __forceinline__ int live(int n) { return n <= kChunk / 2 ? kChunk / 2 : kChunk; }
+template <int W>
+__device__ __forceinline__ void dots(const float* A, const float* B, int n, float s[2][4]) {
+  if (live(n) < kChunk)
+    dots_of<W, 2>(A, B, s);
+  else
+    dots_of<W, 4>(A, B, s);
 }
 
 // Columns of a product that a thread holds: VEC at tx * VEC + 16 * VEC * u, u < NU.
@@ -80,21 +90,25 @@ struct Cols {
   static constexpr int N = VEC * NU;
 };
 
-// acc[i][:] += sum_{j < n} P[ty + 8 i][j] B[j][cols]
+// acc[i][:] += sum_{j < n} P[ty + 8 i][j] B[j][cols], four j at a time: P and B are 0 from n on.
 template <int W>
 __device__ __forceinline__ void accum(const float* P, const float* B, int n, float (*acc)[Cols<W>::N]) {
   constexpr int VEC = Cols<W>::VEC, NU = Cols<W>::NU;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (int j = 0; j < n; ++j) {
-    const float p0 = P[ty * kWStride + j], p1 = P[(ty + 8) * kWStride + j];
+  for (int j = 0; j < n; j += 4) {
+    const float4 p0 = *reinterpret_cast<const float4*>(P + ty * kWStride + j);
+    const float4 p1 = *reinterpret_cast<const float4*>(P + (ty + 8) * kWStride + j);
+    const float q[2][4] = {{p0.x, p0.y, p0.z, p0.w}, {p1.x, p1.y, p1.z, p1.w}};
 #pragma unroll
-    for (int u = 0; u < NU; ++u)
+    for (int y = 0; y < 4; ++y)
 #pragma unroll
-      for (int x = 0; x < VEC; ++x) {
-        const float b = B[j * (W + 4) + tx * VEC + 16 * VEC * u + x];
-        acc[0][u * VEC + x] = fmaf(p0, b, acc[0][u * VEC + x]);
-        acc[1][u * VEC + x] = fmaf(p1, b, acc[1][u * VEC + x]);
-      }
+      for (int u = 0; u < NU; ++u)
+#pragma unroll
+        for (int x = 0; x < VEC; ++x) {
+          const float b = B[(j + y) * (W + 4) + tx * VEC + 16 * VEC * u + x];
+          acc[0][u * VEC + x] = fmaf(q[0][y], b, acc[0][u * VEC + x]);
+          acc[1][u * VEC + x] = fmaf(q[1][y], b, acc[1][u * VEC + x]);
+        }
   }
 }
 
@@ -148,7 +162,7 @@ __device__ __forceinline__ void scores(const WinArgs& a, int h, const float* sm,
                                        float s[2][4]) {
   using L = Lay<D, MAPS>;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  dots<D>(sm + L::A + u * kTile * (D + 4), sm + L::B + u * kChunk * (D + 4), s);
+  dots<D>(sm + L::A + u * kTile * (D + 4), sm + L::B + u * kChunk * (D + 4), n, s);
   const int* codes = reinterpret_cast<const int*>(sm + L::codes);
   const int c0 = a.table ? center(a.m) : 0;
 #pragma unroll
@@ -201,8 +215,8 @@ __global__ void __launch_bounds__(kThreads) window_fwd_kernel(WinArgs a) {
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < MAPS; ++u)
-          fill<E, D, D>(sm + L::B + u * kChunk * (D + 4), a.k, nullptr, a.hkv, MAPS * hk + u, a.rows, k0, n, kChunk);
-        if (pass == 1) fill<E, D, DV>(sm + L::V, a.v, nullptr, a.hkv, MAPS * hk, a.rows, k0, n, kChunk);
+          fill<E, D, D>(sm + L::B + u * kChunk * (D + 4), a.k, nullptr, a.hkv, MAPS * hk + u, a.rows, k0, n, live(n));
+        if (pass == 1) fill<E, D, DV>(sm + L::V, a.v, nullptr, a.hkv, MAPS * hk, a.rows, k0, n, live(n));
         if (threadIdx.x < kChunk) codes[threadIdx.x] = threadIdx.x < n ? a.rows[k0 + threadIdx.x].y : 0;
         __syncthreads();
 #pragma unroll
@@ -293,13 +307,13 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(WinArgs a) {
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < MAPS; ++u)
-          fill<E, D, D>(sm + L::B + u * kChunk * (D + 4), a.k, a.sk, a.hkv, MAPS * hk + u, a.rows, k0, n, kChunk);
-        fill<E, D, DV>(sm + L::V, a.v, a.sv, a.hkv, MAPS * hk, a.rows, k0, n, kChunk);
+          fill<E, D, D>(sm + L::B + u * kChunk * (D + 4), a.k, a.sk, a.hkv, MAPS * hk + u, a.rows, k0, n, live(n));
+        fill<E, D, DV>(sm + L::V, a.v, a.sv, a.hkv, MAPS * hk, a.rows, k0, n, live(n));
         if (threadIdx.x < kChunk) codes[threadIdx.x] = threadIdx.x < n ? a.rows[k0 + threadIdx.x].y : 0;
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < MAPS; ++u) scores<D, MAPS>(a, h, sm, u, n, mul, s[u]);
-        dots<DV>(sm + L::O, sm + L::V, dp);
+        dots<DV>(sm + L::O, sm + L::V, n, dp);
         if (pass == 0 || one) {
 #pragma unroll
           for (int u = 0; u < MAPS; ++u)
@@ -347,16 +361,36 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(WinArgs a) {
             r1 = __popc(__match_any_sync(0xffffffffu, v1 ? k1c : -1 - lane) & below);
             most = __reduce_max_sync(0xffffffffu, max(r0, r1));
           }
-          for (int r = 0; r < nr; ++r) {
-            const int cr = codes[kChunk + r] + c0;
-            const float* ds = sm + L::P + r * kWStride;
-            for (int i = 0; i <= most; ++i) {
-              if (v0 && r0 == i) dtab[cr - k0c] += ds[lane];
+          if (!(tile.y & kDupFlag)) {  // a row's offsets are distinct: its two halves at once, dS read ahead
+            float d0[kTile], d1[kTile];
+#pragma unroll
+            for (int r = 0; r < kTile; ++r) {
+              d0[r] = sm[L::P + r * kWStride + lane];
+              d1[r] = sm[L::P + r * kWStride + 32 + lane];
+            }
+#pragma unroll
+            for (int r = 0; r < kTile; ++r) {
+              if (r >= nr) break;
+              float* at = dtab + codes[kChunk + r] + c0;
+              float x0 = 0.f, x1 = 0.f;
+              if (v0) x0 = at[-k0c];
+              if (v1) x1 = at[-k1c];
+              if (v0) at[-k0c] = x0 + d0[r];
+              if (v1) at[-k1c] = x1 + d1[r];
               __syncwarp();
             }
-            for (int i = 0; i <= most; ++i) {
-              if (v1 && r1 == i) dtab[cr - k1c] += ds[32 + lane];
-              __syncwarp();
+          } else {
+            for (int r = 0; r < nr; ++r) {
+              const int cr = codes[kChunk + r] + c0;
+              const float* ds = sm + L::P + r * kWStride;
+              for (int i = 0; i <= most; ++i) {
+                if (v0 && r0 == i) dtab[cr - k0c] += ds[lane];
+                __syncwarp();
+              }
+              for (int i = 0; i <= most; ++i) {
+                if (v1 && r1 == i) dtab[cr - k1c] += ds[32 + lane];
+                __syncwarp();
+              }
             }
           }
         }
@@ -424,8 +458,8 @@ __global__ void __launch_bounds__(kThreads) window_dkv_kernel(WinArgs a) {
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < MAPS; ++u)
-          fill<E, D, D>(sm + L::B + u * kChunk * (D + 4), a.q, a.sq, a.hq, MAPS * h + u, a.rows, k0, n, kChunk);
-        fill<T, D, DV>(sm + L::V, a.dout, nullptr, a.hq, MAPS * h, a.rows, k0, n, kChunk);
+          fill<E, D, D>(sm + L::B + u * kChunk * (D + 4), a.q, a.sq, a.hq, MAPS * h + u, a.rows, k0, n, live(n));
+        fill<T, D, DV>(sm + L::V, a.dout, nullptr, a.hq, MAPS * h, a.rows, k0, n, live(n));
         if (threadIdx.x < kChunk) {
           codes[threadIdx.x] = threadIdx.x < n ? a.rows[k0 + threadIdx.x].y : 0;
 #pragma unroll
@@ -437,10 +471,10 @@ __global__ void __launch_bounds__(kThreads) window_dkv_kernel(WinArgs a) {
         }
         __syncthreads();
         float s[MAPS][2][4], dp[2][4];
-        dots<DV>(sm + L::O, sm + L::V, dp);
+        dots<DV>(sm + L::O, sm + L::V, n, dp);
 #pragma unroll
         for (int u = 0; u < MAPS; ++u)
-          dots<D>(sm + L::A + u * kTile * (D + 4), sm + L::B + u * kChunk * (D + 4), s[u]);
+          dots<D>(sm + L::A + u * kTile * (D + 4), sm + L::B + u * kChunk * (D + 4), n, s[u]);
         float pv[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
