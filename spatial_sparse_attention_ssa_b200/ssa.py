@@ -714,6 +714,8 @@ def _qkv(p: WindowParams, plan: WindowPlan, q, k, v):
             _want(x.scale, (n, h), torch.float32, name + ".scale")
         arr = (Act8C * 3)(*((_ptr(x.codes), _ptr(x.scale)) for x in (q, k, v)))
         return (None, None, None), arr, [t for x in (q, k, v) for t in (x.codes, x.scale)]
+    if any(isinstance(x, Act8) for x in (q, k, v)):
+        raise ValueError("q, k, v must be three tensors or three Act8")
     for name, x, h in names:
         _want(x, (n, h, p.d), p._dtype, name)
     return (_ptr(q), _ptr(k), _ptr(v)), None, [q, k, v]
@@ -724,7 +726,9 @@ def ssa_window_forward(p: WindowParams, plan: WindowPlan, q: torch.Tensor, k: to
                        lse: torch.Tensor | None = None) -> torch.Tensor:
     """Attention of every token over the tokens of its cell, with an optional learned relative
     position bias: out [N, hq, d].  `lse` (fp32 [N, hq]) receives the softmax normalisers."""
-    ptrs, _, ts = _qkv(p, plan, q, k, v)
+    ptrs, a8, ts = _qkv(p, plan, q, k, v)
+    if a8 is not None:
+        raise ValueError("the forward reads tensors, not Act8")
     bc, _ = _bias_c(bias, p, plan)
     dev = _on_one_device(*ts, plan.rows, out, lse, *((bias.table, bias.bucket) if bias else ()))
     if out is None:
@@ -741,7 +745,9 @@ def _window_backward(op: int, name: str, p: WindowParams, plan: WindowPlan, extr
                      last: torch.Tensor | None, grads, workspace):
     ptrs, a8, ts = _qkv(p, plan, q, k, v)
     _want(dout, (plan.n, p.hq, p.d), p._dtype, "dout")
-    dev = _on_one_device(*ts, dout, plan.rows, last, *extra_tensors, *(grads or ()))
+    dev = _on_one_device(*ts, dout, plan.rows, last, workspace, *extra_tensors, *(grads or ()))
+    if workspace is not None and workspace.dtype != torch.uint8:
+        raise ValueError("workspace must be uint8")
     shapes = ((plan.n, p.hq, p.d), (plan.n, p.hkv, p.d), (plan.n, p.hkv, p.d))
     if grads is None:
         grads = tuple(torch.empty(s, dtype=p._dtype, device=dev) for s in shapes)
@@ -777,7 +783,9 @@ def ssa_diff_forward(p: WindowParams, plan: WindowPlan, q: torch.Tensor, k: torc
     """Differential attention inside the cells: the difference of the softmax maps of heads
     2h and 2h+1 over the value heads 2h, 2h+1 side by side; lam fp32 [4, hq/2, d] holds the
     weights' vectors (see ssa_diff_forward in include/ssa.h).  Returns out [N, hq, d]."""
-    ptrs, _, ts = _qkv(p, plan, q, k, v)
+    ptrs, a8, ts = _qkv(p, plan, q, k, v)
+    if a8 is not None:
+        raise ValueError("the forward reads tensors, not Act8")
     _want(lam, (4, p.hq // 2, p.d), torch.float32, "lam")
     dev = _on_one_device(*ts, lam, plan.rows, out)
     if out is None:

@@ -517,6 +517,87 @@ def test_given_buffers_are_filled_and_nothing_beside_them():
     assert torch.equal(db[1:5], want["dbias"]) and bool((db[0] == 7).all()) and bool((db[5] == 7).all())
 
 
+def test_workspaces_and_checkpoints_where_they_do_not_belong_are_refused():
+    coords, cu = shell(51, 200)
+    pr = Problem(coords, cu, 4, 2, 1, 32, torch.bfloat16, seed=52)
+    held = [ssa.ssa_act8_pack(x) for x in (pr.q, pr.k, pr.v)]
+    with pytest.raises(ValueError, match="Act8"):
+        ssa.ssa_window_forward(pr.p, pr.plan, *held)
+    with pytest.raises(ValueError, match="Act8"):
+        ssa.ssa_window_backward(pr.p, pr.plan, held[0], pr.k, pr.v, pr.dout)
+    need = pr.plan.workspace_size(ssa.OP_WINDOW_BACKWARD, pr.p)
+    with pytest.raises(ValueError, match="uint8"):
+        ssa.ssa_window_backward(pr.p, pr.plan, pr.q, pr.k, pr.v, pr.dout,
+                                workspace=torch.empty(need, dtype=torch.float32, device="cuda"))
+    with pytest.raises(ValueError, match="CUDA"):
+        ssa.ssa_window_backward(pr.p, pr.plan, pr.q, pr.k, pr.v, pr.dout, workspace=torch.empty(need, dtype=torch.uint8))
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Two backward passes of different sizes that overlap give what each gives alone."""
+    prs = []
+    for seed, n, m, hq in ((61, 900, 6, 8), (62, 2500, 8, 4)):
+        coords, cu = shell(seed, n, r=20)
+        prs.append(Problem(coords, cu, m, hq, 2, 64, torch.bfloat16, seed=seed, bias="offset"))
+    alone = [run_window(pr) for pr in prs]
+    streams = [torch.cuda.Stream() for _ in prs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        both = []
+        for pr, st in zip(prs, streams):
+            with torch.cuda.stream(st):
+                both.append(run_window(pr))
+        torch.cuda.synchronize()
+        for a, b in zip(alone, both):
+            assert all(torch.equal(a[x], b[x]) for x in a)
+
+
+@pytest.mark.parametrize("dtype,hkv", [("bf16", 64), ("f32", 4)])
+def test_places_past_32_bits(dtype, hkv):
+    """A full cube of 274625 tokens with 64 heads of 128: elements past 2^31 in q (and, in bf16, k
+    and v).  The last cell against fp64 for the first and the last head; bounds of one storage
+    rounding of P or dS and of the result (bf16 2 x 2^-8 of the row sums' magnitudes; fp32 1e-5 for
+    sums of up to 128 fp32 products, 2^-24 each)."""
+    side, m, hq, d, dt = 65, 5, 64, 128, DT[dtype]
+    n = side ** 3
+    key = torch.arange(n, device="cuda")
+    coords = torch.stack([key // side ** 2, key // side % side, key % side], 1).to(torch.int32)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    _, win = ssa.ssa_bin(coords, cu, 1024, m, m)
+    plan = ssa.ssa_window_plan(coords, win, m)
+    assert n * hq * d > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    f = lambda h: torch.randn(n, h, d, generator=gen, dtype=dt, device="cuda")  # noqa: E731
+    q, k, v, dout = f(hq), f(hkv), f(hkv), f(hq)
+    p = ssa.make_window_params(hq, hkv, d, dt)
+    out = ssa.ssa_window_forward(p, plan, q, k, v)
+    dq, dk, dv, _ = ssa.ssa_window_backward(p, plan, q, k, v, dout)
+    last = (coords >= side - m).all(1).nonzero()[:, 0]
+    g = hq // hkv
+    tol = 2 * 2.0 ** -8 if dtype == "bf16" else 1e-5
+
+    def near(got, ref, mag):
+        assert bool(((got.double() - ref).abs() <= tol * mag + 1e-30).all())
+    for hk in (0, hkv - 1):
+        kk, vv = k[last, hk].double(), v[last, hk].double()
+        rdk, rdv, mdk, mdv = (torch.zeros_like(kk) for _ in range(4))
+        for h in range(hk * g, hk * g + g):
+            qq, do = q[last, h].double(), dout[last, h].double()
+            s = torch.softmax(qq @ kk.T / np.sqrt(d), -1)
+            dp = do @ vv.T
+            dd = (s * dp).sum(-1, keepdim=True)
+            ds = s * (dp - dd)
+            mds = s * (dp.abs() + (s * dp.abs()).sum(-1, keepdim=True))
+            near(out[last, h], s @ vv, s @ vv.abs())
+            near(dq[last, h], ds @ kk / np.sqrt(d), mds @ kk.abs() / np.sqrt(d))
+            rdk += ds.T @ qq / np.sqrt(d)
+            mdk += mds.T @ qq.abs() / np.sqrt(d)
+            rdv += s.T @ do
+            mdv += s.T @ do.abs()
+        near(dk[last, hk], rdk, mdk)
+        near(dv[last, hk], rdv, mdv)
+
+
 def test_no_tokens():
     z = lambda *s, dt=torch.float32: torch.empty(*s, dtype=dt, device="cuda")  # noqa: E731
     win = ssa.Bins.empty(0, 1, "cuda")
