@@ -6,8 +6,16 @@
 // (cp.async, completion on an mbarrier); the cell's rows, 16 at a time, go to the other warps in
 // turn, so no warp waits for another but through the ring.  Scores never leave registers: a step is
 // 16 rows by 32 keys.  Tiles of 128 rows (tcgen05) would stand half empty on windows of some 50
-// tokens and hand every score through TMEM.  What bounds these kernels is instruction issue: the
-// softmax, the bias and the masks of a score take several times the issue slots of its products.
+// tokens and hand every score through TMEM.
+//
+// What bounds these kernels is instruction issue and its latencies: of some 330 instructions of a
+// forward step 32 are products, the rest the bias, the mask, the exponential and the sums; and a tile
+// of 16 rows costs some 500 before its first and after its last step, which cells of 47 tokens (1.9
+// steps a tile) do not spread.  32768 tokens (32/2 heads of 64, edge 8; forward, statistics, dq,
+// dk/dv): issue slots used 46, 47, 41, 37%, tensor pipe 19, 19, 19, 37%, shared memory 51, 44, 57,
+// 59%, HBM below 20%.  Times at 131072 tokens, and the TFLOP/s of the products alone (31.3 GFLOP each):
+// forward 790 us (79), statistics 803 us (78), dq with dbias 1324 us (71), dk/dv 927 us (135);
+// differential 1155, 705, 1027, 967 us; full cube of 24576, 16/2 heads of 128: 398, 408, 661, 567 us.
 #include "tc.cuh"
 #include "window.cuh"
 
@@ -874,7 +882,10 @@ cudaError_t rows_pass(const char* name, const WinArgs& a, cudaStream_t st) {
 
 // A CTA of four warps takes 64 keys of a cell and one key head, 16 keys per warp: the transposed
 // scores of the cell's queries, 64 at a time, of every query head that reads the key head.  Q, dO,
-// the statistics and the head's bias table of the next step arrive while this one is computed.
+// the statistics and the head's bias table of the next step arrive while this one is computed.  Keys
+// stay with a CTA so that dk and dv are sums in registers, with no atomics, rounded once.  Bound by
+// issue and by the barriers of a step (cells of 47 tokens leave one warp in four without keys): 927 us
+// at 131072 tokens, 32/2 heads of 64; one barrier a step instead of two, its copies begun after it: 935.
 constexpr int kDkvWarps = 4;
 
 // Number of key tiles of the CTA of a slot: four from every fourth tile of a cell.

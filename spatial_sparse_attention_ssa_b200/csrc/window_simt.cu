@@ -1,10 +1,15 @@
-// Attention inside the cells on the CUDA cores: fp32 products and sums from fp32 or 8-bit rows.  See window.cuh for the mathematics and the meaning of MAPS.
+// Attention inside the cells on the CUDA cores: fp32 products and sums from fp32 or 8-bit rows.  See
+// window.cuh for the mathematics and the meaning of MAPS.
 //
 // One CTA (128 threads) takes tiles of 16 rows of a cell against the cell in chunks of 64.
 // Thread (ty, tx), tid = 16 ty + tx, holds the scores of rows ty, ty + 8 against the chunk's
 // rows tx + 16 j, and of the products with a chunk the columns tx * VEC (+ 64).  Cells of up
 // to 64 tokens keep their one chunk's scores in registers; larger cells take two passes, one
-// for the softmax statistics (and D), one for the products.
+// for the softmax statistics (and D), one for the products.  fp32 results within a few 2^-24 leave the
+// tensor core formats out.  Bound by shared memory (59 to 79% of its wavefronts) and by the loads that
+// fill a tile before its one or two chunks: 20011 tokens, 8/2 heads of 32, edge 6: forward 105 us,
+// dq with dbias 173 us, dk/dv 135 us (7, 6 and 11 TFLOP/s of products); differential, 9001 tokens: 50, 72, 73.
+// Loads of four rows ahead in `fill` cost registers and with them CTAs (dq 173 -> 238 us).
 #include "window.cuh"
 
 namespace ssa {
@@ -413,7 +418,7 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(WinArgs a) {
   for (int i = threadIdx.x; i < T3; i += kThreads) part[i] = dtab[i];
 }
 
-// dk, dv of 16 keys: the transposed scores of all query heads of the key head against the
+// dk, dv of 16 keys (sums in registers, no atomics): the transposed scores of all query heads of the key head against the
 // cell's rows in chunks of 64.
 template <typename E, typename T, int D, int MAPS>
 __global__ void __launch_bounds__(kThreads) window_dkv_kernel(WinArgs a) {
