@@ -408,7 +408,8 @@ struct Shape {
                                          : MAPS == 2 || (MODE == kDq && DV == 64) ? 10 : 14;
   // Q and dO stay in registers as fragments, or are read again from the scratch tiles for every step
   // where that leaves registers for more warps (forward of rows of 128: six warps 452 us, ten 404 us;
-  // differential, both maps' sums: 1259 -> 1112 us; its statistics 787 -> 704 us)
+  // differential, both maps' sums: 1259 -> 1155 us; its statistics 787 -> 705 us; dq of rows of 32,
+  // 5003 tokens: ten warps 40.2 us, fourteen 38.3 us; but dq of rows of 64: 1324, 1386 us)
   static constexpr bool held = (MODE == kDq && DV >= 64) || (MODE == kStats && MAPS == 1);
 };
 constexpr int kStages = 8;  // of the ring at most

@@ -168,12 +168,13 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
                                             pack_bf16x2(x[6], x[7]));
 }
 
-// 2^sh = d / 8 lanes per row, 8 values each, kGroups such rounds in flight per thread: bound by HBM, and
-// with one round at a time a round's loads waited for the stores of the one before.  Q, K, V of 131072
-// tokens (32/2 heads of 64, 925 MB to move either way): 234 us packing (60% of the measured copy
-// bandwidth), 175 us unpacking (81%); 465 us together with one round.  Packing takes the codes out of the
-// low bits of a float sum, which costs fewer instructions than a conversion, a clamp and a shift for each
-// (247 -> 234 us).
+// Packing: 2^sh = d / 16 lanes per row, 16 values each, two rounds in flight per thread; unpacking: d / 8
+// lanes, 8 values, kGroups rounds.  Bound by HBM; with one round at a time a round's loads waited for the
+// stores of the one before.  Q, K, V of 131072 tokens (32/2 heads of 64, 925 MB to move either way):
+// 202 us packing (70% of the measured copy bandwidth; 234 us with 8 values a lane, whose codes are half
+// a lane's widest store), 175 us unpacking (81%); 465 us together with one round of 8 values.  Packing
+// takes the codes out of the low bits of a float sum, which costs fewer instructions than a conversion,
+// a clamp and a shift for each (247 -> 234 us).
 // The step is the smallest power of two s >= 2^-126 with top <= 127 s: with top = f 2^e, f in [1, 2),
 // s = 2^(e - 6) while f <= 127 / 64, else 2^(e - 5).
 constexpr int kGroups = 4;
@@ -181,25 +182,27 @@ constexpr int kGroups = 4;
 template <typename T>
 __global__ void act8_pack_kernel(const T* __restrict__ x, int64_t groups, int sh, int8_t* __restrict__ codes,
                                  float* __restrict__ scale) {
+  constexpr int G = 2;  // rounds in flight, of 16 values a lane
   const int64_t stride = (int64_t)gridDim.x * blockDim.x;
   for (int64_t i0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i0 - (threadIdx.x & 31) < groups;
-       i0 += kGroups * stride) {
-    float v[kGroups][8];
+       i0 += G * stride) {
+    float v[G][16];
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
+    for (int g = 0; g < G; ++g) {
       if (i0 + g * stride < groups) {
-        load8<T>(x + 8 * (i0 + g * stride), v[g]);
+        load8<T>(x + 16 * (i0 + g * stride), v[g]);
+        load8<T>(x + 16 * (i0 + g * stride) + 8, v[g] + 8);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[g][j] = 0.f;
+        for (int j = 0; j < 16; ++j) v[g][j] = 0.f;
       }
     }
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
+    for (int g = 0; g < G; ++g) {
       const int64_t i = i0 + g * stride;
       uint32_t top = 0;  // of the magnitudes' bits: NaN and infinity come out on top
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[g][j]) & 0x7fffffffu);
+      for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(v[g][j]) & 0x7fffffffu);
       for (int o = 1 << sh >> 1; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       int e = (int)(top >> 23);  // biased exponent; 0 for zero and subnormal rows
       e = e - 6 + ((top & 0x7fffffu) > 0x7e0000u ? 1 : 0);
@@ -212,16 +215,16 @@ __global__ void act8_pack_kernel(const T* __restrict__ x, int64_t groups, int sh
       if (i < groups) {
         // the nearest whole number is in the low bits of v / s + 1.5 2^23 (v / s is exact, so the sum
         // is rounded once, ties to even)
-        uint32_t n[8];
+        uint32_t n[16];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 16; ++j)
           n[j] = bad ? 0u : __float_as_uint(fmaf(fminf(fmaxf(v[g][j], -limit), limit), r, 12582912.f));
-        uint32_t w[2];
+        uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 4; ++j)
           w[j] = __byte_perm(__byte_perm(n[4 * j], n[4 * j + 1], 0x0040), __byte_perm(n[4 * j + 2], n[4 * j + 3], 0x0040),
                              0x5410);
-        reinterpret_cast<uint2*>(codes)[i] = make_uint2(w[0], w[1]);
+        reinterpret_cast<uint4*>(codes)[i] = make_uint4(w[0], w[1], w[2], w[3]);
         if ((i & ((1 << sh) - 1)) == 0) scale[i >> sh] = s;
       }
     }
@@ -293,13 +296,13 @@ cudaError_t window_param_grads(const WinArgs& a, cudaStream_t st) {
 }
 
 cudaError_t act8_pack(int dtype, int64_t rows, int d, const void* x, int8_t* codes, float* scale, cudaStream_t st) {
-  const int64_t g = rows * (d / 8);
-  const int sh = d == 32 ? 2 : d == 64 ? 3 : 4;
+  const int64_t g = rows * (d / 16);
+  const int sh = d == 32 ? 1 : d == 64 ? 2 : 3;
   if (dtype == SSA_DTYPE_BF16)
-    SSA_LAUNCH("act8_pack_kernel", act8_pack_kernel<__nv_bfloat16>, blocks_for((g + kGroups - 1) / kGroups, 256), 256, 0, st,
+    SSA_LAUNCH("act8_pack_kernel", act8_pack_kernel<__nv_bfloat16>, blocks_for((g + 1) / 2, 256), 256, 0, st,
                static_cast<const __nv_bfloat16*>(x), g, sh, codes, scale);
   else
-    SSA_LAUNCH("act8_pack_kernel", act8_pack_kernel<float>, blocks_for((g + kGroups - 1) / kGroups, 256), 256, 0, st,
+    SSA_LAUNCH("act8_pack_kernel", act8_pack_kernel<float>, blocks_for((g + 1) / 2, 256), 256, 0, st,
                static_cast<const float*>(x), g, sh, codes, scale);
   return cudaGetLastError();
 }
