@@ -457,8 +457,8 @@ SSA_API ssa_status ssa_window_forward(const ssa_window_params* p, const ssa_win_
  * ssa_window_backward -- gradients of sum(dout * out): dq [N, hq, d], dk, dv [N, hkv, d] in
  * dtype (each summed in fp32 and rounded once), dbias fp32 [hq, nb] (NULL: not wanted, or
  * no bias); all written.  It recomputes the probabilities and needs nothing the forward left.
- *          A NaN or an infinity in the inputs of a head makes all of its dbias NaN in
- *          SSA_DTYPE_BF16; dq, dk, dv show it in its own cell only.
+ *          A NaN or an infinity in the inputs of a head, or a |<dout_i, v_j>| of 2^127 or more,
+ *          makes all of its dbias NaN in SSA_DTYPE_BF16; dq, dk, dv show it in its own cell only.
  *   act8   NULL, or an array of three: Q, K, V from 8-bit checkpoints (q, k, v are then
  *          ignored); the gradients are those at the values the codes hold, in dtype.  In
  *          SSA_DTYPE_BF16 the workspace holds them as bf16 during the call

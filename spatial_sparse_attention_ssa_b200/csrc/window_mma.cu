@@ -284,7 +284,9 @@ __device__ __forceinline__ void red_shared(uint32_t at, int x) {
 // so 2^k <= 2^31 / (adds per offset) keeps the second, adds = rows times the most tokens that one voxel
 // holds (a.tiles[T].x).  The rows of the CTA are counted, not bounded by its slots: at 131072 tokens
 // that is two bits more for each number.  Below 2^12 rows and without shared voxels the unit is at most
-// M 2^-34.  A NaN or an infinity in dP or in a softmax makes the head's gradient NaN.
+// M 2^-34.  A NaN or an infinity in dP or in a softmax makes the head's gradient NaN, and so does an M
+// from 2^127 on (dP - D could overflow); below, 2^s and 2^-s are normal numbers.
+constexpr uint32_t kTopDp = 0x7f000000u;  // 2^127
 struct Limbs {
   float s, k, unit;  // 2^s, 2^k, 2^-s
   int kbits;
@@ -294,9 +296,9 @@ struct Limbs {
     const int rb = 32 - __clz(rows), ab = 64 - __clzll(adds);  // rows < 2^rb, adds < 2^ab
     const int e = (int)(bits >> 23) - 126;                      // M < 2^e
     int sb = min(29 - rb - 1 - e, 20 - e);                      // |dS 2^s| < 2^22: see add()
-    sb = max(-100, min(100, sb));
+    sb = max(-126, min(126, sb));
     kbits = max(0, min(21, 31 - ab));
-    s = __uint_as_float(bits >= 0x7f800000u ? 0x7fc00000u : (uint32_t)(sb + 127) << 23);
+    s = __uint_as_float(bits >= kTopDp ? 0x7fc00000u : (uint32_t)(sb + 127) << 23);
     k = (float)(1 << kbits);
     unit = 1.f / s;
   }
@@ -319,15 +321,14 @@ struct Limbs {
 __host__ __device__ inline int wide_bits(uint32_t amax, int64_t N) {
   int rb = 0;
   while (rb < 62 && (int64_t(1) << rb) <= N) ++rb;  // N < 2^rb
-  const int sb = 61 - rb - 1 - ((int)(amax >> 23) - 126);
-  return sb < -100 ? -100 : sb > 100 ? 100 : sb;
+  return 61 - rb - 1 - ((int)(amax >> 23) - 126);
 }
 struct Wide {
   char* sums;  // of the head
   double s;
   __device__ __forceinline__ void set(const WinArgs& a, int h) {
     sums = reinterpret_cast<char*>(a.sums + (size_t)h * offsets(a.m));
-    s = (double)__uint_as_float((uint32_t)(wide_bits(__ldg(a.amax + h), a.N) + 127) << 23);
+    s = __longlong_as_double((long long)(wide_bits(__ldg(a.amax + h), a.N) + 1023) << 52);
   }
   __device__ __forceinline__ void add(int at, float x) const {  // at: four times the offset
     atomicAdd(reinterpret_cast<unsigned long long*>(sums + 2 * (int64_t)at), (unsigned long long)__double2ll_rn((double)x * s));
@@ -1148,7 +1149,7 @@ __global__ void bias_wide_kernel(WinArgs a) {
   if (o >= T3) return;
   const uint32_t amax = a.amax[h];
   const double v = ldexp((double)(long long)a.sums[(size_t)h * T3 + o], -wide_bits(amax, a.N));
-  a.part[(size_t)h * T3 + o] = amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : (float)v;
+  a.part[(size_t)h * T3 + o] = amax >= kTopDp ? __uint_as_float(0x7fc00000u) : (float)v;
 }
 
 }  // namespace
