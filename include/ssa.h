@@ -389,8 +389,9 @@ SSA_API ssa_status ssa_sp_backward(const ssa_params* p, int32_t S, int64_t N, co
 typedef struct ssa_win_plan {
   int32_t* rows;   /* [n, 2] in cell order: the token and its offset code */
   int32_t* tiles;  /* [n / SSA_WINDOW_TILE + count + 1, 4]: up to 16 rows of one cell: first row, rows
-                      (+ 65536 where the cell holds two tokens in one voxel), the cell's first and
-                      end row; unused entries hold zeros; the last entry: the most tokens that one
+                      (where the cell holds two tokens in one voxel: + 65536, + 131072 times the most
+                      tokens of one voxel, counted to 16383), the cell's first and end row; unused
+                      entries hold zeros; the last entry: the most tokens that one
                       voxel of a cell holds, and three zeros */
   int64_t n;       /* out: tokens */
   int64_t count;   /* out: cells of the partition */

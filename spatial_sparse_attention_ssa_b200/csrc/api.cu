@@ -789,7 +789,7 @@ size_t carve_window(void* base, const ssa_window_params* p, const ssa_win_plan* 
   float* part = c.take<float>(tab * parts);
   float* tab2 = c.take<float>(tab ? tab + 3 * (size_t)p->hq : 0);  // rows of a multiple of 4
   unsigned* amax = c.take<unsigned>(p->hq);
-  unsigned long long* sums = c.take<unsigned long long>(wide ? tab : 0);
+  unsigned long long* sums = c.take<unsigned long long>(p->dtype == SSA_DTYPE_BF16 ? tab : 0);
   // the rows of 8-bit checkpoints as bf16: the bf16 kernels read them several times, K and V once
   // per query head
   const size_t q_values = act8 && p->dtype == SSA_DTYPE_BF16 ? (size_t)p->hq * plan->n * p->d : 0;
@@ -808,7 +808,7 @@ size_t carve_window(void* base, const ssa_window_params* p, const ssa_win_plan* 
     a->tab2 = tab2;
     a->amax = amax;
     a->wide = wide;
-    a->sums = sums;
+    a->sums = p->dtype == SSA_DTYPE_BF16 ? sums : nullptr;
   }
   return c.used;
 }

@@ -155,7 +155,8 @@ struct WinArgs {
   float scale;
   int64_t N;
   const int2* rows;   // [N] token, code in cell order
-  const int4* tiles;  // [T] first row, rows (+ flag), cell begin, cell end; [T].x: most tokens of a voxel
+  const int4* tiles;  // [T] first row, rows (+ flag, + kDupUnit times most tokens of a voxel), cell begin,
+                      // cell end; [T].x: most tokens of a voxel of any cell
   int T, m;
   int64_t cells;
   const float* table;  // bias [hq, nb], or null
@@ -180,7 +181,7 @@ struct WinArgs {
   unsigned* amax;   // [hq] the largest |dP| of a head, as bits
   int* status;      // device check word
   int wide;         // bf16 and an edge from kWideEdge on: one part, summed in `sums`
-  unsigned long long* sums;  // [hq][offsets]
+  unsigned long long* sums;  // [hq][offsets] (bf16 with a bias): also for cells with a crowded voxel
 };
 cudaError_t window_plan(const int32_t* coords, int64_t N, int m, const ssa_partition* win, int2* rows, int4* tiles,
                         int* status, cudaStream_t st);

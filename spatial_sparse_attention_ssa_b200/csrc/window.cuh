@@ -21,12 +21,24 @@ namespace win {
 
 constexpr int kTile = SSA_WINDOW_TILE;  // rows of a work tile
 constexpr int kDupFlag = 65536;         // tiles[].y: two tokens of the cell share a voxel
+constexpr int kDupUnit = 131072;        // and from here on: the most tokens of one voxel, kDupTop at most
+constexpr int kDupTop = 16383;
+constexpr int kDupMost = 2048;  // more in one voxel: the cell's bias gradient goes to the 64-bit sums (bf16)
 
 // Offsets of a window of edge m, and the number of the offset 0.
 __host__ __device__ inline int offsets(int m) { return (2 * m - 1) * (2 * m - 1) * (2 * m - 1); }
 // Floats from one head's table of offsets to the next in WinArgs::tab2.
 __host__ __device__ inline int table_pitch(int m) { return (offsets(m) + 3) & ~3; }
 __host__ __device__ inline int center(int m) { return (m - 1) * ((2 * m - 1) * (2 * m - 1) + (2 * m - 1) + 1); }
+
+// The 64-bit sums of the bias gradient (WinArgs::sums): dS 2^s with 2^s <= 2^61 / (2 M N), M < 2^127 the
+// largest |dP| of the head, as bits.
+constexpr uint32_t kTopDp = 0x7f000000u;  // 2^127
+__host__ __device__ inline int wide_bits(uint32_t amax, int64_t N) {
+  int rb = 0;
+  while (rb < 62 && (int64_t(1) << rb) <= N) ++rb;  // N < 2^rb
+  return 61 - rb - 1 - ((int)(amax >> 23) - 126);
+}
 
 // 2^x (x <= 0 here, or minus infinity, or NaN).
 __device__ __forceinline__ float ex2(float x) {

@@ -281,29 +281,33 @@ __device__ __forceinline__ void red_shared(uint32_t at, int x) {
 // memory, whose order cannot change the sums.  Bounds: the |dS| of a row sum to at most 2 M, M the
 // largest |dP| of the head (from the row statistics, a.amax), so 2^s <= 2^29 / (2 M rows) keeps the
 // first (a rounding at most doubles a number that it does not make 0); each remainder is at most 1/2,
-// so 2^k <= 2^31 / (adds per offset) keeps the second, adds = rows times the most tokens that one voxel
-// holds (a.tiles[T].x).  The rows of the CTA are counted, not bounded by its slots: at 131072 tokens
-// that is two bits more for each number.  Below 2^12 rows and without shared voxels the unit is at most
-// M 2^-34.  A NaN or an infinity in dP or in a softmax makes the head's gradient NaN, and so does an M
-// from 2^127 on (dP - D could overflow); below, 2^s and 2^-s are normal numbers.
-constexpr uint32_t kTopDp = 0x7f000000u;  // 2^127
+// so 2^k <= 2^31 / (adds per offset) keeps the second, adds = rows times the most tokens that a voxel
+// of their cell holds.  Both stay below 2^13: before they pass it the CTA's sums go to its partial
+// gradient and start again, so the unit is M 2^-33 however many rows a CTA has.  An item of one crowded
+// cell can pass that alone: up to kDupMost tokens in a voxel the unit of its own few rows is M 2^-32
+// where dS is some M 2^-11; cells that are more crowded (kFar) take the 64-bit sums below.  A NaN or an infinity in dP or in a softmax makes the
+// head's gradient NaN, and so does an M from 2^127 on (dP - D could overflow); below, 2^s and 2^-s are
+// normal numbers.
+constexpr int kAdds = 8191;    // at most between two flushes, but for a lone item
+constexpr int kFar = 1 << 16;  // items[].y: a cell for the 64-bit sums
 struct Limbs {
-  float s, k, unit;  // 2^s, 2^k, 2^-s
-  int kbits;
-  __device__ __forceinline__ void set(const WinArgs& a, int h, int rows) {
+  float s, k;            // 2^s, 2^k
+  double unit, unit_lo;  // 2^-s, 2^-s-k
+  __device__ __forceinline__ void set(const WinArgs& a, int h, int rows, int adds) {
+    if (adds <= kAdds) rows = adds = kAdds;
     const uint32_t bits = __ldg(a.amax + h);
-    const int64_t adds = (int64_t)rows * max(1, __ldg(&a.tiles[a.T].x));
-    const int rb = 32 - __clz(rows), ab = 64 - __clzll(adds);  // rows < 2^rb, adds < 2^ab
+    const int rb = 32 - __clz(rows), ab = 32 - __clz(adds);  // rows < 2^rb, adds < 2^ab
     const int e = (int)(bits >> 23) - 126;                      // M < 2^e
     int sb = min(29 - rb - 1 - e, 20 - e);                      // |dS 2^s| < 2^22: see add()
     sb = max(-126, min(126, sb));
-    kbits = max(0, min(21, 31 - ab));
+    const int kbits = max(0, min(21, 31 - ab));
     s = __uint_as_float(bits >= kTopDp ? 0x7fc00000u : (uint32_t)(sb + 127) << 23);
     k = (float)(1 << kbits);
-    unit = 1.f / s;
+    unit = (double)(1.f / s);
+    unit_lo = unit * (double)(1.f / k);
   }
   __device__ __forceinline__ float value(int hi, int lo) const {
-    return (float)(((double)hi + (double)lo / (double)(1 << kbits)) * (double)unit);
+    return (float)((double)hi * unit + (double)lo * unit_lo);
   }
   // x 2^s to the nearest whole number by adding 1.5 2^23 (|x 2^s| < 2^22), and the rest
   __device__ __forceinline__ void add(uint32_t hi, uint32_t lo, float x) const {
@@ -316,13 +320,8 @@ struct Limbs {
   }
 };
 
-// Edges whose two tables do not fit beside the ring keep one 64-bit number per offset in global
-// memory: dS 2^s with 2^s <= 2^61 / (2 M N).
-__host__ __device__ inline int wide_bits(uint32_t amax, int64_t N) {
-  int rb = 0;
-  while (rb < 62 && (int64_t(1) << rb) <= N) ++rb;  // N < 2^rb
-  return 61 - rb - 1 - ((int)(amax >> 23) - 126);
-}
+// Edges whose two tables do not fit beside the ring, and cells with a crowded voxel: one 64-bit number
+// per offset in global memory (wide_bits).
 struct Wide {
   char* sums;  // of the head
   double s;
@@ -331,7 +330,10 @@ struct Wide {
     s = __longlong_as_double((long long)(wide_bits(__ldg(a.amax + h), a.N) + 1023) << 52);
   }
   __device__ __forceinline__ void add(int at, float x) const {  // at: four times the offset
-    atomicAdd(reinterpret_cast<unsigned long long*>(sums + 2 * (int64_t)at), (unsigned long long)__double2ll_rn((double)x * s));
+    add_ll(at, __double2ll_rn((double)x * s));
+  }
+  __device__ __forceinline__ void add_ll(int at, long long x) const {
+    atomicAdd(reinterpret_cast<unsigned long long*>(sums + 2 * (int64_t)at), (unsigned long long)x);
   }
 };
 
@@ -346,6 +348,32 @@ __device__ __forceinline__ void add_bias_grad(const F& add, float (*ds)[4], cons
 #pragma unroll
     for (int x = 0; x < 4; ++x) add((x & 2 ? ci8 : ci) - (x & 1 ? cj.y : cj.x), ds[j][x]);
   }
+}
+
+// The same for a cell with a crowded voxel: a step whose rows and positions all lie in one voxel adds its
+// 512 numbers up first, since their atomics would queue for one address.  Not inlined: it would stand in
+// the way of the instructions of every step (dq of 131072 tokens: inlined 1536 us, called 1490).
+__device__ __noinline__ void add_crowded(Wide wide, const float (*v)[4], const int* codes, int ci, int ci8) {
+  float ds[4][4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) ds[j][x] = v[j][x];
+  const int lane = threadIdx.x & 31, c = codes[lane];
+  const int c_first = __shfl_sync(kFull, c, 0), ci_first = __shfl_sync(kFull, ci, 0);  // by every lane
+  if (__all_sync(kFull, c == c_first && ci == ci_first && ci8 == ci_first)) {
+    long long sum = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) sum += __double2ll_rn((double)ds[j][x] * wide.s);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    if (lane == 0) wide.add_ll(ci - c, sum);
+  } else {
+    add_bias_grad([&](int at, float x) { wide.add(at, x); }, ds, codes, ci, ci8);
+  }
+  __syncwarp();
 }
 
 // The keys of a chunk stand in shared memory in another order than in the cell: position
@@ -428,7 +456,8 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
   constexpr bool BIAS = TAB != 0;
   extern __shared__ __align__(128) char sm[];
   __shared__ uint64_t full[kStages], empty[kStages];
-  __shared__ int n_items, n_rows;  // items of the batch; rows of all of the CTA's items
+  __shared__ int n_slots, n_items;         // of the batch
+  __shared__ int n_rows, n_adds, n_flush;  // since the last flush (see Limbs); whether the batch ends with one
   const int NW = (int)blockDim.x / 32 - 2;  // working warps; two more fill the ring
   const uint32_t v_at = chunk * S::row, codes_at = 2 * v_at, stage_size = chunk * S::token;
   const int h0 = pairs * blockIdx.y, hk = h0 / (a.hq / a.hkv), item_size = NW / pairs;
@@ -462,22 +491,6 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
   Limbs fx;
   Wide wide;
   float s2[2] = {0.f, 0.f};
-  if (grad && TAB != 3) {
-    if (threadIdx.x == 0) n_rows = 0;
-    __syncthreads();
-    int mine = 0;
-    for (int64_t t = blockIdx.x + (int64_t)threadIdx.x * gridDim.x; t < a.T; t += (int64_t)blockDim.x * gridDim.x) {
-      const int4 x = __ldg(&a.tiles[t]);
-      if (item_tiles(x, item_size)) mine += min(item_size * kTile, x.w - x.x);
-    }
-    mine = __reduce_add_sync(kFull, mine);
-    if (lane == 0) atomicAdd(&n_rows, mine);
-    __syncthreads();
-    for (int i = pairs - 1; i >= 0; --i) {
-      fx.set(a, h0 + i, n_rows);
-      (i ? s2[1] : s2[0]) = fx.s;
-    }
-  }
   float lams[2] = {0.f, 0.f};
   if constexpr (MAPS == 2) {
     for (int i = 0; i < pairs; ++i) {
@@ -488,27 +501,64 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
   }
   uint32_t tops[2] = {0, 0};  // the largest |dP| of a head, as bits: NaN above all
 
+  bool written = false;             // the CTA's partial gradient
   int rot = 0;                      // the warp that takes the next item's first tile
   int fs = 0, fphase = warp >= NW;  // stage and phase of the next fill (to make one never waits at first)
   bool ok = true;
-  for (int64_t batch = blockIdx.x; batch < a.T && ok; batch += (int64_t)S::items * gridDim.x) {
+  for (int64_t batch = blockIdx.x; batch < a.T && ok; batch += (int64_t)n_slots * gridDim.x) {
     // the batch's items, in the order of their slots
     __syncthreads();
     if (warp == NW) {
-      int n = 0;
+      int n = 0, i0 = 0, rows = 0, adds = 0;
+      if (grad && TAB != 3 && batch != blockIdx.x && !n_flush) rows = n_rows, adds = n_adds;
+      bool more = true;
 #pragma unroll 2
-      for (int i0 = 0; i0 < S::items && batch + (int64_t)i0 * gridDim.x < a.T; i0 += 32) {
+      while (more && i0 < S::items && batch + (int64_t)i0 * gridDim.x < a.T) {
         const int64_t t = batch + (int64_t)(i0 + lane) * gridDim.x;
         int4 x = t < a.T ? __ldg(&a.tiles[t]) : make_int4(0, 0, 0, 0);
+        const int dup = max(1, x.y / kDupUnit);
         x.y = item_tiles(x, item_size);
-        const unsigned some = __ballot_sync(kFull, x.y > 0);
-        if (x.y > 0) items[n + __popc(some & ((1u << lane) - 1u))] = x;
+        int take = 32;  // slots of these 32
+        if (grad && TAB != 3) {
+          const bool far = dup > kDupMost;
+          const int r = x.y > 0 && !far ? min(item_size * kTile, x.w - x.x) : 0;
+          const int all = __reduce_add_sync(kFull, r * dup);
+          if (adds + all <= kAdds) {
+            adds += all;
+          } else {  // the first slot that passes the bound waits for a flush, but for a lone one
+            int sum = r * dup;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const int y = __shfl_up_sync(kFull, sum, o);
+              if (lane >= o) sum += y;
+            }
+            sum += adds;
+            const unsigned over = __ballot_sync(kFull, sum > kAdds && sum > r * dup);
+            if (over) take = __ffs(over) - 1, more = false;
+            if (take > 0) adds = __shfl_sync(kFull, sum, take - 1);
+          }
+          rows += __reduce_add_sync(kFull, lane < take ? r : 0);
+          if (x.y > 0 && far) x.y |= kFar;
+        }
+        const bool mine = lane < take && x.y > 0;
+        const unsigned some = __ballot_sync(kFull, mine);
+        if (mine) items[n + __popc(some & ((1u << lane) - 1u))] = x;
         n += __popc(some);
+        i0 += take;
       }
-      if (lane == 0) n_items = n;
+      if (lane == 0) {
+        n_items = n, n_slots = i0, n_rows = rows, n_adds = adds;
+        n_flush = !more || adds > kAdds || batch + (int64_t)i0 * gridDim.x >= a.T;
+      }
     }
     __syncthreads();
     const int count = n_items;
+    if (grad && TAB != 3) {
+      for (int i = pairs - 1; i >= 0; --i) {
+        fx.set(a, h0 + i, n_rows, n_adds);
+        (i ? s2[1] : s2[0]) = fx.s;
+      }
+    }
     if (warp >= NW) {
       // the filling warps, one for the keys and the codes, one for the values: lane l holds the places
       // (in units of 16 bytes) of the rows l and 32 + l of the coming chunk
@@ -563,10 +613,11 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
             entries(items[ii + 1].z, items[ii + 1].w);
         }
       }
-      continue;
     }
-    for (int ii = 0; ii < count && ok; ++ii) {
-      const int4 item = items[ii];
+    for (int ii = 0; ii < count && ok && warp < NW; ++ii) {
+      int4 item = items[ii];
+      const bool far = item.y & kFar;
+      item.y &= kFar - 1;
       const int lo = item.z, hi = item.w;
       int mine = warp - rot;
       if (mine < 0) mine += NW;
@@ -675,10 +726,19 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
               if (BIAS) {
                 if (grad) {
                   const uint32_t to = tc::smem_u32(limbs) + 8 * pair * T3;
-                  if constexpr (TAB == 3)
+                  if constexpr (TAB == 3) {
                     add_bias_grad([&](int at, float x) { wide.add(at, x); }, s[0], hc, ci, ci8);
-                  else
+                  } else if (far) {
+                    float ds[4][4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                      for (int x = 0; x < 4; ++x) ds[j][x] = s[0][j][x];
+                    wide.set(a, h);
+                    add_crowded(wide, ds, hc, ci, ci8);
+                  } else {
                     add_bias_grad([&](int at, float x) { fx.add(to + at, to + at + 4 * T3, x); }, s[0], hc, ci, ci8);
+                  }
                 }
               }
               uint32_t f[2][4];
@@ -804,6 +864,21 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
         store_acc<D, DV>(scratch, acc, a.scale, a.scale, static_cast<bf16*>(a.dq), a.hq, MAPS * h, a.rows, first, nr);
       }
     }
+    if (grad && TAB != 3 && n_flush) {
+      // the sums since the last flush; each thread has offsets of its own
+      __syncthreads();
+      for (int p = 0; p < pairs; ++p) {
+        fx.set(a, h0 + p, n_rows, n_adds);
+        int* from = limbs + p * 2 * T3;
+        float* part = a.part + ((size_t)(h0 + p) * a.parts + blockIdx.x) * T3;
+        for (int i = threadIdx.x; i < T3; i += blockDim.x) {
+          const float x = fx.value(from[i], from[T3 + i]);
+          part[i] = written ? part[i] + x : x;
+          from[i] = from[T3 + i] = 0;
+        }
+      }
+      written = true;
+    }
   }
   cp_commit();
   cp_wait<0>();
@@ -812,15 +887,6 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
     for (int i = 0; i < pairs; ++i) {
       const uint32_t top = __reduce_max_sync(kFull, i ? tops[1] : tops[0]);
       if (lane == 0 && a.dbias) atomicMax(a.amax + h0 + i, top);
-    }
-  }
-  if (grad && TAB != 3) {
-    __syncthreads();
-    for (int p = 0; p < pairs; ++p) {
-      fx.set(a, h0 + p, n_rows);
-      const int* from = limbs + p * 2 * T3;
-      float* part = a.part + ((size_t)(h0 + p) * a.parts + blockIdx.x) * T3;
-      for (int i = threadIdx.x; i < T3; i += blockDim.x) part[i] = fx.value(from[i], from[T3 + i]);
     }
   }
 }
@@ -1101,12 +1167,12 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
   store_acc<D, DV>(scratch, dv, 1.f, 1.f, static_cast<bf16*>(a.dv), a.hkv, MAPS * hk, a.rows, first, nr);
 }
 
-// tab2[h][o]: the bias of every offset in units of log2, rows of a multiple of 4; clears amax and the
-// wide sums.
+// tab2[h][o]: the bias of every offset in units of log2, rows of a multiple of 4; clears amax and, where
+// something will be added to them, the 64-bit sums.
 __global__ void bias_expand_kernel(WinArgs a) {
   const int T3 = offsets(a.m), T3p = table_pitch(a.m), o = blockIdx.x * blockDim.x + threadIdx.x;
   if (o == 0) a.amax[blockIdx.y] = 0;
-  if (a.wide && o < T3) a.sums[(size_t)blockIdx.y * T3 + o] = 0;
+  if ((a.wide || __ldg(&a.tiles[a.T].x) > kDupMost) && o < T3) a.sums[(size_t)blockIdx.y * T3 + o] = 0;
   if (o < T3p) a.tab2[(size_t)blockIdx.y * T3p + o] = o < T3 ? bias2_at(a, blockIdx.y, o) : 0.f;
 }
 
@@ -1143,15 +1209,6 @@ cudaError_t bwd_any(const WinArgs& a, cudaStream_t st) {
                      : bwd<128, 1, false>(a, st);
 }
 
-// part[h][o]: the wide sums as floats; NaN where the head's dP or softmax had no finite bound.
-__global__ void bias_wide_kernel(WinArgs a) {
-  const int T3 = offsets(a.m), o = blockIdx.x * blockDim.x + threadIdx.x, h = blockIdx.y;
-  if (o >= T3) return;
-  const uint32_t amax = a.amax[h];
-  const double v = ldexp((double)(long long)a.sums[(size_t)h * T3 + o], -wide_bits(amax, a.N));
-  a.part[(size_t)h * T3 + o] = amax >= kTopDp ? __uint_as_float(0x7fc00000u) : (float)v;
-}
-
 }  // namespace
 
 cudaError_t window_fwd_mma(const WinArgs& a, cudaStream_t st) {
@@ -1169,10 +1226,7 @@ cudaError_t window_fwd_mma(const WinArgs& a, cudaStream_t st) {
 }
 
 cudaError_t window_bwd_mma(const WinArgs& a, cudaStream_t st) {
-  const cudaError_t e = bwd_any(a, st);
-  if (e == cudaSuccess && a.wide && a.dbias)
-    SSA_LAUNCH("bias_wide_kernel", bias_wide_kernel, dim3((offsets(a.m) + 255) / 256, a.hq), 256, 0, st, a);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return bwd_any(a, st);
 }
 
 }  // namespace ssa

@@ -48,8 +48,8 @@ __global__ void plan_rows_kernel(const int32_t* __restrict__ coords, int64_t N, 
 
 // One warp per cell: the most tokens that one of its m^3 voxels holds (m <= 16, 16-bit counters,
 // so no more than 65535; a larger count can only come from as many tokens in the cell, which is
-// then taken instead).  Flags the cell's tiles where it is above one and keeps the maximum of all
-// cells in tiles[T].x.
+// then taken instead).  Where it is above one the cell's tiles carry it; tiles[T].x: the maximum of
+// all cells.
 __global__ void plan_dup_kernel(int64_t N, int64_t W, int m, const int32_t* __restrict__ ptr,
                                 const int2* __restrict__ rows, int4* __restrict__ tiles, int64_t T) {
   __shared__ uint32_t count[4][2048];  // two voxels to a word
@@ -74,20 +74,36 @@ __global__ void plan_dup_kernel(int64_t N, int64_t W, int m, const int32_t* __re
     if (lane == 0) atomicMax(&tiles[T].x, most);
     if (most > 1) {
       const int64_t slot = a / kTile + c, nt = (b - a + kTile - 1) / kTile;
-      for (int64_t i = lane; i < nt; i += 32) tiles[slot + i].y |= kDupFlag;
+      for (int64_t i = lane; i < nt; i += 32) tiles[slot + i].y |= kDupFlag + kDupUnit * min(most, kDupTop);
     }
   }
 }
 
-// dst[h][o] = sum over parts of part[h][i][o], in a fixed order.  dst may be part i = 0.  Reads the parts
+// dst[h][o] = sum over parts of part[h][i][o], in a fixed order, and of the 64-bit sums where cells or
+// the whole gradient (a.wide) went there; NaN where the head's dP or softmax had no finite bound (the
+// parts are NaN then).  dst may be part i = 0.  Reads the parts
 // once out of L2: 10 us for 27 parts of 32 heads at an edge of 8 (11.7 MB), latency of the chain of adds.
-__global__ void bias_parts_kernel(const float* part, int parts, int T, float* dst, int pitch) {
-  const int o = blockIdx.x * blockDim.x + threadIdx.x;
-  if (o >= T) return;
-  const float* p = part + (size_t)blockIdx.y * parts * T + o;
+__global__ void bias_parts_kernel(WinArgs a, float* dst, int pitch) {
+  const int T3 = offsets(a.m), o = blockIdx.x * blockDim.x + threadIdx.x, h = blockIdx.y;
+  if (o >= T3) return;
+  const float* p = a.part + (size_t)h * a.parts * T3 + o;
   float s = 0.f;
-  for (int i = 0; i < parts; ++i) s += p[(size_t)i * T];
-  dst[(size_t)blockIdx.y * pitch + o] = s;
+  const int parts = a.wide ? 0 : a.parts;
+  int i = 0;
+  for (; i + 8 <= parts; i += 8) {
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = p[(size_t)(i + j) * T3];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += x[j];
+  }
+  for (; i < parts; ++i) s += p[(size_t)i * T3];
+  if (a.sums && (a.wide || __ldg(&a.tiles[a.T].x) > kDupMost)) {
+    const uint32_t amax = a.amax[h];
+    s += (float)ldexp((double)(long long)a.sums[(size_t)h * T3 + o], -wide_bits(amax, a.N));
+    if (amax >= kTopDp) s = __uint_as_float(0x7fc00000u);
+  }
+  dst[(size_t)h * pitch + o] = s;
 }
 
 // dbias[h][b] = sum of the offsets o with bucket b, in a fixed order; one warp per bucket and head:
@@ -282,8 +298,7 @@ cudaError_t window_param_grads(const WinArgs& a, cudaStream_t st) {
     // every offset its own bucket: the sums are the gradient
     float* sums = a.bucket ? a.part : a.dbias;
     const int pitch = a.bucket ? a.parts * T : T;
-    SSA_LAUNCH("bias_parts_kernel", bias_parts_kernel, dim3((T + 127) / 128, a.hq), 128, 0, st, a.part, a.parts, T,
-               sums, pitch);
+    SSA_LAUNCH("bias_parts_kernel", bias_parts_kernel, dim3((T + 127) / 128, a.hq), 128, 0, st, a, sums, pitch);
     if (a.bucket)
       SSA_LAUNCH("bias_buckets_kernel", bias_buckets_kernel, dim3((a.nb + 7) / 8, a.hq), 256, 0, st, a.part, pitch, T,
                  a.bucket, a.nb, a.dbias);

@@ -1,8 +1,10 @@
 """Attention inside the cells at the limits of its numbers."""
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_window import Problem, run_window, shell
+from spatial_sparse_attention_ssa_b200 import ssa
+from test_gpu_window import DT, Problem, check_all, dense, run_window, shell
 
 pytestmark = pytest.mark.gpu
 
@@ -20,3 +22,77 @@ def test_bias_gradient_scales_with_the_size_of_dp(m, shift):
     got = run_window(pr)["dbias"]
     assert bool(torch.isfinite(got).all())
     assert torch.equal(got.double(), want)
+
+
+def dbias64(pr, h):
+    """One head's dbias in fp64, cell by cell, and the root of the sum of all dS^2."""
+    e, g = 2 * pr.m - 1, h // (pr.hq // pr.hkv)
+    ref, power = torch.zeros(e ** 3, dtype=torch.float64, device="cuda"), 0.0
+    ptr = pr.win.ptr[:pr.win.count + 1].tolist()
+    for a, b in zip(ptr[:-1], ptr[1:]):
+        tok = pr.win.perm[a:b].long()
+        x = pr.coords[tok].long() % pr.m
+        code = (x[:, 0] * e + x[:, 1]) * e + x[:, 2]
+        k, v = pr.k[tok, g].double(), pr.v[tok, g].double()
+        for i in range(0, b - a, 1000):
+            t = tok[i:i + 1000]
+            off = code[i:i + 1000, None] - code[None] + (pr.m - 1) * (e * e + e + 1)
+            p = torch.softmax(pr.q[t, h].double() @ k.T / np.sqrt(pr.d) + pr.bias.table[h].double()[off], -1)
+            dp = pr.dout[t, h].double() @ v.T
+            ds = p * (dp - (p * dp).sum(-1, keepdim=True))
+            ref.index_add_(0, off.reshape(-1), ds.reshape(-1))
+            power += float((ds * ds).sum())
+    return ref, power ** 0.5
+
+
+@pytest.mark.parametrize("crowd,hq,hkv,m", [(2000, 128, 2, 4), (5000, 128, 2, 4), (20000, 4, 2, 4), (700, 128, 2, 13), (4097, 2, 1, 3)])
+def test_bias_gradient_of_a_crowded_voxel_keeps_fp32_precision(crowd, hq, hkv, m):
+    """One voxel with thousands of tokens beside ordinary cells.  Error of dbias in the 2-norm against
+    that of all dS (a crowded voxel's own offsets nearly cancel).  Per dS, as random numbers: exponential
+    2^-22, score, lse2 and their difference 2^-22 ln 2 each below 8 and twice that below 16 (lse2 of
+    20000 keys), over sqrt 3: 7e-7; dP 2 x 2^-23.  Per row: the sums of up to n / 4 terms per lane are off by
+    2^-25 sqrt(n / 12), 1.2e-6, common to a row, whose dS sum to zero but for the offsets that the crowd does
+    not hold.  Together below 3e-6, which the fixed point must not add to."""
+    coords, cu = shell(73, 600, r=9)
+    coords = np.concatenate([coords, np.repeat(coords[100:101], crowd, 0)])
+    coords = coords[np.random.default_rng(74).permutation(len(coords))]
+    pr = Problem(coords, np.array([0, len(coords)], np.int32), m, hq, hkv, 32, torch.bfloat16, seed=75, bias="offset")
+    got = ssa.ssa_window_backward(pr.p, pr.plan, pr.q, pr.k, pr.v, pr.dout, bias=pr.bias)[3]
+    again = ssa.ssa_window_backward(pr.p, pr.plan, pr.q, pr.k, pr.v, pr.dout, bias=pr.bias)[3]
+    assert torch.equal(got, again) and ssa.device_status() == 0
+    for h in (0, hq - 1):
+        ref, power = dbias64(pr, h)
+        assert float((got[h].double() - ref).norm()) < 3e-6 * power
+
+
+def test_bias_gradient_of_many_heads_keeps_fp32_precision():
+    """512 heads leave a head one CTA, which adds the dS of all of its 125000 rows.  The tolerance is that of
+    the test of many rows in test_gpu_window.py: below 7e-7 by the arithmetic of one dS, cells of 125."""
+    coords, cu = dense(76, 50 ** 3, 50)
+    pr = Problem(coords, cu, 5, 2, 2, 32, torch.bfloat16, seed=77)
+    gen = torch.Generator(device="cuda").manual_seed(78)
+    f = lambda *x: torch.randn(*x, generator=gen, device="cuda")  # noqa: E731
+    pr.hq, pr.p = 512, ssa.make_window_params(512, 2, 32, torch.bfloat16)
+    pr.q, pr.dout = (f(50 ** 3, 512, 32).bfloat16() for _ in range(2))
+    pr.bias = ssa.WindowBias(0.5 * f(512, 729))
+    got = ssa.ssa_window_backward(pr.p, pr.plan, pr.q, pr.k, pr.v, pr.dout, bias=pr.bias)[3]
+    for h in (0, 300):
+        ref, _ = dbias64(pr, h)
+        assert float((got[h].double() - ref).norm() / ref.norm()) < 7e-7
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m", [3, 13])
+def test_plan_counts_the_tokens_of_a_voxel_per_cell(m, dtype):
+    """Cells with one, two and thirty tokens in a voxel side by side: the plan's counts, and results."""
+    coords, _ = shell(78, 250, r=8)
+    coords = np.concatenate([coords, coords[:40], np.repeat(coords[200:201], 29, 0)])
+    pr = Problem(coords, np.array([0, len(coords)], np.int32), m, 2, 1, 32, DT[dtype], seed=79, bias="offset")
+    ids = pr.win.id.cpu().numpy()
+    tiles = pr.plan.tiles.cpu().numpy()[:-1]
+    perm = pr.win.perm.cpu().numpy()
+    for t in tiles[(tiles[:, 1] & 65535) > 0]:
+        c = coords[ids == ids[perm[t[0]]]]
+        most = int(np.unique(c, axis=0, return_counts=True)[1].max())
+        assert t[1] >> 17 == (most if most > 1 else 0) and (t[1] >> 16 & 1) == (most > 1)
+    check_all(run_window(pr), pr.ref_window())
