@@ -25,6 +25,16 @@ constexpr int kDupUnit = 131072;        // and from here on: the most tokens of 
 constexpr int kDupTop = 16383;
 constexpr int kDupMost = 2048;  // more in one voxel: the cell's bias gradient goes to the 64-bit sums (bf16)
 
+// Dynamic shared memory of a CTA at most, beside what kernels declare; and the bound that a kernel is
+// given before its first launch above 48 KB.  The same for every call: the size of a launch depends on its
+// plan, and a bound that follows it would be lowered by another host thread between this one's two calls.
+constexpr size_t kSmemMost = 226 * 1024;
+template <typename K>
+cudaError_t need_smem(K kern, size_t smem) {
+  return smem > 47 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost)
+                          : cudaSuccess;
+}
+
 // Offsets of a window of edge m, and the number of the offset 0.
 __host__ __device__ inline int offsets(int m) { return (2 * m - 1) * (2 * m - 1) * (2 * m - 1); }
 // Floats from one head's table of offsets to the next in WinArgs::tab2.

@@ -28,7 +28,6 @@ using bf16 = __nv_bfloat16;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kChunk = 64;
 constexpr float kSlack = 8.f;
-constexpr size_t kSmemMost = 226 * 1024;  // dynamic shared memory of a CTA, beside the barriers
 
 __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -896,12 +895,6 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
 int grid_x(int64_t heads, int64_t T) {
   const int64_t waves = max((int64_t)1, min((int64_t)6, heads * T / (16 * kSms)));
   return (int)max((int64_t)1, min(T, waves * kSms / heads));
-}
-
-template <typename K>
-cudaError_t need_smem(K kern, size_t smem) {
-  return smem > 47 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
-                          : cudaSuccess;
 }
 
 template <int D, int MAPS, bool BIAS, int MODE>

@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kThreads) window_dkv_kernel(WinArgs a) {
 
 template <typename K>
 cudaError_t go(const char* name, K kern, dim3 grid, size_t smem, const WinArgs& a, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = need_smem(kern, smem);
   if (e != cudaSuccess) return e;
   SSA_LAUNCH(name, kern, grid, kThreads, smem, st, a);
   return cudaGetLastError();

@@ -1,4 +1,6 @@
 """Attention inside the cells at the limits of its numbers."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -96,3 +98,38 @@ def test_plan_counts_the_tokens_of_a_voxel_per_cell(m, dtype):
         most = int(np.unique(c, axis=0, return_counts=True)[1].max())
         assert t[1] >> 17 == (most if most > 1 else 0) and (t[1] >> 16 & 1) == (most > 1)
     check_all(run_window(pr), pr.ref_window())
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 32), ("bf16", 64)])
+def test_host_threads_with_plans_of_different_sizes(dtype, d):
+    """Calls that overlap on the host, of plans that need different shared memory, give what each gives
+    alone."""
+    prs = []
+    for seed, m, hkv in ((81, 3, 4), (82, 12, 2), (83, 6, 4), (84, 12, 1)):
+        coords, cu = shell(seed, 300, r=9)
+        prs.append(Problem(coords, cu, m, 4, hkv, d, DT[dtype], seed=seed, bias="offset"))
+    alone = [run_window(pr) for pr in prs]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(pr, want):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                grads = tuple(torch.empty_like(want[n]) for n in ("dq", "dk", "dv"))
+                db, out = torch.empty_like(want["dbias"]), torch.empty_like(want["out"])
+                ws = torch.empty(pr.plan.workspace_size(ssa.OP_WINDOW_BACKWARD, pr.p), dtype=torch.uint8, device="cuda")
+                for _ in range(3000):
+                    ssa.ssa_window_forward(pr.p, pr.plan, pr.q, pr.k, pr.v, bias=pr.bias, out=out)
+                    ssa.ssa_window_backward(pr.p, pr.plan, pr.q, pr.k, pr.v, pr.dout, bias=pr.bias, grads=grads,
+                                            dbias=db, workspace=ws)
+                torch.cuda.current_stream().synchronize()
+                for x, n in zip((out, *grads, db), ("out", "dq", "dk", "dv", "dbias")):
+                    assert torch.equal(x, want[n]), n
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=a) for a in zip(prs, alone)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
