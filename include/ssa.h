@@ -446,7 +446,8 @@ typedef struct ssa_act8 {
 
 /*
  * ssa_window_forward -- p_ij = softmax over the tokens j of i's cell of scale <q_i, k_j> +
- * bias; out_i = sum_j p_ij v_j.
+ * bias; out_i = sum_j p_ij v_j.  A row whose scores are all minus infinity though the bias bars not
+ * every key (an infinity in q or k, a product past fp32) is NaN, as its softmax is.
  *   q, out [N, hq, d], k, v [N, hkv, d] in dtype, 16-byte aligned; bias NULL: none
  *   lse    fp32 [N, hq] natural-log normalisers, or NULL
  */
@@ -458,8 +459,9 @@ SSA_API ssa_status ssa_window_forward(const ssa_window_params* p, const ssa_win_
  * ssa_window_backward -- gradients of sum(dout * out): dq [N, hq, d], dk, dv [N, hkv, d] in
  * dtype (each summed in fp32 and rounded once), dbias fp32 [hq, nb] (NULL: not wanted, or
  * no bias); all written.  It recomputes the probabilities and needs nothing the forward left.
- *          A NaN or an infinity in the inputs of a head, or a |<dout_i, v_j>| of 2^127 or more,
- *          makes all of its dbias NaN in SSA_DTYPE_BF16; dq, dk, dv show it in its own cell only.
+ *          Where a NaN or an infinity in the inputs of a head reaches a weight or <dout_i, v_j>, and
+ *          where |<dout_i, v_j>| is 2^127 or more, all of its dbias is NaN in SSA_DTYPE_BF16; dq, dk,
+ *          dv show it in its own cell only.
  *   act8   NULL, or an array of three: Q, K, V from 8-bit checkpoints (q, k, v are then
  *          ignored); the gradients are those at the values the codes hold, in dtype.  In
  *          SSA_DTYPE_BF16 the workspace holds them as bf16 during the call

@@ -101,5 +101,16 @@ __device__ __forceinline__ float bias2_at(const WinArgs& a, int h, int off) {
   return x <= kBar ? kNegInf : x * kLog2e;
 }
 
+// Whether the bias leaves the row with code `code` a key: looked at by `step` lanes from key lo + `at` on.
+// For rows whose sum is 0: with a key left their scores are minus infinity by themselves (an infinity in
+// q or k, or a product past fp32), and their softmax is NaN, not a row with nothing left.
+__device__ __forceinline__ bool key_left(const WinArgs& a, int h, int code, int lo, int hi, int at, int step) {
+  bool left = false;
+#pragma unroll 1
+  for (int j = lo + at; j < hi && !left; j += step)
+    left = bias2_at(a, h, code - __ldg(&a.rows[j].y) + center(a.m)) > kNegInf;
+  return left;
+}
+
 }  // namespace win
 }  // namespace ssa

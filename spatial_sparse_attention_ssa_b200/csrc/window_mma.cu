@@ -817,12 +817,32 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
         if (lane == 0) tc::mbar_arrive(done);
       }
       if (!on || !ok) continue;
+      if constexpr (MODE != kDq) {
+        bool none = false;
+#pragma unroll
+        for (int u = 0; u < MAPS; ++u)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            l[u][i] = quad_sum(l[u][i]);
+            none |= l[u][i] == 0.f;
+          }
+        if (__any_sync(kFull, none)) {  // rows that sum to 0: NaN where the bias did not bar all keys
+#pragma unroll
+          for (int u = 0; u < MAPS; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              bool left = l[u][i] == 0.f;
+              if constexpr (BIAS)
+                left = left && key_left(a, h, (i ? ci8 : ci) / 4 - c0, lo, hi, t4, 4);
+              if (quad_max(left ? 1.f : 0.f) > 0.f) l[u][i] = __uint_as_float(0x7fc00000u);
+            }
+        }
+      }
       if constexpr (MODE == kForward) {
         float f[2] = {1.f, 1.f};
         if constexpr (MAPS == 1) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            l[0][i] = quad_sum(l[0][i]);
             f[i] = safe_inv(l[0][i]);
             if (a.lse && t4 == 0 && g + 8 * i < nr)
               a.lse[(size_t)__ldg(&a.rows[first + g + 8 * i].x) * a.hq + h] =
@@ -832,7 +852,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
         if constexpr (MAPS == 2) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float f0 = safe_inv(quad_sum(l[0][i])), f1 = lam * safe_inv(quad_sum(l[MAPS - 1][i]));
+            const float f0 = safe_inv(l[0][i]), f1 = lam * safe_inv(l[MAPS - 1][i]);
 #pragma unroll
             for (int e = 0; e < DV / 8; ++e)
 #pragma unroll
@@ -846,7 +866,6 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
         for (int u = 0; u < MAPS; ++u)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            l[u][i] = quad_sum(l[u][i]);
             dd[u][i] = quad_sum(dd[u][i]);
             if (t4 == 0 && g + 8 * i < nr) {
               const size_t at = (size_t)(MAPS * h + u) * a.N + first + g + 8 * i;

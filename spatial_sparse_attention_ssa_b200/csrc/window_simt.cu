@@ -180,6 +180,25 @@ __device__ __forceinline__ void scores(const WinArgs& a, int h, const float* sm,
     }
 }
 
+// Sums of 0 are made NaN in rows that the bias leaves a key (key_left).  By whole warps, whose halves
+// hold rows of their own.
+template <int MAPS>
+__device__ __forceinline__ void check_sums(const WinArgs& a, int h, const int* codes, int lo, int hi, float (*l)[2]) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  bool none = false;
+#pragma unroll
+  for (int u = 0; u < MAPS; ++u) none |= l[u][0] == 0.f || l[u][1] == 0.f;
+  if (!__any_sync(0xffffffffu, none)) return;
+#pragma unroll
+  for (int u = 0; u < MAPS; ++u)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      bool left = l[u][i] == 0.f;
+      if (a.table) left = left && key_left(a, h, codes[kChunk + ty + 8 * i], lo, hi, tx, 16);
+      if (row_max(left ? 1.f : 0.f) > 0.f) l[u][i] = __uint_as_float(0x7fc00000u);
+    }
+}
+
 template <typename E, typename T, int D, int MAPS>
 __global__ void __launch_bounds__(kThreads) window_fwd_kernel(WinArgs a) {
   using L = Lay<D, MAPS>;
@@ -241,6 +260,7 @@ __global__ void __launch_bounds__(kThreads) window_fwd_kernel(WinArgs a) {
             }
         }
         if (pass == 0) continue;
+        if (k0 == lo) check_sums<MAPS>(a, h, codes, lo, hi, l);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -339,6 +359,7 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(WinArgs a) {
             }
         }
         if (pass == 0) continue;
+        if (k0 == lo) check_sums<MAPS>(a, h, codes, lo, hi, l);
 #pragma unroll
         for (int u = 0; u < MAPS; ++u)
 #pragma unroll

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from spatial_sparse_attention_ssa_b200 import ssa
-from test_gpu_window import DT, Problem, check_all, dense, run_window, shell
+from test_gpu_window import DT, Problem, check_all, dense, run_diff, run_window, shell
 
 pytestmark = pytest.mark.gpu
 
@@ -133,3 +133,55 @@ def test_host_threads_with_plans_of_different_sizes(dtype, d):
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("op", ["window", "bias", "diff"])
+@pytest.mark.parametrize("d", [32, 64])
+def test_a_row_whose_scores_all_overflow_is_nan(d, op, dtype):
+    """One infinite component of q makes every score of a row minus infinity: a softmax of NaN, not a row
+    with nothing left.  Lone tokens, and a cell of 70 where every key is negative there."""
+    n = 80
+    coords = np.stack([np.arange(n) * 9, np.zeros(n), np.zeros(n)], 1).astype(np.int32)
+    coords[10:] = dense(91, 70, 8)[0] + np.array([8 * 100, 0, 0])
+    pr = Problem(coords, np.array([0, n], np.int32), 8, 4, 2, d, DT[dtype], seed=92, bias="offset" if op == "bias" else None)
+    run = run_diff if op == "diff" else run_window
+    pr.k[..., 3] = -pr.k[..., 3].abs() - 0.1
+    clean = run(pr)
+    for tok in (4, 30):
+        pr.q[tok, :, 3] = float("inf")
+    dirty = run(pr)
+    other = (pr.win.id != pr.win.id[4]) & (pr.win.id != pr.win.id[30])
+    for x in ("out", "dq", "dk", "dv"):
+        assert torch.equal(clean[x][other], dirty[x][other]), x
+        for tok in (4, 30):
+            assert bool(torch.isnan(dirty[x][tok]).all()), x
+    rest = torch.arange(n, device="cuda") >= 10
+    rest[30] = False
+    assert torch.equal(clean["out"][rest], dirty["out"][rest])       # other rows of the cell: their own scores
+    if op == "bias" and dtype == "bf16":
+        assert bool(torch.isnan(dirty["dbias"]).all())
+    if op != "diff":
+        assert bool(torch.isnan(dirty["lse"][[4, 30]]).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_what_the_bias_bars_stays_barred_beside_scores_that_overflow(dtype):
+    """Barred keys count for nothing: a row with all keys barred gives zeros, and a row whose one key that
+    is left overflows gives NaN."""
+    coords, cu = dense(93, 100, 5)
+    pr = Problem(coords, cu, 5, 2, 2, 32, DT[dtype], seed=94, bias="offset")
+    pr.k[..., 3] = -pr.k[..., 3].abs() - 0.1
+    pr.bias.table[0] = float("-inf")
+    pr.bias.table[1] = float("-inf")
+    pr.bias.table[1, 364] = 0.5            # the offset 0: every token sees itself alone
+    clean = run_window(pr)
+    assert float(clean["out"][:, 0].abs().max()) == 0 and torch.equal(clean["out"][:, 1], pr.v[:, 1])
+    pr.q[7, 1, 3] = float("inf")
+    dirty = run_window(pr)
+    assert bool(torch.isnan(dirty["out"][7, 1]).all()) and bool(torch.isnan(dirty["lse"][7, 1]))
+    keep = torch.arange(100, device="cuda") != 7
+    assert torch.equal(dirty["out"][:, 0], clean["out"][:, 0]) and torch.equal(dirty["out"][keep], clean["out"][keep])
+    assert float(dirty["dq"][:, 0].abs().max()) == 0 and bool(torch.isnan(dirty["dq"][7, 1]).any())
+    assert bool(torch.isneginf(dirty["lse"][:, 0]).all())
+    assert float(dirty["dbias"][0].abs().max()) == 0
