@@ -775,7 +775,7 @@ ssa::WinArgs window_args(const ssa_window_params* p, const ssa_win_plan* plan, i
   return a;
 }
 
-// Workspace of the backward: lse2 and D per query head and row, partial bias gradients.
+// Workspace of the backward: lse2, D and lse2's rest per query head and row, partial bias gradients.
 size_t carve_window(void* base, const ssa_window_params* p, const ssa_win_plan* plan, int maps, bool act8,
                     ssa::WinArgs* a) {
   Carver c(base);
@@ -785,6 +785,8 @@ size_t carve_window(void* base, const ssa_window_params* p, const ssa_win_plan* 
   const int parts = wide ? 1 : ssa::window_parts(p->hq, T);
   float* lse2 = c.take<float>((size_t)p->hq * plan->n);
   float* D = c.take<float>((size_t)p->hq * plan->n);
+  float* rest = c.take<float>((size_t)p->hq * plan->n);
+  int* far = c.take<int>(1);
   const size_t tab = maps == 1 && plan->m > 0 ? (size_t)p->hq * e * e * e : 0;
   float* part = c.take<float>(tab * parts);
   float* tab2 = c.take<float>(tab ? tab + 3 * (size_t)p->hq : 0);  // rows of a multiple of 4
@@ -803,6 +805,8 @@ size_t carve_window(void* base, const ssa_window_params* p, const ssa_win_plan* 
     a->v16 = v16;
     a->lse2 = lse2;
     a->D = D;
+    a->rest = rest;
+    a->far = far;
     a->part = part;
     a->parts = parts;
     a->tab2 = tab2;

@@ -174,6 +174,8 @@ struct WinArgs {
   void *dq, *dk, *dv;
   float *dbias, *dlam;
   float *lse2, *D;  // [hq][N] in row order
+  float* rest;      // [hq][N] what lse2 rounded away, of rows far from zero only
+  int* far;         // whether there are any
   float* part;      // [hq][parts][offsets] partial bias gradients
   int parts;
   float* tab2;      // [hq][offsets] the bias by offset, in units of log2

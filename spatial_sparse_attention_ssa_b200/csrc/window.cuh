@@ -8,7 +8,9 @@
 //
 // Scores are held in units of log2: s2 = (scale <q, k> + bias) log2(e), p = 2^(s2 - max) / sum.
 // The backward keeps two numbers per row and map between its kernels: lse2 = max + log2(sum)
-// (plus infinity for a row with nothing left, so that every p is 0) and D = sum_j p_j dP_j.
+// (plus infinity for a row with nothing left, so that every p is 0) and D = sum_j p_j dP_j.  Where
+// lse2 is so large that its rounding shows in the weights (kFarScore), what it rounded away is kept
+// too; far from zero all of log2(sum) is lost in it, and the weights of a row would sum to its keys.
 // D comes from the recomputed p and dP, not from the rounded output, so the fp32 gradients of
 // the bias and of lambda do not carry a rounding to bf16; the forward has to leave nothing.
 #pragma once
@@ -68,6 +70,24 @@ __device__ __forceinline__ float rescale(float old, float now) { return old == k
 // 1 / sum, 0 for a row with nothing left; a NaN sum stays NaN.
 __device__ __forceinline__ float safe_inv(float l) { return l == 0.f ? 0.f : 1.f / l; }
 __device__ __forceinline__ float lse2_of(float m, float l) { return l == 0.f ? kPosInf : m + log2f(l); }
+
+// Rows whose |lse2| is at least this: rounding it is off by 2^-15 and more, and the rest goes to a.rest;
+// *a.far (bf16) tells the kernels after it to look there.
+constexpr float kFarScore = 1024.f;
+__device__ __forceinline__ bool is_far(float lse2) { return fabsf(lse2) >= kFarScore && fabsf(lse2) < kPosInf; }
+// Keeps lse2 of the row `at`: maximum m, sum l.
+__device__ __forceinline__ void store_lse2(const WinArgs& a, size_t at, float m, float l) {
+  const float lse2 = lse2_of(m, l);
+  a.lse2[at] = lse2;
+  if (is_far(lse2)) {
+    a.rest[at] = log2f(l) - (lse2 - m);  // exact: |m| is the larger
+    *a.far = 1;
+  }
+}
+// What weights 2^(s - lse2) of the row `at` have to be multiplied by.
+__device__ __forceinline__ float far_factor(const WinArgs& a, size_t at, float lse2) {
+  return is_far(lse2) ? ex2(-a.rest[at]) : 1.f;
+}
 
 // exp(<a, b>) pair of one head: lambda = e1 - e2 + init, from lam [4, heads, d].  Called by
 // whole warps.

@@ -284,13 +284,13 @@ __device__ __forceinline__ void red_shared(uint32_t at, int x) {
 // of their cell holds.  Both stay below 2^13: before they pass it the CTA's sums go to its partial
 // gradient and start again, so the unit is M 2^-33 however many rows a CTA has.  An item of one crowded
 // cell can pass that alone: up to kDupMost tokens in a voxel the unit of its own few rows is M 2^-32
-// where dS is some M 2^-11; cells that are more crowded (kFar) take the 64-bit sums below.  A NaN or an infinity in dP or in a softmax makes the
-// head's gradient NaN, and so does an M from 2^127 on (dP - D could overflow); below, 2^s and 2^-s are
-// normal numbers.
-constexpr int kAdds = 8191;    // at most between two flushes, but for a lone item
-constexpr int kFar = 1 << 16;  // items[].y: a cell for the 64-bit sums
+// where dS is some M 2^-11; cells that are more crowded (kCrowd) take the 64-bit sums below.  A NaN or an
+// infinity in dP or in a softmax makes the head's gradient NaN, and so does an M from 2^127 on (dP - D
+// could overflow); below, 2^s and 2^-s are normal numbers.
+constexpr int kAdds = 8191;      // at most between two flushes, but for a lone item
+constexpr int kCrowd = 1 << 16;  // items[].y: a cell for the 64-bit sums
 struct Limbs {
-  float s, k;            // 2^s, 2^k
+  float s[2], k;         // 2^s for the rows g, g + 8 (times far_factor, see store_lse2), 2^k
   double unit, unit_lo;  // 2^-s, 2^-s-k
   __device__ __forceinline__ void set(const WinArgs& a, int h, int rows, int adds) {
     if (adds <= kAdds) rows = adds = kAdds;
@@ -300,19 +300,19 @@ struct Limbs {
     int sb = min(29 - rb - 1 - e, 20 - e);                      // |dS 2^s| < 2^22: see add()
     sb = max(-126, min(126, sb));
     const int kbits = max(0, min(21, 31 - ab));
-    s = __uint_as_float(bits >= kTopDp ? 0x7fc00000u : (uint32_t)(sb + 127) << 23);
+    s[0] = s[1] = __uint_as_float(bits >= kTopDp ? 0x7fc00000u : (uint32_t)(sb + 127) << 23);
     k = (float)(1 << kbits);
-    unit = (double)(1.f / s);
+    unit = (double)(1.f / s[0]);
     unit_lo = unit * (double)(1.f / k);
   }
   __device__ __forceinline__ float value(int hi, int lo) const {
     return (float)((double)hi * unit + (double)lo * unit_lo);
   }
   // x 2^s to the nearest whole number by adding 1.5 2^23 (|x 2^s| < 2^22), and the rest
-  __device__ __forceinline__ void add(uint32_t hi, uint32_t lo, float x) const {
+  __device__ __forceinline__ void add(uint32_t hi, uint32_t lo, float x, int row) const {
     constexpr float kMagic = 12582912.f;
-    const float a = fmaf(x, s, kMagic);
-    const float r = fmaf(x, s, kMagic - a);
+    const float a = fmaf(x, s[row], kMagic);
+    const float r = fmaf(x, s[row], kMagic - a);
     const float b = fmaf(r, k, kMagic);
     red_shared(hi, __float_as_int(a) - __float_as_int(kMagic));
     red_shared(lo, __float_as_int(b) - __float_as_int(kMagic));
@@ -324,20 +324,22 @@ struct Limbs {
 struct Wide {
   char* sums;  // of the head
   double s;
+  float c[2];  // far_factor of the rows g, g + 8
   __device__ __forceinline__ void set(const WinArgs& a, int h) {
+    c[0] = c[1] = 1.f;
     sums = reinterpret_cast<char*>(a.sums + (size_t)h * offsets(a.m));
     s = __longlong_as_double((long long)(wide_bits(__ldg(a.amax + h), a.N) + 1023) << 52);
   }
-  __device__ __forceinline__ void add(int at, float x) const {  // at: four times the offset
-    add_ll(at, __double2ll_rn((double)x * s));
-  }
+  __device__ __forceinline__ long long whole(float x, int row) const { return __double2ll_rn((double)(x * c[row]) * s); }
+  // at: four times the offset
+  __device__ __forceinline__ void add(int at, float x, int row) const { add_ll(at, whole(x, row)); }
   __device__ __forceinline__ void add_ll(int at, long long x) const {
     atomicAdd(reinterpret_cast<unsigned long long*>(sums + 2 * (int64_t)at), (unsigned long long)x);
   }
 };
 
-// add(4 (code of row - code of key), dS) for a fragment tile of 16 rows and 32 positions.  Rows and
-// positions without a token have dS 0 and the codes of others.
+// add(4 (code of row - code of key), dS, 0 for the row g, 1 for g + 8) for a fragment tile of 16 rows and 32
+// positions.  Rows and positions without a token have dS 0 and the codes of others.
 template <typename F>
 __device__ __forceinline__ void add_bias_grad(const F& add, float (*ds)[4], const int* codes, int ci, int ci8) {
   const int t = threadIdx.x & 3;
@@ -345,7 +347,7 @@ __device__ __forceinline__ void add_bias_grad(const F& add, float (*ds)[4], cons
   for (int j = 0; j < 4; ++j) {
     const int2 cj = *reinterpret_cast<const int2*>(codes + 8 * j + 2 * t);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) add((x & 2 ? ci8 : ci) - (x & 1 ? cj.y : cj.x), ds[j][x]);
+    for (int x = 0; x < 4; ++x) add((x & 2 ? ci8 : ci) - (x & 1 ? cj.y : cj.x), ds[j][x], x >> 1);
   }
 }
 
@@ -358,19 +360,19 @@ __device__ __noinline__ void add_crowded(Wide wide, const float (*v)[4], const i
   for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int x = 0; x < 4; ++x) ds[j][x] = v[j][x];
-  const int lane = threadIdx.x & 31, c = codes[lane];
-  const int c_first = __shfl_sync(kFull, c, 0), ci_first = __shfl_sync(kFull, ci, 0);  // by every lane
-  if (__all_sync(kFull, c == c_first && ci == ci_first && ci8 == ci_first)) {
+  const int lane = threadIdx.x & 31, code = codes[lane];
+  const int code0 = __shfl_sync(kFull, code, 0), ci0 = __shfl_sync(kFull, ci, 0);  // by every lane
+  if (__all_sync(kFull, code == code0 && ci == ci0 && ci8 == ci0)) {
     long long sum = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) sum += __double2ll_rn((double)ds[j][x] * wide.s);
+      for (int x = 0; x < 4; ++x) sum += wide.whole(ds[j][x], x >> 1);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-    if (lane == 0) wide.add_ll(ci - c, sum);
+    if (lane == 0) wide.add_ll(ci - code, sum);
   } else {
-    add_bias_grad([&](int at, float x) { wide.add(at, x); }, ds, codes, ci, ci8);
+    add_bias_grad([&](int at, float x, int row) { wide.add(at, x, row); }, ds, codes, ci, ci8);
   }
   __syncwarp();
 }
@@ -519,8 +521,8 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
         x.y = item_tiles(x, item_size);
         int take = 32;  // slots of these 32
         if (grad && TAB != 3) {
-          const bool far = dup > kDupMost;
-          const int r = x.y > 0 && !far ? min(item_size * kTile, x.w - x.x) : 0;
+          const bool crowd = dup > kDupMost;
+          const int r = x.y > 0 && !crowd ? min(item_size * kTile, x.w - x.x) : 0;
           const int all = __reduce_add_sync(kFull, r * dup);
           if (adds + all <= kAdds) {
             adds += all;
@@ -537,7 +539,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
             if (take > 0) adds = __shfl_sync(kFull, sum, take - 1);
           }
           rows += __reduce_add_sync(kFull, lane < take ? r : 0);
-          if (x.y > 0 && far) x.y |= kFar;
+          if (x.y > 0 && crowd) x.y |= kCrowd;
         }
         const bool mine = lane < take && x.y > 0;
         const unsigned some = __ballot_sync(kFull, mine);
@@ -555,7 +557,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
     if (grad && TAB != 3) {
       for (int i = pairs - 1; i >= 0; --i) {
         fx.set(a, h0 + i, n_rows, n_adds);
-        (i ? s2[1] : s2[0]) = fx.s;
+        (i ? s2[1] : s2[0]) = fx.s[0];
       }
     }
     if (warp >= NW) {
@@ -615,8 +617,8 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
     }
     for (int ii = 0; ii < count && ok && warp < NW; ++ii) {
       int4 item = items[ii];
-      const bool far = item.y & kFar;
-      item.y &= kFar - 1;
+      const bool crowd = item.y & kCrowd, far = MODE == kDq && *a.far;
+      item.y &= kCrowd - 1;
       const int lo = item.z, hi = item.w;
       int mine = warp - rot;
       if (mine < 0) mine += NW;
@@ -628,12 +630,6 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
       const int h = h0 + pair;
       const float lam = pair ? lams[1] : lams[0];
       uint32_t top = 0;
-      if (grad && on) {
-        if (TAB == 3)
-          wide.set(a, h);
-        else
-          fx.s = pair ? s2[1] : s2[0];
-      }
       constexpr int NACC = MODE == kStats ? 1 : MODE == kForward ? MAPS * DV / 8 : DV / 8;
       float m[MAPS][2], l[MAPS][2], dd[MAPS][2], acc[NACC][4];
       uint32_t q[S::held ? DV / 16 : 1][4], o[S::held ? DV / 16 : 1][4];
@@ -663,6 +659,20 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
               dd[u][i] = g + 8 * i < nr ? a.D[at] : 0.f;
             }
           }
+        if (grad) {
+          if (TAB == 3)
+            wide.set(a, h);
+          else
+            fx.s[0] = fx.s[1] = pair ? s2[1] : s2[0];
+          if (far) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float c = far_factor(a, (size_t)h * a.N + first + min(g + 8 * i, nr - 1), m[0][i]);
+              wide.c[i] = c;
+              fx.s[i] *= c;
+            }
+          }
+        }
 #pragma unroll
         for (int e = 0; e < NACC; ++e) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
       }
@@ -726,17 +736,20 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
                 if (grad) {
                   const uint32_t to = tc::smem_u32(limbs) + 8 * pair * T3;
                   if constexpr (TAB == 3) {
-                    add_bias_grad([&](int at, float x) { wide.add(at, x); }, s[0], hc, ci, ci8);
-                  } else if (far) {
+                    add_bias_grad([&](int at, float x, int row) { wide.add(at, x, row); }, s[0], hc, ci, ci8);
+                  } else if (crowd) {
                     float ds[4][4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
 #pragma unroll
                       for (int x = 0; x < 4; ++x) ds[j][x] = s[0][j][x];
                     wide.set(a, h);
+                    const float one = pair ? s2[1] : s2[0];
+                    wide.c[0] = fx.s[0] / one, wide.c[1] = fx.s[1] / one;
                     add_crowded(wide, ds, hc, ci, ci8);
                   } else {
-                    add_bias_grad([&](int at, float x) { fx.add(to + at, to + at + 4 * T3, x); }, s[0], hc, ci, ci8);
+                    add_bias_grad([&](int at, float x, int row) { fx.add(to + at, to + at + 4 * T3, x, row); }, s[0], hc,
+                                  ci, ci8);
                   }
                 }
               }
@@ -869,7 +882,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
             dd[u][i] = quad_sum(dd[u][i]);
             if (t4 == 0 && g + 8 * i < nr) {
               const size_t at = (size_t)(MAPS * h + u) * a.N + first + g + 8 * i;
-              a.lse2[at] = lse2_of(m[u][i], l[u][i]);
+              store_lse2(a, at, m[u][i], l[u][i]);
               a.D[at] = dd[u][i] * safe_inv(l[u][i]);
               if (!(l[u][i] >= 0.f)) top = 0x7fffffffu;
             }
@@ -879,6 +892,16 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
         else
           tops[0] = max(tops[0], top);
       } else {
+        if (far) {
+#pragma unroll
+          for (int u = 0; u < MAPS; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float c = far_factor(a, (size_t)(MAPS * h + u) * a.N + first + min(g + 8 * i, nr - 1), m[u][i]);
+#pragma unroll
+              for (int e = u * D / 8; e < (u + 1) * D / 8; ++e) acc[e][2 * i] *= c, acc[e][2 * i + 1] *= c;
+            }
+        }
         store_acc<D, DV>(scratch, acc, a.scale, a.scale, static_cast<bf16*>(a.dq), a.hq, MAPS * h, a.rows, first, nr);
       }
     }
@@ -985,8 +1008,10 @@ struct DkvShape {
 };
 
 // TAB: 0 no bias, 1 tables staged in shared memory, 2 read in global memory (the largest edges).
-template <int D, int MAPS, int TAB>
-__global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window_dkv_mma_kernel(WinArgs a) {
+// FAR: weights of rows far from zero (kFarScore) are set right.  A body of its own, taken once per CTA,
+// because tests inside the steps cost 9% (131072 tokens: 1001 -> 1088 us; differential 1044 -> 1176).
+template <int D, int MAPS, int TAB, bool FAR>
+__device__ __forceinline__ void dkv_body(const WinArgs& a) {
   using S = DkvShape<D, MAPS>;
   constexpr int DV = S::DV, NTH = 32 * kDkvWarps;
   constexpr bool BIAS = TAB != 0;
@@ -1148,7 +1173,12 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               // columns past the last query: lse2 is plus infinity, so p is 0, and their dO is 0
-              const float p = ex2(fmaf(sc[j][x], mul, b[x]) - (x & 1 ? L.y : L.x));
+              float p = ex2(fmaf(sc[j][x], mul, b[x]) - (x & 1 ? L.y : L.x));
+              if constexpr (FAR) {
+                const size_t at = (size_t)(MAPS * h + u) * a.N + k0 + min(c + (x & 1), n - 1);
+                p *= far_factor(a, at, x & 1 ? L.y : L.x);
+                if (p > 1.f) p = 1.f;  // a score may round to one side here, to the other where lse2 was taken
+              }
               const float w = u ? -lam * p : p;
               pv[j][x] = u ? pv[j][x] + w : w;
               sc[j][x] = w * (dp[j][x] - (x & 1 ? Dq.y : Dq.x));
@@ -1179,11 +1209,18 @@ __global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window
   store_acc<D, DV>(scratch, dv, 1.f, 1.f, static_cast<bf16*>(a.dv), a.hkv, MAPS * hk, a.rows, first, nr);
 }
 
-// tab2[h][o]: the bias of every offset in units of log2, rows of a multiple of 4; clears amax and, where
-// something will be added to them, the 64-bit sums.
+template <int D, int MAPS, int TAB>
+__global__ void __launch_bounds__(32 * kDkvWarps, D* MAPS == 128 ? 2 : 3) window_dkv_mma_kernel(WinArgs a) {
+  if (*a.far) return dkv_body<D, MAPS, TAB, true>(a);
+  dkv_body<D, MAPS, TAB, false>(a);
+}
+
+// tab2[h][o]: the bias of every offset in units of log2, rows of a multiple of 4; clears amax, far and,
+// where something will be added to them, the 64-bit sums.
 __global__ void bias_expand_kernel(WinArgs a) {
   const int T3 = offsets(a.m), T3p = table_pitch(a.m), o = blockIdx.x * blockDim.x + threadIdx.x;
   if (o == 0) a.amax[blockIdx.y] = 0;
+  if (o == 0 && blockIdx.y == 0) *a.far = 0;
   if ((a.wide || __ldg(&a.tiles[a.T].x) > kDupMost) && o < T3) a.sums[(size_t)blockIdx.y * T3 + o] = 0;
   if (o < T3p) a.tab2[(size_t)blockIdx.y * T3p + o] = o < T3 ? bias2_at(a, blockIdx.y, o) : 0.f;
 }
@@ -1192,6 +1229,10 @@ template <int D, int MAPS, bool BIAS>
 cudaError_t bwd(const WinArgs& a, cudaStream_t st) {
   constexpr int ON = BIAS ? 1 : 0;
   const size_t T3p = BIAS ? table_pitch(a.m) : 0;
+  if (!BIAS) {
+    const cudaError_t e = cudaMemsetAsync(a.far, 0, sizeof(int), st);
+    if (e != cudaSuccess) return e;
+  }
   if (BIAS)
     SSA_LAUNCH("bias_expand_kernel", bias_expand_kernel, dim3(((int)T3p + 255) / 256, a.hq), 256, 0, st, a);
   cudaError_t r = rows_pass<D, MAPS, BIAS, kStats>("window_stats_kernel", a, st);

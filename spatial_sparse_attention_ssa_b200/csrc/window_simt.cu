@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(WinArgs a) {
         for (int i = 0; i < 2; ++i)
           if (ty + 8 * i < nr) {
             const size_t at = (size_t)(MAPS * h + u) * a.N + first + ty + 8 * i;
-            a.lse2[at] = lse2_of(m[u][i], l[u][i]);
+            store_lse2(a, at, m[u][i], l[u][i]);
             a.D[at] = dd[u][i] * safe_inv(l[u][i]);
           }
     }
@@ -486,16 +486,19 @@ __global__ void __launch_bounds__(kThreads) window_dkv_kernel(WinArgs a) {
         for (int u = 0; u < MAPS; ++u)
           fill<E, D, D>(sm + L::B + u * kChunk * (D + 4), a.q, a.sq, a.hq, MAPS * h + u, a.rows, k0, n, live(n));
         fill<T, D, DV>(sm + L::V, a.dout, nullptr, a.hq, MAPS * h, a.rows, k0, n, live(n));
+        bool any_far = false;
         if (threadIdx.x < kChunk) {
           codes[threadIdx.x] = threadIdx.x < n ? a.rows[k0 + threadIdx.x].y : 0;
 #pragma unroll
           for (int u = 0; u < MAPS; ++u) {
             const size_t at = (size_t)(MAPS * h + u) * a.N + k0 + threadIdx.x;
-            stat[2 * u * kChunk + threadIdx.x] = threadIdx.x < n ? a.lse2[at] : kPosInf;
+            const float lse2 = threadIdx.x < n ? a.lse2[at] : kPosInf;
+            any_far |= is_far(lse2);
+            stat[2 * u * kChunk + threadIdx.x] = lse2;
             stat[(2 * u + 1) * kChunk + threadIdx.x] = threadIdx.x < n ? a.D[at] : 0.f;
           }
         }
-        __syncthreads();
+        any_far = __syncthreads_or(any_far);
         float s[MAPS][2][4], dp[2][4];
         dots<DV>(sm + L::O, sm + L::V, n, dp);
 #pragma unroll
@@ -512,7 +515,12 @@ __global__ void __launch_bounds__(kThreads) window_dkv_kernel(WinArgs a) {
             for (int u = 0; u < MAPS; ++u) {
               float x = s[u][i][j] * mul;
               if (a.table && c < n) x += bias2_at(a, h, codes[c] - codes[kChunk + ty + 8 * i] + c0);
-              const float p = c < n ? ex2(x - stat[2 * u * kChunk + c]) : 0.f;
+              float p = c < n ? ex2(x - stat[2 * u * kChunk + c]) : 0.f;
+              if (any_far && c < n) {
+                const size_t at = (size_t)(MAPS * h + u) * a.N + k0 + c;
+                p *= far_factor(a, at, stat[2 * u * kChunk + c]);
+                if (p > 1.f) p = 1.f;  // a score may round to one side here, to the other where lse2 was taken
+              }
               const float ds = c < n ? p * (dp[i][j] - stat[(2 * u + 1) * kChunk + c]) : 0.f;
               pv[i][j] += u ? -lam * p : p;
               s[u][i][j] = u ? -lam * ds : ds;

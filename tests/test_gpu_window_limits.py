@@ -185,3 +185,84 @@ def test_what_the_bias_bars_stays_barred_beside_scores_that_overflow(dtype):
     assert float(dirty["dq"][:, 0].abs().max()) == 0 and bool(torch.isnan(dirty["dq"][7, 1]).any())
     assert bool(torch.isneginf(dirty["lse"][:, 0]).all())
     assert float(dirty["dbias"][0].abs().max()) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("far", [-1e9, -65504.0, -2000.0, 3e6])
+def test_weights_of_a_row_sum_to_one_however_far_its_scores(far, dtype):
+    """A large number on every key of a row, as a mask of -1e9 is: the backward's weights are those of the
+    forward and sum to one.  dv of a cell with dout of ones is the sum of all its rows' weights: the number
+    of rows.  bf16: a step's half of 2^-8 each for the weights and for dv; fp32: two exponentials 2^-22."""
+    coords, cu = dense(95, 40, 4)
+    pr = Problem(coords, cu, 4, 2, 1, 32, DT[dtype], seed=96, bias="offset")
+    pr.bias.table[:] = far
+    pr.dout[:] = 1.0
+    r = run_window(pr)
+    total = r["dv"].double().sum(0) / 80
+    tol = 2.1 * 2.0 ** -8 if dtype == "bf16" else 1e-6
+    assert float((total - 1).abs().max()) < tol, total
+    # dout of ones times v of one: dP is the same for every key, so dS is zero but for roundings of dP - D
+    pr.v[:] = 1.0
+    r = run_window(pr)
+    for x in ("dq", "dk", "dbias"):
+        assert float(r[x].double().abs().max()) < 32 * 80 * 2.0 ** -18, x
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m,crowd", [(4, 0), (4, 3000), (14, 0)])
+def test_gradients_do_not_see_a_bias_that_all_keys_share(m, crowd, dtype):
+    """q of zeros, so every score is the bias: with -1e9 everywhere the weights, and so all gradients, are
+    those with 0 everywhere.  lse2 and its rest against lse2 alone: an exponential of 2^-22 more and a
+    rounding of log2 of the sum, 12 at most, 2^-21 ln 2: below 1e-6 of each weight; bf16 weights and results
+    may round to the other side, 2^-7 of a weight each."""
+    coords, cu = shell(97, 300, r=9)
+    if crowd:
+        coords = np.concatenate([coords, np.repeat(coords[100:101], crowd, 0)])
+        cu = np.array([0, len(coords)], np.int32)
+    pr = Problem(coords, cu, m, 4, 2, 32, DT[dtype], seed=98, bias="offset")
+    pr.q[:] = 0
+    pr.bias.table[:] = 0
+    want = run_window(pr)
+    pr.bias.table[:] = -1e9
+    got = run_window(pr)
+    for x in ("out", "dq", "dk", "dv", "dbias"):
+        near = float((got[x].double() - want[x].double()).norm())
+        tol = 2.0 ** -7 if dtype == "bf16" and x != "dbias" else 1e-5
+        assert near <= tol * float(want[x].double().norm()), x
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("op", ["window", "diff"])
+@pytest.mark.parametrize("size", [2.0 ** 6, 2.0 ** 12])
+def test_weights_of_rows_with_large_equal_scores(size, op, dtype):
+    """No bias, q and k the same large vector everywhere: equal scores up to 10^8, weights 1 / n, so dv of dout of
+    ones is the number of maps that read a value head, the second ones times -lambda."""
+    coords, cu = dense(99, 40, 4)
+    pr = Problem(coords, cu, 4, 4, 2, 32, DT[dtype], seed=100)
+    pr.q[:], pr.k[:], pr.dout[:] = size, size, 1.0
+    pr.lam[:] = 0
+    r = run_window(pr) if op == "window" else run_diff(pr)
+    # a key's weights over 40 rows sum to 1 in a map; window: 2 query heads read a key head; differential:
+    # 2 output heads read the one value head, lambda is its initial value, 0.5
+    want = 2.0 if op == "window" else 1.0
+    tol = 2.1 * 2.0 ** -8 if dtype == "bf16" else 1e-6
+    if op == "diff" and dtype == "bf16":
+        tol *= 3                                    # the maps' weights are rounded each: (1 + 0.5) / (1 - 0.5)
+    assert float((r["dv"].double() / want - 1).abs().max()) < tol
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_what_is_not_finite_shows_beside_rows_far_from_zero(bad, dtype):
+    coords, cu = shell(101, 250, r=8)
+    pr = Problem(coords, cu, 5, 4, 2, 32, DT[dtype], seed=102, bias="offset")
+    pr.bias.table[:] = -1e9
+    clean = run_window(pr)
+    for x in (pr.q, pr.k, pr.v, pr.dout):
+        x[11] = bad
+    dirty = run_window(pr)
+    cell = pr.win.id == pr.win.id[11]
+    for x in ("out", "dq", "dk", "dv"):
+        assert torch.equal(clean[x][~cell], dirty[x][~cell]), x
+        assert not bool(torch.isfinite(dirty[x][11]).any()), x
+        assert x == "out" or not bool(torch.isfinite(dirty[x][cell]).any()), x
