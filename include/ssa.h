@@ -80,8 +80,10 @@ enum {
   SSA_OP_CROSS_BACKWARD = 5,
   SSA_OP_SP_FORWARD = 6,
   SSA_OP_SP_BACKWARD = 7,
-  SSA_OP_WINDOW_BACKWARD = 8, /* ssa_window_workspace_size */
-  SSA_OP_DIFF_BACKWARD = 9    /* ssa_window_workspace_size */
+  SSA_OP_WINDOW_BACKWARD = 8,         /* ssa_window_workspace_size */
+  SSA_OP_DIFF_BACKWARD = 9,           /* ssa_window_workspace_size */
+  SSA_OP_WINDOW_BACKWARD_TENSORS = 10, /* the same for calls without act8 */
+  SSA_OP_DIFF_BACKWARD_TENSORS = 11
 };
 
 /* Shape and method parameters shared by forward and backward. */
@@ -466,7 +468,8 @@ SSA_API ssa_status ssa_window_forward(const ssa_window_params* p, const ssa_win_
  *          ignored); the gradients are those at the values the codes hold, in dtype.  In
  *          SSA_DTYPE_BF16 the workspace holds them as bf16 during the call
  *   ws     device workspace, 256-byte aligned, ssa_window_workspace_size(SSA_OP_WINDOW_BACKWARD,
- *          p, plan) bytes (SSA_ERR_WORKSPACE if ws_bytes is less)
+ *          p, plan) bytes, without act8 SSA_OP_WINDOW_BACKWARD_TENSORS (SSA_ERR_WORKSPACE if
+ *          ws_bytes is less)
  */
 SSA_API ssa_status ssa_window_backward(const ssa_window_params* p, const ssa_win_plan* plan,
                                        const ssa_window_bias* bias, const void* q, const void* k, const void* v,
@@ -482,7 +485,8 @@ SSA_API ssa_status ssa_window_backward(const ssa_window_params* p, const ssa_win
  *   of q reads pair h / (hq / hkv) of k and v; lam fp32 [4, hq/2, d].  The plan's codes are not read.
  *
  * ssa_diff_backward -- gradients of sum(dout * out): dq, dk, dv in dtype and dlam fp32
- * [4, hq/2, d]; act8 and ws as in ssa_window_backward (SSA_OP_DIFF_BACKWARD).
+ * [4, hq/2, d]; act8 and ws as in ssa_window_backward (SSA_OP_DIFF_BACKWARD, without act8
+ * SSA_OP_DIFF_BACKWARD_TENSORS).
  */
 SSA_API ssa_status ssa_diff_forward(const ssa_window_params* p, const ssa_win_plan* plan, const float* lam,
                                     float lam_init, const void* q, const void* k, const void* v, void* out,
@@ -492,7 +496,11 @@ SSA_API ssa_status ssa_diff_backward(const ssa_window_params* p, const ssa_win_p
                                      const ssa_act8* act8, const void* dout, void* dq, void* dk, void* dv,
                                      float* dlam, void* ws, size_t ws_bytes, void* stream);
 
-/* Workspace bytes of SSA_OP_WINDOW_BACKWARD / SSA_OP_DIFF_BACKWARD; 0 for invalid arguments. */
+/*
+ * Workspace bytes of SSA_OP_WINDOW_BACKWARD / SSA_OP_DIFF_BACKWARD, which hold Q, K, V as bf16 in
+ * SSA_DTYPE_BF16 in case they come in 8 bits, and of their _TENSORS forms, which do not; 0 for
+ * invalid arguments.
+ */
 SSA_API size_t ssa_window_workspace_size(int32_t op, const ssa_window_params* p, const ssa_win_plan* plan);
 
 /*

@@ -888,9 +888,12 @@ SSA_API ssa_status ssa_window_plan(const int32_t* coords, int64_t N, int32_t m, 
 }
 
 SSA_API size_t ssa_window_workspace_size(int32_t op, const ssa_window_params* p, const ssa_win_plan* plan) {
-  const int maps = op == SSA_OP_WINDOW_BACKWARD ? 1 : op == SSA_OP_DIFF_BACKWARD ? 2 : 0;
+  const bool tensors = op == SSA_OP_WINDOW_BACKWARD_TENSORS || op == SSA_OP_DIFF_BACKWARD_TENSORS;
+  const int maps = op == SSA_OP_WINDOW_BACKWARD || op == SSA_OP_WINDOW_BACKWARD_TENSORS ? 1
+                   : op == SSA_OP_DIFF_BACKWARD || op == SSA_OP_DIFF_BACKWARD_TENSORS   ? 2
+                                                                                        : 0;
   if (!maps || check_window(p, plan, maps) != SSA_OK) return 0;
-  return carve_window(nullptr, p, plan, maps, true, nullptr);
+  return carve_window(nullptr, p, plan, maps, !tensors, nullptr);
 }
 
 SSA_API ssa_status ssa_window_forward(const ssa_window_params* p, const ssa_win_plan* plan,

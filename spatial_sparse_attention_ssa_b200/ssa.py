@@ -26,7 +26,7 @@ DTYPE_BF16, DTYPE_F32 = 0, 1
 GATE_WEIGHTS, GATE_LOGITS = 0, 1
 OP_BIN, OP_FORWARD, OP_BACKWARD, OP_GEO_SELECT, OP_CROSS_FORWARD, OP_CROSS_BACKWARD = 0, 1, 2, 3, 4, 5
 OP_SP_FORWARD, OP_SP_BACKWARD = 6, 7
-OP_WINDOW_BACKWARD, OP_DIFF_BACKWARD = 8, 9
+OP_WINDOW_BACKWARD, OP_DIFF_BACKWARD, OP_WINDOW_BACKWARD_TENSORS, OP_DIFF_BACKWARD_TENSORS = 8, 9, 10, 11
 WINDOW_MAX_EDGE, WINDOW_TILE = 16, 16
 SEL_SCORES, SEL_GIVEN = 0, 1
 
@@ -634,7 +634,8 @@ class WindowPlan:
         self._ws = {}  # workspace bytes by call and heads
 
     def workspace_size(self, op: int, p: "WindowParams") -> int:
-        """Bytes that OP_WINDOW_BACKWARD or OP_DIFF_BACKWARD needs for these heads."""
+        """Bytes that OP_WINDOW_BACKWARD or OP_DIFF_BACKWARD needs for these heads, or their
+        _TENSORS forms for calls whose q, k, v are not Act8."""
         key = (op, p.hq, p.hkv, p.d, p.dtype)
         if key not in self._ws:
             self._ws[key] = int(_lib().ssa_window_workspace_size(op, p, self._ref))
@@ -741,6 +742,10 @@ def ssa_window_forward(p: WindowParams, plan: WindowPlan, q: torch.Tensor, k: to
     return out
 
 
+# the backward calls whose q, k, v are tensors
+_TENSORS_OP = {OP_WINDOW_BACKWARD: OP_WINDOW_BACKWARD_TENSORS, OP_DIFF_BACKWARD: OP_DIFF_BACKWARD_TENSORS}
+
+
 def _window_backward(op: int, name: str, p: WindowParams, plan: WindowPlan, extra, extra_tensors, q, k, v, dout,
                      last: torch.Tensor | None, grads, workspace):
     ptrs, a8, ts = _qkv(p, plan, q, k, v)
@@ -754,7 +759,7 @@ def _window_backward(op: int, name: str, p: WindowParams, plan: WindowPlan, extr
     else:
         for g, s in zip(grads, shapes):
             _want(g, s, p._dtype, "grads")
-    need = plan.workspace_size(op, p)
+    need = plan.workspace_size(op if a8 is not None else _TENSORS_OP[op], p)
     ws = workspace if workspace is not None and workspace.numel() >= need else _workspace(need, dev)
     _call(dev, name, p, plan._ref, *extra, *ptrs, a8, _ptr(dout), *(_ptr(g) for g in grads), _ptr(last), _ptr(ws),
           ws.numel())

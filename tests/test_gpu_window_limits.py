@@ -266,3 +266,35 @@ def test_what_is_not_finite_shows_beside_rows_far_from_zero(bad, dtype):
         assert torch.equal(clean[x][~cell], dirty[x][~cell]), x
         assert not bool(torch.isfinite(dirty[x][11]).any()), x
         assert x == "out" or not bool(torch.isfinite(dirty[x][cell]).any()), x
+
+
+@pytest.mark.parametrize("op", ["window", "diff"])
+def test_a_workspace_for_tensors_serves_a_call_with_tensors(op):
+    """Nothing is allocated beside what the caller gives; from checkpoints the same workspace is too small."""
+    coords, cu = shell(103, 300, r=9)
+    pr = Problem(coords, cu, 6, 4, 2, 64, torch.bfloat16, seed=104, bias="offset")
+    window = op == "window"
+    need = pr.plan.workspace_size(ssa.OP_WINDOW_BACKWARD_TENSORS if window else ssa.OP_DIFF_BACKWARD_TENSORS, pr.p)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    grads = tuple(torch.empty_like(x) for x in (pr.q, pr.k, pr.v))
+    last = torch.empty_like(pr.bias.table if window else pr.lam)
+
+    def call(q, k, v):
+        if window:
+            return ssa.ssa_window_backward(pr.p, pr.plan, q, k, v, pr.dout, bias=pr.bias, grads=grads, dbias=last,
+                                           workspace=ws)
+        return ssa.ssa_diff_backward(pr.p, pr.plan, q, k, v, pr.lam, 0.5, pr.dout, grads=grads, dlam=last, workspace=ws)
+    want = run_window(pr) if window else run_diff(pr)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    got = call(pr.q, pr.k, pr.v)
+    torch.cuda.synchronize()
+    assert torch.cuda.max_memory_allocated() == before
+    for x, y in zip(got, ("dq", "dk", "dv", "dbias" if window else "dlam")):
+        assert torch.equal(x, want[y]), y
+    held = [ssa.ssa_act8_pack(x) for x in (pr.q, pr.k, pr.v)]
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    call(*held)
+    assert torch.cuda.max_memory_allocated() > before

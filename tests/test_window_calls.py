@@ -1,0 +1,20 @@
+"""The window, differential and 8-bit calls from the caller's side: sizes and arguments, no GPU needed."""
+import pytest
+
+from spatial_sparse_attention_ssa_b200 import ssa
+
+PLAN = ssa.WinPlanC(16, 16, 131072, 2800, 8)
+
+
+@pytest.mark.parametrize("ops", [(ssa.OP_WINDOW_BACKWARD, ssa.OP_WINDOW_BACKWARD_TENSORS),
+                                 (ssa.OP_DIFF_BACKWARD, ssa.OP_DIFF_BACKWARD_TENSORS)])
+def test_workspace_of_calls_without_checkpoints_holds_no_copies(ops):
+    """131072 tokens, 32/2 heads of 64: the bf16 copies of Q, K, V are 604 MB, the rest is below 100 MB."""
+    lib = ssa.lib()
+    for dtype in (ssa.DTYPE_BF16, ssa.DTYPE_F32):
+        p = ssa.WindowParams(32, 2, 64, dtype, 0.0)
+        full, tensors = (lib.ssa_window_workspace_size(op, p, PLAN) for op in ops)
+        # arrays start on 256 bytes, empty ones too
+        assert abs(full - tensors - (2 * 131072 * 64 * (32 + 2 + 2) if dtype == ssa.DTYPE_BF16 else 0)) < 3 * 512
+        assert 0 < tensors < 100 << 20
+    assert lib.ssa_window_workspace_size(ops[1], ssa.WindowParams(32, 3, 64, 0, 0.0), PLAN) == 0
