@@ -84,6 +84,13 @@ class WindowParams(ctypes.Structure):
     _fields_ = [("hq", ctypes.c_int32), ("hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("scale", ctypes.c_float)]
 
+    @property
+    def _dtype(self) -> torch.dtype:
+        """The type of the tensors, from the field that the library reads."""
+        if self.dtype not in (DTYPE_BF16, DTYPE_F32):
+            raise ValueError("dtype must be DTYPE_BF16 or DTYPE_F32")
+        return torch.bfloat16 if self.dtype == DTYPE_BF16 else torch.float32
+
 
 class WindowBiasC(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("bucket", ctypes.c_void_p), ("nb", ctypes.c_int32)]
@@ -662,9 +669,7 @@ def make_window_params(hq: int, hkv: int, d: int, dtype: torch.dtype, scale: flo
     dt = DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32 if dtype == torch.float32 else None
     if dt is None:
         raise ValueError("dtype must be torch.bfloat16 or torch.float32")
-    p = WindowParams(hq, hkv, d, dt, scale)
-    p._dtype = dtype
-    return p
+    return WindowParams(hq, hkv, d, dt, scale)
 
 
 @dataclass

@@ -1,5 +1,6 @@
 """The window, differential and 8-bit calls from the caller's side: sizes and arguments, no GPU needed."""
 import pytest
+import torch
 
 from spatial_sparse_attention_ssa_b200 import ssa
 
@@ -18,3 +19,22 @@ def test_workspace_of_calls_without_checkpoints_holds_no_copies(ops):
         assert abs(full - tensors - (2 * 131072 * 64 * (32 + 2 + 2) if dtype == ssa.DTYPE_BF16 else 0)) < 3 * 512
         assert 0 < tensors < 100 << 20
     assert lib.ssa_window_workspace_size(ops[1], ssa.WindowParams(32, 3, 64, 0, 0.0), PLAN) == 0
+
+
+def test_params_made_as_a_struct_and_changed_later():
+    """The type that the binding checks is the one that the library reads."""
+    e = lambda *s, dt=torch.bfloat16: torch.empty(*s, dtype=dt)  # noqa: E731
+    plan = ssa.WindowPlan(e(10, 2, dt=torch.int32), e(4, 4, dt=torch.int32), 10, 3, 4)
+    q, k = e(10, 4, 32), e(10, 2, 32)
+    for p in (ssa.WindowParams(4, 2, 32, ssa.DTYPE_F32, 0.0), ssa.make_window_params(4, 2, 32, torch.bfloat16)):
+        p.dtype = ssa.DTYPE_BF16
+        with pytest.raises(ValueError, match="CUDA"):        # types and shapes are right
+            ssa.ssa_window_forward(p, plan, q, k, k)
+        p.dtype = ssa.DTYPE_F32
+        with pytest.raises(ValueError, match="q must be"):
+            ssa.ssa_window_forward(p, plan, q, k, k)
+        with pytest.raises(ValueError, match="dout must be"):
+            ssa.ssa_window_backward(p, plan, q.float(), k.float(), k.float(), q)
+        p.dtype = 7
+        with pytest.raises(ValueError, match="dtype"):
+            ssa.ssa_window_forward(p, plan, q, k, k)
