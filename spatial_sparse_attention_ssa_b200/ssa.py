@@ -80,6 +80,9 @@ class WinPlanC(ctypes.Structure):
                 ("count", ctypes.c_int64), ("m", ctypes.c_int32)]
 
 
+_TORCH_DTYPE = {DTYPE_BF16: torch.bfloat16, DTYPE_F32: torch.float32}
+
+
 class WindowParams(ctypes.Structure):
     _fields_ = [("hq", ctypes.c_int32), ("hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("scale", ctypes.c_float)]
@@ -87,9 +90,10 @@ class WindowParams(ctypes.Structure):
     @property
     def _dtype(self) -> torch.dtype:
         """The type of the tensors, from the field that the library reads."""
-        if self.dtype not in (DTYPE_BF16, DTYPE_F32):
+        dt = _TORCH_DTYPE.get(self.dtype)
+        if dt is None:
             raise ValueError("dtype must be DTYPE_BF16 or DTYPE_F32")
-        return torch.bfloat16 if self.dtype == DTYPE_BF16 else torch.float32
+        return dt
 
 
 class WindowBiasC(ctypes.Structure):
@@ -625,7 +629,7 @@ def _want(t: torch.Tensor, shape: tuple, dtype: torch.dtype, name: str) -> None:
         raise ValueError("%s must be %s %s, got %s %s" % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
 
 
-@dataclass
+@dataclass(frozen=True)
 class WindowPlan:
     """Work plan of one partition (see ssa_win_plan in include/ssa.h): made once per voxel
     set, read by every layer and both passes of the window and differential calls."""
@@ -636,9 +640,23 @@ class WindowPlan:
     m: int
 
     def __post_init__(self):
-        self._c = WinPlanC(_ptr(self.rows), _ptr(self.tiles), self.n, self.count, self.m)
-        self._ref = ctypes.byref(self._c)
-        self._ws = {}  # workspace bytes by call and heads
+        put = lambda name, x: object.__setattr__(self, name, x)  # noqa: E731
+        put("_c", WinPlanC(_ptr(self.rows), _ptr(self.tiles), self.n, self.count, self.m))
+        put("_ref", ctypes.byref(self._c))
+        put("_ws", {})  # workspace bytes by call and heads
+        put("_sizes", (tuple(self.rows.shape), self.rows.dtype, tuple(self.tiles.shape), self.tiles.dtype) == (
+            (self.n, 2), torch.int32, (self.n // WINDOW_TILE + self.count + 1, 4), torch.int32))
+        put("_dev", self.rows.device if all(x.is_cuda and x.is_contiguous() and x.device == self.rows.device
+                                            for x in (self.rows, self.tiles)) else None)
+
+    def device(self, *ts: torch.Tensor | None) -> torch.device:
+        """The device of the plan and of `ts`."""
+        dev = _on_one_device(*ts)
+        if dev != self._dev:
+            raise ValueError("the plan's arrays must be contiguous CUDA tensors on the device of the others")
+        if not self._sizes:
+            raise ValueError("the plan's rows must be int32 [n, 2], its tiles int32 [n // 16 + count + 1, 4]")
+        return dev
 
     def workspace_size(self, op: int, p: "WindowParams") -> int:
         """Bytes that OP_WINDOW_BACKWARD or OP_DIFF_BACKWARD needs for these heads, or their
@@ -653,10 +671,14 @@ def ssa_window_plan(coords: torch.Tensor | None, win: Bins, m: int = 0) -> Windo
     """Plan of the partition `win` (from ssa_bin; `blk` serves as well).  With the binned
     coordinates and the window edge m (at most WINDOW_MAX_EDGE) it carries the offset codes
     that a bias reads; coords = None makes a plan without them, for any partition."""
-    dev = _on_one_device(win.perm, win.id, win.ptr, coords)
     n = int(win.perm.shape[0])
+    for name, x in (("win.perm", win.perm), ("win.id", win.id)):
+        _want(x, (n,), torch.int32, name)
+    if win.ptr.dtype != torch.int32 or win.ptr.dim() != 1 or win.ptr.shape[0] < win.count + 1:
+        raise ValueError("win.ptr must be int32 of win.count + 1 entries at least")
     if coords is not None:
         _want(coords, (n, 3), torch.int32, "coords")
+    dev = _on_one_device(win.perm, win.id, win.ptr, win.cu, win.key, coords)
     e = lambda *s: torch.empty(*s, dtype=torch.int32, device=dev)  # noqa: E731
     plan = WindowPlan(e(n, 2), e(n // WINDOW_TILE + win.count + 1, 4), n, int(win.count), int(m) if coords is not None else 0)
     pb = win.c()
@@ -722,8 +744,9 @@ def _qkv(p: WindowParams, plan: WindowPlan, q, k, v):
         return (None, None, None), arr, [t for x in (q, k, v) for t in (x.codes, x.scale)]
     if any(isinstance(x, Act8) for x in (q, k, v)):
         raise ValueError("q, k, v must be three tensors or three Act8")
+    dt = p._dtype
     for name, x, h in names:
-        _want(x, (n, h, p.d), p._dtype, name)
+        _want(x, (n, h, p.d), dt, name)
     return (_ptr(q), _ptr(k), _ptr(v)), None, [q, k, v]
 
 
@@ -736,7 +759,7 @@ def ssa_window_forward(p: WindowParams, plan: WindowPlan, q: torch.Tensor, k: to
     if a8 is not None:
         raise ValueError("the forward reads tensors, not Act8")
     bc, _ = _bias_c(bias, p, plan)
-    dev = _on_one_device(*ts, plan.rows, out, lse, *((bias.table, bias.bucket) if bias else ()))
+    dev = plan.device(*ts, out, lse, *((bias.table, bias.bucket) if bias else ()))
     if out is None:
         out = torch.empty_like(q)
     else:
@@ -755,7 +778,7 @@ def _window_backward(op: int, name: str, p: WindowParams, plan: WindowPlan, extr
                      last: torch.Tensor | None, grads, workspace):
     ptrs, a8, ts = _qkv(p, plan, q, k, v)
     _want(dout, (plan.n, p.hq, p.d), p._dtype, "dout")
-    dev = _on_one_device(*ts, dout, plan.rows, last, workspace, *extra_tensors, *(grads or ()))
+    dev = plan.device(*ts, dout, last, workspace, *extra_tensors, *(grads or ()))
     if workspace is not None and workspace.dtype != torch.uint8:
         raise ValueError("workspace must be uint8")
     shapes = ((plan.n, p.hq, p.d), (plan.n, p.hkv, p.d), (plan.n, p.hkv, p.d))
@@ -797,7 +820,7 @@ def ssa_diff_forward(p: WindowParams, plan: WindowPlan, q: torch.Tensor, k: torc
     if a8 is not None:
         raise ValueError("the forward reads tensors, not Act8")
     _want(lam, (4, p.hq // 2, p.d), torch.float32, "lam")
-    dev = _on_one_device(*ts, lam, plan.rows, out)
+    dev = plan.device(*ts, lam, out)
     if out is None:
         out = torch.empty_like(q)
     else:

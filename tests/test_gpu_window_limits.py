@@ -298,3 +298,19 @@ def test_a_workspace_for_tensors_serves_a_call_with_tensors(op):
     torch.cuda.reset_peak_memory_stats()
     call(*held)
     assert torch.cuda.max_memory_allocated() > before
+
+
+def test_plans_whose_arrays_have_other_sizes_are_refused():
+    coords, cu = shell(105, 200)
+    pr = Problem(coords, cu, 4, 2, 1, 32, torch.float32, seed=106)
+    ok = pr.plan
+    for bad, what in ((ssa.WindowPlan(ok.rows, ok.tiles[:-1].contiguous(), ok.n, ok.count, ok.m), "tiles"),
+                      (ssa.WindowPlan(ok.rows.long(), ok.tiles, ok.n, ok.count, ok.m), "rows"),
+                      (ssa.WindowPlan(ok.rows, ok.tiles, ok.n, ok.count + 1, ok.m), "tiles"),
+                      (ssa.WindowPlan(ok.rows.cpu(), ok.tiles, ok.n, ok.count, ok.m), "CUDA")):
+        for call in (lambda: ssa.ssa_window_forward(pr.p, bad, pr.q, pr.k, pr.v),
+                     lambda: ssa.ssa_window_backward(pr.p, bad, pr.q, pr.k, pr.v, pr.dout)):
+            with pytest.raises(ValueError, match=what):
+                call()
+    with pytest.raises(AttributeError):          # the library would go on reading the old array
+        ok.tiles = ok.tiles.clone()

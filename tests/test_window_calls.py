@@ -38,3 +38,18 @@ def test_params_made_as_a_struct_and_changed_later():
         p.dtype = 7
         with pytest.raises(ValueError, match="dtype"):
             ssa.ssa_window_forward(p, plan, q, k, k)
+
+
+def test_partitions_whose_arrays_have_other_sizes_are_refused():
+    e = lambda *s, dt=torch.int32: torch.empty(*s, dtype=dt)  # noqa: E731
+    bins = lambda **kw: ssa.Bins(**dict(dict(id=e(10), perm=e(10), ptr=e(11), cu=e(2), key=e(10, 3), count=4), **kw))  # noqa: E731
+    with pytest.raises(ValueError, match="CUDA"):
+        ssa.ssa_window_plan(e(10, 3), bins(), 4)
+    with pytest.raises(ValueError, match="win.id"):
+        ssa.ssa_window_plan(e(10, 3), bins(id=e(9)), 4)
+    with pytest.raises(ValueError, match="win.perm"):
+        ssa.ssa_window_plan(e(10, 3), bins(perm=e(10, dt=torch.int64)), 4)
+    with pytest.raises(ValueError, match="win.ptr"):
+        ssa.ssa_window_plan(e(10, 3), bins(ptr=e(4)), 4)
+    with pytest.raises(ValueError, match="coords"):
+        ssa.ssa_window_plan(e(11, 3), bins(), 4)
