@@ -375,8 +375,9 @@ SSA_API ssa_status ssa_sp_backward(const ssa_params* p, int32_t S, int64_t N, co
  * the bias, the difference of maps and the checkpoints have no counterpart on the pages):
  * every token attends the tokens of its own cell (window or block) of any partition that
  * ssa_bin made.  All of them are asynchronous, allocate nothing, find argument errors on
- * the host before anything is enqueued, and give the same bits on every run.  A tensor of
- * 64 GB or more (n * hq * d / 8 above 2^32 - 1) is SSA_ERR_UNSUPPORTED.
+ * the host before anything is enqueued, and give the same bits on every run.  Outputs overlap
+ * neither inputs nor one another (SSA_ERR_INVALID_ARG), but for out = q, dk = k and dv = v (not from
+ * codes), which may be the same arrays.  A tensor of 64 GB or more (n * hq * d / 8 above 2^32 - 1) is SSA_ERR_UNSUPPORTED.
  */
 
 /* The largest window edge a relative position bias can have ((2*16-1)^3 offsets). */

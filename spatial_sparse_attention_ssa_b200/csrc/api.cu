@@ -4,6 +4,8 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <initializer_list>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -719,6 +721,33 @@ namespace {
 
 bool aligned16(const void* x) { return reinterpret_cast<uintptr_t>(x) % 16 == 0; }
 
+// An array of a call, and whether one of `out` overlaps another or one of `in`.  in[i] may be out[i]
+// itself where a kernel reads a row before it writes it and no other block reads it (same > i).
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+bool any_overlap(std::initializer_list<Span> out, std::initializer_list<Span> in, size_t same) {
+  for (size_t i = 0; i < out.size(); ++i) {
+    const Span& o = out.begin()[i];
+    for (size_t j = 0; j < i; ++j)
+      if (overlap(o, out.begin()[j])) return true;
+    for (size_t j = 0; j < in.size(); ++j)
+      if (overlap(o, in.begin()[j]) && !(i == j && i < same && o.p == in.begin()[j].p)) return true;
+  }
+  return false;
+}
+
+// Bytes of q (or out, dout, dq) and of k (or v, dk, dv).
+size_t q_bytes(const ssa_window_params* p, const ssa_win_plan* plan) {
+  return (size_t)plan->n * p->hq * p->d * (p->dtype == SSA_DTYPE_BF16 ? 2 : 4);
+}
+size_t kv_bytes(const ssa_window_params* p, const ssa_win_plan* plan) { return q_bytes(p, plan) / p->hq * p->hkv; }
+
 // Heads, types and plan; maps: 1 window, 2 differential.
 ssa_status check_window(const ssa_window_params* p, const ssa_win_plan* plan, int maps) {
   if (!p || !plan) return SSA_ERR_INVALID_ARG;
@@ -841,6 +870,11 @@ ssa_status window_backward(const ssa_window_params* p, const ssa_win_plan* plan,
     if (!x || !aligned16(x)) return SSA_ERR_INVALID_ARG;
   if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0) return SSA_ERR_INVALID_ARG;
   if (ws_bytes < carve_window(ws, p, plan, maps, act8 != nullptr, &a)) return SSA_ERR_WORKSPACE;
+  const size_t nq = q_bytes(p, plan), nkv = kv_bytes(p, plan), div = !act8 ? 1 : p->dtype == SSA_DTYPE_BF16 ? 2 : 4;
+  const size_t nlam = sizeof(float) * 2 * (size_t)p->hq * p->d;
+  if (any_overlap({{dk, nkv}, {dv, nkv}, {dq, nq}, {dlam, nlam}},
+                  {{a.k, nkv / div}, {a.v, nkv / div}, {a.q, nq / div}, {dout, nq}, {a.lam, nlam}}, act8 ? 0 : 2))
+    return SSA_ERR_INVALID_ARG;
   a.dout = dout;
   a.dq = dq;
   a.dk = dk;
@@ -904,6 +938,9 @@ SSA_API ssa_status ssa_window_forward(const ssa_window_params* p, const ssa_win_
   if (s != SSA_OK || plan->n == 0) return s;
   for (const void* x : {q, k, v, (const void*)out})
     if (!x || !aligned16(x)) return SSA_ERR_INVALID_ARG;
+  const size_t nq = q_bytes(p, plan), nkv = kv_bytes(p, plan);
+  if (any_overlap({{out, nq}, {lse, sizeof(float) * (size_t)plan->n * p->hq}}, {{q, nq}, {k, nkv}, {v, nkv}}, 1))
+    return SSA_ERR_INVALID_ARG;
   ssa::WinArgs a = window_args(p, plan, 1, bias, nullptr, 0.f, q, k, v);
   a.out = out;
   a.lse = lse;
@@ -934,6 +971,8 @@ SSA_API ssa_status ssa_diff_forward(const ssa_window_params* p, const ssa_win_pl
   if (plan->n == 0) return SSA_OK;
   for (const void* x : {q, k, v, (const void*)out})
     if (!x || !aligned16(x)) return SSA_ERR_INVALID_ARG;
+  const size_t nq = q_bytes(p, plan), nkv = kv_bytes(p, plan);
+  if (any_overlap({{out, nq}}, {{q, nq}, {k, nkv}, {v, nkv}}, 1)) return SSA_ERR_INVALID_ARG;
   ssa::WinArgs a = window_args(p, plan, 2, nullptr, lam, lam_init, q, k, v);
   a.out = out;
   return cuda_status(window_forward(a, static_cast<cudaStream_t>(stream)));

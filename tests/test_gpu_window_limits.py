@@ -314,3 +314,23 @@ def test_plans_whose_arrays_have_other_sizes_are_refused():
                 call()
     with pytest.raises(AttributeError):          # the library would go on reading the old array
         ok.tiles = ok.tiles.clone()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("op", ["window", "diff"])
+def test_results_in_the_place_of_what_they_replace(op, dtype):
+    """out = q, dk = k, dv = v: the same bits."""
+    coords, cu = dense(107, 420, 8)
+    pr = Problem(coords, cu, 8, 4, 2, 64, DT[dtype], seed=108, bias="offset" if op == "window" else None)
+    want = (run_window if op == "window" else run_diff)(pr)
+    q, k, v, dq = pr.q.clone(), pr.k.clone(), pr.v.clone(), torch.empty_like(pr.q)
+    if op == "window":
+        ssa.ssa_window_backward(pr.p, pr.plan, pr.q, k, v, pr.dout, bias=pr.bias, grads=(dq, k, v))
+        ssa.ssa_window_forward(pr.p, pr.plan, q, pr.k, pr.v, bias=pr.bias, out=q)
+    else:
+        ssa.ssa_diff_backward(pr.p, pr.plan, pr.q, k, v, pr.lam, 0.5, pr.dout, grads=(dq, k, v))
+        ssa.ssa_diff_forward(pr.p, pr.plan, q, pr.k, pr.v, pr.lam, 0.5, out=q)
+    for x, y in ((q, "out"), (dq, "dq"), (k, "dk"), (v, "dv")):
+        assert torch.equal(x, want[y]), y
+    with pytest.raises(ssa.SSAError, match="INVALID_ARG"):
+        ssa.ssa_window_backward(pr.p, pr.plan, q, pr.k, pr.v, pr.dout, grads=(q, k, v))

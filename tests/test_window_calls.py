@@ -53,3 +53,47 @@ def test_partitions_whose_arrays_have_other_sizes_are_refused():
         ssa.ssa_window_plan(e(10, 3), bins(ptr=e(4)), 4)
     with pytest.raises(ValueError, match="coords"):
         ssa.ssa_window_plan(e(11, 3), bins(), 4)
+
+
+N, HQ, HKV, D = 100, 4, 2, 32
+Q, KV = N * HQ * D * 2, N * HKV * D * 2
+AT = 1 << 30          # no call gets far enough to read there: there is no device, or the call is refused
+A = {x: AT + i * (1 << 20) for i, x in enumerate(("q", "k", "v", "out", "lse", "dout", "dq", "dk", "dv", "lam", "dlam", "ws"))}
+REFUSED = 1
+
+
+def _fwd(op, **kw):
+    a, p, plan = dict(A, **kw), ssa.WindowParams(HQ, HKV, D, ssa.DTYPE_BF16, 0.0), ssa.WinPlanC(16, 16, N, 10, 0)
+    if op == "window":
+        return ssa.lib().ssa_window_forward(p, plan, None, a["q"], a["k"], a["v"], a["out"], a["lse"], None)
+    return ssa.lib().ssa_diff_forward(p, plan, a["lam"], 0.5, a["q"], a["k"], a["v"], a["out"], None)
+
+
+def _bwd(op, codes=False, **kw):
+    a, p, plan = dict(A, **kw), ssa.WindowParams(HQ, HKV, D, ssa.DTYPE_BF16, 0.0), ssa.WinPlanC(16, 16, N, 10, 0)
+    a8 = (ssa.Act8C * 3)(*((a[x], 16) for x in "qkv")) if codes else None
+    tail = (a["q"], a["k"], a["v"], a8, a["dout"], a["dq"], a["dk"], a["dv"])
+    if op == "window":
+        return ssa.lib().ssa_window_backward(p, plan, None, *tail, None, a["ws"], 1 << 30, None)
+    return ssa.lib().ssa_diff_backward(p, plan, a["lam"], 0.5, *tail, a["dlam"], a["ws"], 1 << 30, None)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the calls that pass would read the addresses")
+@pytest.mark.parametrize("op", ["window", "diff"])
+def test_outputs_that_overlap_are_refused(op):
+    assert _fwd(op) != REFUSED and _bwd(op) != REFUSED and _bwd(op, codes=True) != REFUSED
+    assert _fwd(op, out=A["q"]) != REFUSED and _bwd(op, dk=A["k"], dv=A["v"]) != REFUSED
+    for x in ("k", "v"):
+        assert _fwd(op, out=A[x]) == REFUSED and _fwd(op, out=A[x] + KV - 16) == REFUSED
+        assert _fwd(op, out=A[x] - Q + 16) == REFUSED and _fwd(op, out=A[x] + KV) != REFUSED
+    assert _fwd(op, out=A["q"] + 16) == REFUSED
+    for x in ("q", "k", "v", "dout"):
+        assert _bwd(op, dq=A[x]) == REFUSED and _bwd(op, codes=True, dq=A[x]) == REFUSED
+    for x in ("dk", "dv"):
+        assert _bwd(op, **{x: A["dout"]}) == REFUSED and _bwd(op, **{x: A["dq"] + Q - 16}) == REFUSED
+        assert _bwd(op, **{x: A["q"]}) == REFUSED and _bwd(op, codes=True, **{x: A[x[1]]}) == REFUSED
+    assert _bwd(op, dk=A["v"]) == REFUSED and _bwd(op, dv=A["dk"]) == REFUSED and _bwd(op, dk=A["k"] + 16) == REFUSED
+    if op == "window":
+        assert _fwd(op, lse=A["out"]) == REFUSED and _fwd(op, lse=A["q"]) == REFUSED
+    else:
+        assert _bwd(op, dlam=A["lam"]) == REFUSED
