@@ -800,7 +800,6 @@ ssa::WinArgs window_args(const ssa_window_params* p, const ssa_win_plan* plan, i
   a.q = q;
   a.k = k;
   a.v = v;
-  a.cells = plan->count;
   return a;
 }
 

@@ -158,7 +158,6 @@ struct WinArgs {
   const int4* tiles;  // [T] first row, rows (+ flag, + kDupUnit times most tokens of a voxel), cell begin,
                       // cell end; [T].x: most tokens of a voxel of any cell
   int T, m;
-  int64_t cells;
   const float* table;  // bias [hq, nb], or null
   const int32_t* bucket;
   int nb;

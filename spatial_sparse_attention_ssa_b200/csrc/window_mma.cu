@@ -945,17 +945,18 @@ cudaError_t rows_pass(const char* name, const WinArgs& a, cudaStream_t st) {
   constexpr int ON = BIAS ? 1 : 0;
   const bool grad = MODE == kDq && BIAS && a.dbias;
   const size_t T3 = BIAS ? offsets(a.m) : 0, list = sizeof(int4) * S::items;
-  // Two heads to a CTA where they share a key head: the stages then serve twice the work.  Chunks of
-  // 64 keys, of 32 where cells are so small that more of them in flight count for more than fewer
-  // steps.  The bias lies in shared memory where room is left beside it for eight warps and four
-  // stages (the forward always has it there); then as many warps as may be, and as many stages as fit.
-  // What does not fit takes one head, then small chunks, then three stages.
+  // Two heads to a CTA where they share a key head: the stages then serve twice the work.  Chunks of 64
+  // keys: chunks of 32 cost 4 to 6% of a step of cells of 21 to 41 tokens (131072 tokens, edges 5 to 7:
+  // 3638, 3234, 3560 us against 3776, 3423, 3680) and gain 1% at most where cells hold 4 to 16.  The bias
+  // lies in shared memory where room is left beside it for eight warps and four stages (the forward always
+  // has it there); then as many warps as may be, and as many stages as fit.  What does not fit takes one
+  // head, then chunks of 32, then three stages.
   int chunk = 0, pairs = 0, NW = 0, NS = 0;
   bool in_smem = false;
   size_t smem = 0;
   for (int attempt = 0; attempt < 4 && !smem; ++attempt) {
     pairs = attempt == 0 && a.hq / a.hkv % 2 == 0 && S::warps >= 10 ? 2 : 1;
-    chunk = attempt >= 2 || a.N <= 24 * (int64_t)a.cells ? 32 : kChunk;
+    chunk = attempt >= 2 ? 32 : kChunk;
     const size_t stage = (size_t)chunk * S::token, table = 4 * T3 * pairs, limbs = grad && !a.wide ? 8 * T3 * pairs : 0;
     const size_t least = list + limbs + min(8, S::warps) * S::warp + (attempt == 3 ? 3 : 4) * stage;
     in_smem = BIAS && !(grad && a.wide) && least + table <= kSmemMost;

@@ -678,7 +678,7 @@ def ssa_window_plan(coords: torch.Tensor | None, win: Bins, m: int = 0) -> Windo
         raise ValueError("win.ptr must be int32 of win.count + 1 entries at least")
     if coords is not None:
         _want(coords, (n, 3), torch.int32, "coords")
-    dev = _on_one_device(win.perm, win.id, win.ptr, win.cu, win.key, coords)
+    dev = _on_one_device(win.perm, win.id, win.ptr, coords)
     e = lambda *s: torch.empty(*s, dtype=torch.int32, device=dev)  # noqa: E731
     plan = WindowPlan(e(n, 2), e(n // WINDOW_TILE + win.count + 1, 4), n, int(win.count), int(m) if coords is not None else 0)
     pb = win.c()
