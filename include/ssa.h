@@ -430,11 +430,14 @@ typedef struct ssa_window_params {
  * scaled score.  Offsets are numbered ((ox+m-1)*E + oy+m-1)*E + oz+m-1, E = 2m-1.
  */
 typedef struct ssa_window_bias {
-  const float* table;    /* [hq, nb] fp32; a value at or below -1e38 (minus infinity, the type's
-                            lowest) bars the offsets of a bucket: a row with nothing left gives
-                            zeros, lse minus infinity and no gradient */
+  const float* table;    /* [hq, nb] fp32, below 2e38; a value at or below -1e38 (minus infinity, the
+                            type's lowest) bars the offsets of a bucket: a row with nothing left gives
+                            zeros, lse minus infinity and no gradient.  A barred key's weight is 0, and
+                            0 times a NaN or an infinity in its row of k or v is NaN.  Scores are fp32:
+                            keys whose scores are far from zero keep only that precision */
   const int32_t* bucket; /* [E^3], or NULL: every offset is its own bucket (nb = E^3); an offset
-                            whose bucket is outside [0, nb) gets no bias and no gradient */
+                            whose bucket is outside [0, nb) gets no bias and no gradient.  The time of
+                            dbias grows with nb E^3 hq: NULL is the way to one bucket per offset */
   int32_t nb;            /* buckets */
 } ssa_window_bias;
 

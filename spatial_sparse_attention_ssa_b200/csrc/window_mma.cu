@@ -1,21 +1,23 @@
 // Attention inside the cells on warp-level tensor-core MMAs (mma.sync m16n8k16, bf16 operands,
 // fp32 sums).  See window.cuh for the mathematics and the meaning of MAPS.
 //
-// A CTA keeps one head (its bias table lies in shared memory) and walks cells.  The keys of the
-// cells, 64 at a time, go through a ring of stages in shared memory that two warps fill ahead
-// (cp.async, completion on an mbarrier); the cell's rows, 16 at a time, go to the other warps in
-// turn, so no warp waits for another but through the ring.  Scores never leave registers: a step is
-// 16 rows by 32 keys.  Tiles of 128 rows (tcgen05) would stand half empty on windows of some 50
-// tokens and hand every score through TMEM.
+// A CTA keeps one head, or two that share a key head (their bias tables lie in shared memory while they
+// fit), and walks cells.  The keys of the cells, 64 at a time, go through a ring of stages in shared
+// memory that two warps fill ahead (cp.async, completion on an mbarrier); the cell's rows, 16 at a time,
+// go to the other warps in turn, so no warp waits for another but through the ring.  Scores never leave
+// registers: a step is 16 rows by 32 keys.  Tiles of 128 rows on tcgen05 are not tried here.  Of one head
+// and a cell of some 50 tokens they would stand half empty, but with rows of several heads that share a
+// key head, as win_tc.cu packs them, or on cells of hundreds of tokens they would not; that kernel reaches
+// 80 TFLOP/s of products on a shell of 131072 tokens (its hand-offs per item bind it), this forward 80.
 //
 // What bounds these kernels is instruction issue and its latencies: of some 330 instructions of a
 // forward step 32 are products, the rest the bias, the mask, the exponential and the sums; and a tile
 // of 16 rows costs some 500 before its first and after its last step, which cells of 47 tokens (1.9
 // steps a tile) do not spread.  32768 tokens (32/2 heads of 64, edge 8; forward, statistics, dq,
-// dk/dv): issue slots used 46, 47, 41, 37%, tensor pipe 19, 19, 19, 37%, shared memory 51, 44, 57,
+// dk/dv): issue slots used 46, 48, 43, 39%, tensor pipe 19, 18, 20, 39%, shared memory 50, 43, 58,
 // 59%, HBM below 20%.  Times at 131072 tokens, and the TFLOP/s of the products alone (31.3 GFLOP each):
-// forward 790 us (79), statistics 803 us (78), dq with dbias 1324 us (71), dk/dv 927 us (135);
-// differential 1155, 705, 1027, 967 us; full cube of 24576, 16/2 heads of 128: 398, 408, 661, 567 us.
+// forward 787 us (80), statistics 808 us (77), dq with dbias 1325 us (71), dk/dv 887 us (141);
+// differential 1171, 709, 1035, 963 us; full cube of 24576, 16/2 heads of 128: 390, 414, 656, 571 us.
 #include "tc.cuh"
 #include "window.cuh"
 
@@ -431,9 +433,10 @@ struct Shape {
   static constexpr int warp = MODE == kForward ? scratch : 2 * scratch;
   static constexpr int items = 256;  // of a batch
   // Working warps of a CTA at most, beside the two that fill the ring; one CTA per SM, so that all
-  // stages are one ring.  As many as leave a thread the registers that its fragments need: spills
-  // cost more than warps gain (dq of rows of 128, 131072 tokens, differential: ten warps with 168
-  // registers 1.68 ms, six with 255 1.04 ms; dq of rows of 64: fourteen with 128 1.69 ms, ten 1.40 ms).
+  // stages are one ring.  As many as leave a thread nearly the registers that its fragments need: spills
+  // of fragments cost more than warps gain (dq of rows of 128, 131072 tokens, differential: ten warps
+  // with 168 registers 1.68 ms, six with 255 1.04 ms; dq of rows of 64: fourteen with 128 1.69 ms, ten
+  // 1.40 ms).  Eight of the instances still spill 4 to 76 bytes a thread.
   static constexpr int warps = DV == 128 ? (MODE == kDq || (MODE == kForward && MAPS == 2) ? 6 : 10)
                                          : MAPS == 2 || (MODE == kDq && DV == 64) ? 10 : 14;
   // Q and dO stay in registers as fragments, or are read again from the scratch tiles for every step
@@ -988,8 +991,9 @@ cudaError_t rows_pass(const char* name, const WinArgs& a, cudaStream_t st) {
 // scores of the cell's queries, 64 at a time, of every query head that reads the key head.  Q, dO,
 // the statistics and the head's bias table of the next step arrive while this one is computed.  Keys
 // stay with a CTA so that dk and dv are sums in registers, with no atomics, rounded once.  Bound by
-// issue and by the barriers of a step (cells of 47 tokens leave one warp in four without keys): 927 us
-// at 131072 tokens, 32/2 heads of 64; one barrier a step instead of two, its copies begun after it: 935.
+// issue and by the barriers of a step (cells of 47 tokens leave one warp in four without keys): 887 us
+// at 131072 tokens, 32/2 heads of 64; one barrier a step instead of two, its copies begun after it, took
+// 1% longer.
 constexpr int kDkvWarps = 4;
 
 // Number of key tiles of the CTA of a slot: four from every fourth tile of a cell.

@@ -5,10 +5,14 @@
 // Thread (ty, tx), tid = 16 ty + tx, holds the scores of rows ty, ty + 8 against the chunk's
 // rows tx + 16 j, and of the products with a chunk the columns tx * VEC (+ 64).  Cells of up
 // to 64 tokens keep their one chunk's scores in registers; larger cells take two passes, one
-// for the softmax statistics (and D), one for the products.  fp32 results within a few 2^-24 leave the
-// tensor core formats out.  Bound by shared memory (59 to 79% of its wavefronts) and by the loads that
-// fill a tile before its one or two chunks: 20011 tokens, 8/2 heads of 32, edge 6: forward 105 us,
-// dq with dbias 173 us, dk/dv 135 us (7, 6 and 11 TFLOP/s of products); differential, 9001 tokens: 50, 72, 73.
+// for the softmax statistics (and D), one for the products.  Products and sums are fp32: a weight is off
+// by 2^-22 (the exponential) and 2^-24 ln 2 times its score in units of log2 for each rounding of the
+// score, where operands of the tensor cores' formats would be off by 2^-11 (tf32) and more.  dbias sums
+// its rows in fp32 one after another: a relative error of about 2^-23 sqrt(adds) / 6, adds those of an
+// offset in a CTA.
+// Bound by shared memory (59 to 79% of its wavefronts) and by the loads that fill a tile before its one
+// or two chunks: 20011 tokens, 8/2 heads of 32, edge 6: forward 104 us, dq with dbias 177 us, dk/dv
+// 137 us (7, 6 and 11 TFLOP/s of products); differential, 9001 tokens: 51, 73, 75.
 // Loads of four rows ahead in `fill` cost registers and with them CTAs (dq 173 -> 238 us).
 #include "window.cuh"
 
