@@ -467,7 +467,8 @@ SSA_API ssa_status ssa_window_forward(const ssa_window_params* p, const ssa_win_
  * no bias); all written.  It recomputes the probabilities and needs nothing the forward left.
  *          Where a NaN or an infinity in the inputs of a head reaches a weight or <dout_i, v_j>, and
  *          where |<dout_i, v_j>| is 2^127 or more, all of its dbias is NaN in SSA_DTYPE_BF16; dq, dk,
- *          dv show it in its own cell only.
+ *          dv show it in its own cell only.  In SSA_DTYPE_BF16 what goes into dbias is rounded to
+ *          2^-32 of the largest |<dout_i, v_j>| of the head, or finer.
  *   act8   NULL, or an array of three: Q, K, V from 8-bit checkpoints (q, k, v are then
  *          ignored); the gradients are those at the values the codes hold, in dtype.  In
  *          SSA_DTYPE_BF16 the workspace holds them as bf16 during the call

@@ -284,18 +284,18 @@ __device__ __forceinline__ void red_shared(uint32_t at, int x) {
 // first (a rounding at most doubles a number that it does not make 0); each remainder is at most 1/2,
 // so 2^k <= 2^31 / (adds per offset) keeps the second, adds = rows times the most tokens that a voxel
 // of their cell holds.  Both stay below 2^13: before they pass it the CTA's sums go to its partial
-// gradient and start again, so the unit is M 2^-33 however many rows a CTA has.  An item of one crowded
-// cell can pass that alone: up to kDupMost tokens in a voxel the unit of its own few rows is M 2^-32
-// where dS is some M 2^-11; cells that are more crowded (kCrowd) take the 64-bit sums below.  A NaN or an
-// infinity in dP or in a softmax makes the head's gradient NaN, and so does an M from 2^127 on (dP - D
-// could overflow); below, 2^s and 2^-s are normal numbers.
+// gradient and start again, so the unit is at most M 2^-33 however many rows a CTA has; a batch alone
+// between two flushes counts its own (M 2^-41 for few rows).  An item of one crowded cell can pass the
+// bound alone: up to kDupMost tokens in a voxel its unit is M 2^-32, where dS is some M 2^-11; cells that
+// are more crowded (kCrowd) take the 64-bit sums below.  A NaN or an infinity in dP or in a softmax makes
+// the head's gradient NaN, and so does an M from 2^127 on (dP - D could overflow); below, 2^s and 2^-s are
+// normal numbers.
 constexpr int kAdds = 8191;      // at most between two flushes, but for a lone item
 constexpr int kCrowd = 1 << 16;  // items[].y: a cell for the 64-bit sums
 struct Limbs {
   float s[2], k;         // 2^s for the rows g, g + 8 (times far_factor, see store_lse2), 2^k
   double unit, unit_lo;  // 2^-s, 2^-s-k
   __device__ __forceinline__ void set(const WinArgs& a, int h, int rows, int adds) {
-    if (adds <= kAdds) rows = adds = kAdds;
     const uint32_t bits = __ldg(a.amax + h);
     const int rb = 32 - __clz(rows), ab = 32 - __clz(adds);  // rows < 2^rb, adds < 2^ab
     const int e = (int)(bits >> 23) - 126;                      // M < 2^e
@@ -461,7 +461,8 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
   extern __shared__ __align__(128) char sm[];
   __shared__ uint64_t full[kStages], empty[kStages];
   __shared__ int n_slots, n_items;         // of the batch
-  __shared__ int n_rows, n_adds, n_flush;  // since the last flush (see Limbs); whether the batch ends with one
+  __shared__ int n_rows, n_adds, n_flush;  // since the last flush; whether the batch ends with one
+  __shared__ int b_rows, b_adds;           // the bounds for Limbs
   const int NW = (int)blockDim.x / 32 - 2;  // working warps; two more fill the ring
   const uint32_t v_at = chunk * S::row, codes_at = 2 * v_at, stage_size = chunk * S::token;
   const int h0 = pairs * blockIdx.y, hk = h0 / (a.hq / a.hkv), item_size = NW / pairs;
@@ -514,7 +515,8 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
     __syncthreads();
     if (warp == NW) {
       int n = 0, i0 = 0, rows = 0, adds = 0;
-      if (grad && TAB != 3 && batch != blockIdx.x && !n_flush) rows = n_rows, adds = n_adds;
+      const bool fresh = batch == blockIdx.x || n_flush;
+      if (grad && TAB != 3 && !fresh) rows = n_rows, adds = n_adds;
       bool more = true;
 #pragma unroll 2
       while (more && i0 < S::items && batch + (int64_t)i0 * gridDim.x < a.T) {
@@ -553,13 +555,15 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
       if (lane == 0) {
         n_items = n, n_slots = i0, n_rows = rows, n_adds = adds;
         n_flush = !more || adds > kAdds || batch + (int64_t)i0 * gridDim.x >= a.T;
+        const bool alone = fresh && n_flush;  // no other batch since the last flush and before the next
+        b_rows = alone ? rows : kAdds, b_adds = alone ? adds : kAdds;
       }
     }
     __syncthreads();
     const int count = n_items;
     if (grad && TAB != 3) {
       for (int i = pairs - 1; i >= 0; --i) {
-        fx.set(a, h0 + i, n_rows, n_adds);
+        fx.set(a, h0 + i, b_rows, b_adds);
         (i ? s2[1] : s2[0]) = fx.s[0];
       }
     }
@@ -912,7 +916,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
       // the sums since the last flush; each thread has offsets of its own
       __syncthreads();
       for (int p = 0; p < pairs; ++p) {
-        fx.set(a, h0 + p, n_rows, n_adds);
+        fx.set(a, h0 + p, b_rows, b_adds);
         int* from = limbs + p * 2 * T3;
         float* part = a.part + ((size_t)(h0 + p) * a.parts + blockIdx.x) * T3;
         for (int i = threadIdx.x; i < T3; i += blockDim.x) {

@@ -334,3 +334,15 @@ def test_results_in_the_place_of_what_they_replace(op, dtype):
         assert torch.equal(x, want[y]), y
     with pytest.raises(ssa.SSAError, match="INVALID_ARG"):
         ssa.ssa_window_backward(pr.p, pr.plan, q, pr.k, pr.v, pr.dout, grads=(q, k, v))
+
+
+@pytest.mark.parametrize("n,side,m,hq,hkv", [(500, 8, 6, 5, 1), (32, 4, 5, 16, 2), (111, 6, 12, 3, 3)])
+def test_bias_gradient_of_few_rows_in_a_fine_unit(n, side, m, hq, hkv):
+    """Sharp softmaxes: offsets whose dS are all small keep their bounds and the roundings of the fixed point.
+    A CTA of few rows has a unit of 2^-41 of the largest |dP|, below 2^6 here: 2^-35.  At most n adds per
+    offset, independent and uniform within half a unit: six times the root of n / 12 units."""
+    coords, cu = dense(109, n, side)
+    pr = Problem(coords, cu, m, hq, hkv, 64, torch.bfloat16, seed=110, bias="offset", std=4.0)
+    got, (value, bound) = run_window(pr)["dbias"], pr.ref_window()["dbias"]
+    err = np.abs(got.double().cpu().numpy() - value)
+    assert np.all(err <= bound + 6 * (n / 12) ** 0.5 * 2.0 ** -35)
