@@ -25,7 +25,7 @@ constexpr int kTile = SSA_WINDOW_TILE;  // rows of a work tile
 constexpr int kDupFlag = 65536;         // tiles[].y: two tokens of the cell share a voxel
 constexpr int kDupUnit = 131072;        // and from here on: the most tokens of one voxel, kDupTop at most
 constexpr int kDupTop = 16383;
-constexpr int kDupMost = 2048;  // more in one voxel: the cell's bias gradient goes to the 64-bit sums (bf16)
+constexpr int kDupMost = 2048;  // up to here no cell's bias gradient goes to the 64-bit sums (bf16, kLone)
 
 // Dynamic shared memory of a CTA at most, beside what kernels declare; and the bound that a kernel is
 // given before its first launch above 48 KB.  The same for every call: the size of a launch depends on its

@@ -286,11 +286,13 @@ __device__ __forceinline__ void red_shared(uint32_t at, int x) {
 // of their cell holds.  Both stay below 2^13: before they pass it the CTA's sums go to its partial
 // gradient and start again, so the unit is at most M 2^-33 however many rows a CTA has; a batch alone
 // between two flushes counts its own (M 2^-41 for few rows).  An item of one crowded cell can pass the
-// bound alone: up to kDupMost tokens in a voxel its unit is M 2^-32, where dS is some M 2^-11; cells that
-// are more crowded (kCrowd) take the 64-bit sums below.  A NaN or an infinity in dP or in a softmax makes
+// bound alone: below 2^19 adds (some thousand tokens in a voxel) its unit is M 2^-32, where dS is some
+// M 2^-12; cells that are more crowded (kCrowd) take the 64-bit sums below (8/2 heads of 64: a voxel of
+// 20000 tokens 43 -> 50 ms; from 2048 tokens on, four such voxels of 2500 in a cell took 36 ms, now 5).  A NaN or an infinity in dP or in a softmax makes
 // the head's gradient NaN, and so does an M from 2^127 on (dP - D could overflow); below, 2^s and 2^-s are
 // normal numbers.
 constexpr int kAdds = 8191;      // at most between two flushes, but for a lone item
+constexpr int kLone = 1 << 19;   // and for a lone item
 constexpr int kCrowd = 1 << 16;  // items[].y: a cell for the 64-bit sums
 struct Limbs {
   float s[2], k;         // 2^s for the rows g, g + 8 (times far_factor, see store_lse2), 2^k
@@ -526,7 +528,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
         x.y = item_tiles(x, item_size);
         int take = 32;  // slots of these 32
         if (grad && TAB != 3) {
-          const bool crowd = dup > kDupMost;
+          const bool crowd = dup > kDupMost && item_size * kTile * dup >= kLone;
           const int r = x.y > 0 && !crowd ? min(item_size * kTile, x.w - x.x) : 0;
           const int all = __reduce_add_sync(kFull, r * dup);
           if (adds + all <= kAdds) {
