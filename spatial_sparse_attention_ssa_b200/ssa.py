@@ -795,17 +795,22 @@ def _window_backward(op: int, name: str, p: WindowParams, plan: WindowPlan, extr
 
 
 def ssa_window_backward(p: WindowParams, plan: WindowPlan, q, k, v, dout: torch.Tensor,
-                        bias: WindowBias | None = None, grads=None, dbias: torch.Tensor | None = None,
+                        bias: WindowBias | None = None, grads=None, dbias: torch.Tensor | bool | None = None,
                         workspace: torch.Tensor | None = None):
     """Gradients of ssa_window_forward: (dq, dk, dv, dbias), dq, dk, dv in the dtype of the
-    inputs, dbias fp32 [hq, nb] (None without a bias).  q, k, v are the forward's, or three
-    Act8 of them."""
+    inputs, dbias fp32 [hq, nb] (None without a bias, or with dbias = False: a bias that is not
+    trained, whose gradient is not computed).  q, k, v are the forward's, or three Act8 of
+    them."""
     bc, nb = _bias_c(bias, p, plan)
+    if dbias is False:
+        dbias, wanted = None, False
+    else:
+        wanted = bias is not None
     if bias is None and dbias is not None:
         raise ValueError("dbias without a bias")
-    if bias is not None and dbias is None:
+    if wanted and dbias is None:
         dbias = torch.empty(p.hq, nb, dtype=torch.float32, device=dout.device)
-    elif bias is not None:
+    elif dbias is not None:
         _want(dbias, (p.hq, nb), torch.float32, "dbias")
     return _window_backward(OP_WINDOW_BACKWARD, "ssa_window_backward", p, plan, (bc,),
                             (bias.table, bias.bucket) if bias else (), q, k, v, dout, dbias, grads, workspace)

@@ -346,3 +346,20 @@ def test_bias_gradient_of_few_rows_in_a_fine_unit(n, side, m, hq, hkv):
     got, (value, bound) = run_window(pr)["dbias"], pr.ref_window()["dbias"]
     err = np.abs(got.double().cpu().numpy() - value)
     assert np.all(err <= bound + 6 * (n / 12) ** 0.5 * 2.0 ** -35)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m,crowd,far", [(5, 0, 0.0), (14, 0, 0.0), (4, 3000, 0.0), (5, 0, -1e9), (14, 0, -1e9)])
+def test_a_bias_that_is_not_trained(m, crowd, far, dtype):
+    """Without the bias gradient the others are the same bits."""
+    coords, cu = shell(111, 300, r=9)
+    if crowd:
+        coords = np.concatenate([coords, np.repeat(coords[100:101], crowd, 0)])
+        cu = np.array([0, len(coords)], np.int32)
+    pr = Problem(coords, cu, m, 4, 2, 32, DT[dtype], seed=112, bias="offset")
+    pr.bias.table += far
+    want = run_window(pr)
+    *got, none = ssa.ssa_window_backward(pr.p, pr.plan, pr.q, pr.k, pr.v, pr.dout, bias=pr.bias, dbias=False)
+    assert none is None and ssa.device_status() == 0
+    for x, y in zip(got, ("dq", "dk", "dv")):
+        assert torch.equal(x, want[y]), y
