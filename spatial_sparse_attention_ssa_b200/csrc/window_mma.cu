@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
     __syncthreads();
     if (warp == NW) {
       int n = 0, i0 = 0, rows = 0, adds = 0;
-      const bool fresh = batch == blockIdx.x || n_flush;
+      const bool fresh = batch == blockIdx.x || n_flush || n_adds == 0;
       if (grad && TAB != 3 && !fresh) rows = n_rows, adds = n_adds;
       bool more = true;
 #pragma unroll 2
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(32 * (Shape<D, MAPS, MODE>::warps + 2), 1)
       if (lane == 0) {
         n_items = n, n_slots = i0, n_rows = rows, n_adds = adds;
         n_flush = !more || adds > kAdds || batch + (int64_t)i0 * gridDim.x >= a.T;
-        const bool alone = fresh && n_flush;  // no other batch since the last flush and before the next
+        const bool alone = fresh && n_flush;  // no adds of another batch since the last flush and to the next
         b_rows = alone ? rows : kAdds, b_adds = alone ? adds : kAdds;
       }
     }

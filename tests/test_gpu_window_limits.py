@@ -363,3 +363,33 @@ def test_a_bias_that_is_not_trained(m, crowd, far, dtype):
     assert none is None and ssa.device_status() == 0
     for x, y in zip(got, ("dq", "dk", "dv")):
         assert torch.equal(x, want[y]), y
+
+
+def test_bias_gradient_of_a_lone_crowded_item_after_64_bit_sums_only():
+    """512 heads, so one CTA to two heads: its first batch holds only a cell for the 64-bit sums, the next
+    begins with a cell of two voxels of 2000 equal tokens each.  Equal dS leave equal remainders, whose sums
+    are as large as their bound.  Two kinds of rows and of keys, so the oracle's bounds in closed form."""
+    coords = np.concatenate([np.tile([[0, 0, 0]], (5000, 1)), np.tile([[4, 0, 0]], (2000, 1)),
+                             np.tile([[5, 0, 0]], (2000, 1))]).astype(np.int32)
+    pr = Problem(coords, np.array([0, 9000], np.int32), 4, 2, 2, 32, torch.bfloat16, seed=113)
+    gen = torch.Generator(device="cuda").manual_seed(114)
+    f = lambda *x: torch.randn(*x, generator=gen, device="cuda")  # noqa: E731
+    pr.hq, pr.p = 512, ssa.make_window_params(512, 2, 32, torch.bfloat16)
+    pr.q, pr.dout = (f(9000, 512, 32).bfloat16() for _ in range(2))
+    for x in (pr.q, pr.dout, pr.k, pr.v):
+        x[5000:7000], x[7000:] = x[5000].clone(), x[7000].clone()
+    pr.bias = ssa.WindowBias(0.5 * f(512, 343))
+    got = ssa.ssa_window_backward(pr.p, pr.plan, pr.q, pr.k, pr.v, pr.dout, bias=pr.bias)[3].double().cpu()
+    off, eps, kind = torch.tensor([[171, 122], [220, 171]]), 2.0 ** -24, [5000, 7000]   # one voxel along x: 49
+    for h in range(0, 512, 7):
+        q, k, v, do = (x[kind, y].double().cpu() for x, y in ((pr.q, h), (pr.k, h // 256), (pr.v, h // 256), (pr.dout, h)))
+        t = pr.bias.table[h].double().cpu()[off]
+        p = torch.softmax(q @ k.T / np.sqrt(32) + t, 1)          # of all 2000 keys of a kind
+        dp, mag = do @ v.T, do.abs() @ v.abs().T
+        D = (p * dp).sum(1, keepdim=True)
+        ep = 2 * 36 * eps * (q.abs() @ k.abs().T / np.sqrt(32) + t.abs()).amax(1, keepdim=True) + 2.0 ** -20
+        eD = (p * (dp.abs() * (ep + 4000 * eps) + 36 * eps * mag)).sum(1, keepdim=True)
+        ds = p * (dp - D)
+        err = p * ((dp - D).abs() * (ep + 4 * eps) + 36 * eps * mag + eD) + ds.abs() * 4000 * eps
+        for a, b in ((0, 1), (1, 0)):
+            assert abs(float(got[h, off[a, b]] - 2000 * ds[a, b])) <= 2000 * float(err[a, b]), (h, a)
